@@ -304,6 +304,72 @@ dgq_status dgq_paged_decode_attn_split(const void *q_bf16, const void *k_new_bf1
                                        void *workspace, size_t workspace_bytes, void *cuda_stream);
 
 /* ---------------------------------------------------------------------------------------
+ * dgq_paged_decode_attn_bf16 -- the same decode step over an unquantised bf16 paged cache: the
+ * layout dgq_compress_paged and the prefill calls read, for requests that are not (or not yet)
+ * compressed.
+ *
+ * For request b and query head hq (KV head h = hq / G): out = softmax(s) . [V ; v_new] with
+ * s_t = q . k_t / sqrt(128) over the cached tokens t < L_b and s_L = q . k_new / sqrt(128).
+ * Same kernel, work split, merge order and workspace as dgq_paged_decode_attn; the weights are
+ * rounded to bf16 before they meet V (values and sums stay in fp32).
+ *
+ * k_src_bf16, v_src_bf16  [num_src_blocks, Hkv, block_size, 128] bf16, device: token t of
+ *                         request b, head h is row src[src_block_tables[b][t / bs]][h][t % bs].
+ *                         Slots behind a request's end may hold anything.
+ * src_block_tables_dev    [batch, max_src_blocks_per_seq] int32, device; max_seqlen <=
+ *                         max_src_blocks_per_seq * block_size.  An entry outside
+ *                         [0, num_src_blocks) is flagged in the workspace (block 0 read instead).
+ * Other arguments, limits and the workspace size as dgq_paged_decode_attn.  q, the cached rows,
+ * k_new and v_new must be finite.
+ */
+dgq_status dgq_paged_decode_attn_bf16(const void *q_bf16, const void *k_new_bf16, const void *v_new_bf16,
+                                      const void *k_src_bf16, const void *v_src_bf16, int32_t num_src_blocks,
+                                      const int32_t *src_block_tables_dev, int32_t max_src_blocks_per_seq,
+                                      const int32_t *seq_lens_dev, int32_t max_seqlen, int32_t batch,
+                                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t block_size, void *out_bf16, void *workspace, size_t workspace_bytes,
+                                      void *cuda_stream);
+
+/* ---------------------------------------------------------------------------------------
+ * dgq_prompt_attn -- causal grouped-query attention of whole prompts over bf16 K and V: what a
+ * layer computes at prefill, on the rows dgq_compress then encodes.
+ *
+ * Request b has n = cu_q[b+1] - cu_q[b] query rows and m = cu_kv[b+1] - cu_kv[b] keys, which end at
+ * the same token: query row i sits at position m - n + i and sees the keys t <= m - n + i (n == m: a
+ * whole prompt; n < m: a chunk behind its history).  For query head hq (KV head h = hq / G):
+ *   out[i][hq] = sum_t softmax_t(q[i][hq] . k[t][h] / sqrt(128)) v[t][h];
+ * a row that sees no key (n > m) gets zeros.  Softmax statistics and sums in fp32; the weights are
+ * rounded to bf16 before they meet V.
+ *
+ * q_bf16, out_bf16  [total_q, Hq, 128] bf16, device; rows from cu_q[batch] on are neither read nor
+ *                   written.
+ * k_bf16, v_bf16    [total_kv, Hkv, 128] bf16, device, packed rows as dgq_compress reads them.
+ * cu_q_dev, cu_kv_dev  [batch+1] int32, device, non-decreasing, at most total_q / total_kv (a
+ *                   request that is not is flagged in the workspace and cut to the buffers).
+ * Supported: Hq % Hkv == 0 with G = Hq / Hkv in {1, 2, 4, 8}.  A request's own rows must be finite;
+ * rows of other requests, and behind the last one, cannot reach its output.
+ * workspace         >= dgq_prompt_attn_workspace_size(batch, Hq, Hkv) bytes, zero-filled before first use.
+ */
+dgq_status dgq_prompt_attn(const void *q_bf16, const void *k_bf16, const void *v_bf16, int32_t total_q,
+                           int32_t total_kv, const int32_t *cu_q_dev, const int32_t *cu_kv_dev, int32_t batch,
+                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, void *out_bf16,
+                           void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+size_t dgq_prompt_attn_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads);
+
+/* dgq_prompt_attn over a bf16 paged cache (the layout dgq_compress_paged and the prefill calls read),
+ * for prompts attended chunk by chunk behind what the cache already holds: the m = seq_lens[b] keys
+ * of request b, its chunk's own among them, are rows src[src_block_tables[b][t / bs]][h][t % bs].
+ * seq_lens_dev [batch] int32, device: at most max_src_blocks_per_seq * block_size (flagged and cut
+ * otherwise).  A block-table entry outside [0, num_src_blocks) is flagged in the workspace (block 0
+ * read instead).  Slots behind a request's end may hold anything. */
+dgq_status dgq_prompt_attn_paged(const void *q_bf16, int32_t total_q, const int32_t *cu_q_dev, const void *k_src_bf16,
+                                 const void *v_src_bf16, int32_t num_src_blocks, const int32_t *src_block_tables_dev,
+                                 int32_t max_src_blocks_per_seq, const int32_t *seq_lens_dev, int32_t batch,
+                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                 void *out_bf16, void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/* ---------------------------------------------------------------------------------------
  * dgq_paged_decode_attn_noalloc -- the same decode attention for callers that cannot
  * allocate device memory.  The source articles have no counterpart: this is a deployment
  * convenience of this library.
@@ -505,22 +571,80 @@ dgq_status dgq_workspace_init(void *workspace, size_t workspace_bytes, void *cud
 dgq_status dgq_workspace_error(const void *workspace, void *cuda_stream, int32_t *device_error);
 
 /* ---------------------------------------------------------------------------------------
+ * dgq_copy_pages -- pages copied between slots of a paged cache: the device half of forking a
+ * request (its last, partly filled block), of copy on write and of a compaction, whose plans
+ * dgq_pool_fork_row, dgq_pool_own_row and dgq_pool_compact make.
+ *
+ * arrays           HOST array of num_arrays device pointers: every array is [num_pages] pages of
+ *                  page_bytes bytes (K and V pools of any number of layers, INT8 or bf16; the
+ *                  parameter arrays of fixed groups; or segment tables, a page being one
+ *                  request's Hkv records of 128 bytes).  Read before the call returns.
+ * page_bytes       a positive multiple of 16.
+ * pairs_dev        [num_pairs, 2] int32, device: (source, destination) page ids.  Destinations are
+ *                  distinct and none of them is a source (of any pair): pairs run in no order.
+ *                  A source may repeat.  A pair with an id outside [0, num_pages) is flagged in the
+ *                  workspace and skipped.
+ * workspace        >= dgq_copy_pages_workspace_size() bytes, zero-filled before first use.
+ * No arrays or no pairs: nothing is launched.  One launch per 256 arrays.
+ */
+dgq_status dgq_copy_pages(void *const *arrays, int32_t num_arrays, int64_t page_bytes, int32_t num_pages,
+                          const int32_t *pairs_dev, int32_t num_pairs, void *workspace, size_t workspace_bytes,
+                          void *cuda_stream);
+
+size_t dgq_copy_pages_workspace_size(void);
+
+/* Block tables renamed after a compaction: out[i] = remap[tables[i]] for num_entries int32 entries
+ * (remap [num_pages] int32 as dgq_pool_compact wrote it, on the device).  out may be tables itself.
+ * An entry outside [0, num_pages) is kept and flagged in the workspace (as for dgq_copy_pages). */
+dgq_status dgq_remap_tables(const int32_t *tables_dev, int64_t num_entries, const int32_t *remap_dev,
+                            int32_t num_pages, int32_t *out_dev, void *workspace, size_t workspace_bytes,
+                            void *cuda_stream);
+
+/* ---------------------------------------------------------------------------------------
  * Host block bookkeeping ([PAGED] BlockTable: physical blocks handed out from a free list
- * and returned when a request ends).  Plain host memory; not thread-safe.
+ * and returned when a request ends).  A block holds one reference per owner; it is free when it
+ * has none.  Plain host memory; not thread-safe.
  */
 typedef struct dgq_pool dgq_pool;
 
 dgq_pool *dgq_pool_create(int32_t num_blocks);          /* NULL on bad size / no memory */
 void dgq_pool_destroy(dgq_pool *pool);
-/* Takes n blocks (all or nothing); ids in ascending order of availability. */
+/* Takes n blocks (all or nothing), one reference each; ids in ascending order of availability. */
 dgq_status dgq_pool_alloc(dgq_pool *pool, int32_t n, int32_t *out_ids);
-/* Returns blocks; an id out of range or already free is DGQ_ERR_INVALID_ARG (nothing freed). */
+/* Drops one reference of each block, which is free again with its last; an id out of range, already
+ * free or named twice is DGQ_ERR_INVALID_ARG (nothing freed). */
 dgq_status dgq_pool_free(dgq_pool *pool, const int32_t *ids, int32_t n);
+/* Adds one reference to each block; ids checked as by dgq_pool_free. */
+dgq_status dgq_pool_share(dgq_pool *pool, const int32_t *ids, int32_t n);
 int32_t dgq_pool_num_free(const dgq_pool *pool);
+/* References of a block: 0 when free, -1 for an id out of range. */
+int32_t dgq_pool_references(const dgq_pool *pool, int32_t id);
 /* Fills row `row` of a host block table [*, max_blocks_per_seq] with blocks for `len`
  * tokens taken from the pool (ceil(len / block_size) of them); unused entries set to 0. */
 dgq_status dgq_pool_alloc_table_row(dgq_pool *pool, int32_t len, int32_t block_size,
                                     int32_t *table, int32_t row, int32_t max_blocks_per_seq);
+/* Row dst_row becomes a fork of the first `len` tokens of row src_row (two different rows): whole
+ * blocks are shared (one more reference), a partly filled last block is replaced by a new one, and
+ * (old, new) goes to out_pair[2] with *num_pairs = 1 (0 when len ends on a block): the caller
+ * copies that page with dgq_copy_pages, and the request's records.  dst_row's former entries are
+ * overwritten, not freed; its unused entries are set to 0.  On error nothing changes. */
+dgq_status dgq_pool_fork_row(dgq_pool *pool, int32_t len, int32_t block_size, int32_t *table, int32_t src_row,
+                             int32_t dst_row, int32_t max_blocks_per_seq, int32_t *out_pair, int32_t *num_pairs);
+/* Copy on write: each of the row's blocks [first_block, first_block + num_row_blocks) that has other
+ * owners is replaced by a new block of the row's own, and (old, new) appended to out_pairs (room for
+ * num_row_blocks pairs); the caller copies those pages.  Needed before anything writes into blocks a
+ * fork shares: dgq_prefill_finish_ex re-encodes a whole request in place.  All or nothing. */
+dgq_status dgq_pool_own_row(dgq_pool *pool, int32_t *table, int32_t row, int32_t max_blocks_per_seq,
+                            int32_t first_block, int32_t num_row_blocks, int32_t *out_pairs, int32_t *num_pairs);
+/* Drops the row's references to its first num_row_blocks blocks and sets the whole row to 0. */
+dgq_status dgq_pool_free_row(dgq_pool *pool, int32_t *table, int32_t row, int32_t max_blocks_per_seq,
+                             int32_t num_row_blocks);
+/* Draws the n live blocks together into ids 0 .. n-1 (so that the tail of the pools can be given
+ * back): each live id >= n moves to a free id < n.  The moves go to out_pairs (room for
+ * num_blocks / 2 pairs; sources and destinations are disjoint: dgq_copy_pages), and
+ * remap[num_blocks] gives every id's new name (its own where it does not move: dgq_remap_tables).
+ * The pool itself is renamed by the call; blocks allocated next are n, n+1, ... */
+dgq_status dgq_pool_compact(dgq_pool *pool, int32_t *remap, int32_t *out_pairs, int32_t *num_pairs);
 
 const char *dgq_status_str(dgq_status status);
 

@@ -30,6 +30,8 @@ __all__ = [
     "dgq_paged_decode_attn", "dgq_encode_format", "dgq_encode_format_workspace_size",
     "dgq_paged_decode_attn_format", "FORMATS", "dgq_prefill_workspace_size", "dgq_prefill_chunk_stats",
     "dgq_prefill_finish", "dgq_paged_decode_attn_split", "dgq_append_split", "dgq_append_ex",
+    "dgq_prompt_attn", "dgq_prompt_attn_paged", "dgq_prompt_attn_workspace_size", "dgq_paged_decode_attn_bf16",
+    "dgq_copy_pages", "dgq_copy_pages_workspace_size", "dgq_remap_tables",
     "dgq_prefill_finish_ex", "RESEG_WINDOW", "RESEG_NGROUPS",
     "dgq_attn_workspace_size", "dgq_workspace_init", "dgq_workspace_error", "BlockPool",
     "seg_record_dtype",
@@ -80,6 +82,9 @@ def lib() -> ctypes.CDLL:
         L.dgq_paged_decode_attn_format.argtypes = [i32, P, P, P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32,
                                                    i32, i32, P, P, sz, P]
         L.dgq_paged_decode_attn_format.restype = ctypes.c_int
+        L.dgq_paged_decode_attn_bf16.argtypes = [P, P, P, P, P, i32, P, i32, P, i32, i32, i32, i32, i32, i32, P, P,
+                                                 sz, P]
+        L.dgq_paged_decode_attn_bf16.restype = ctypes.c_int
         L.dgq_prefill_workspace_size.argtypes = [i32, i32]
         L.dgq_prefill_workspace_size.restype = sz
         L.dgq_prefill_chunk_stats.argtypes = [P, P, i32, P, i32, P, P, i32, i32, i32, i32, i32, P, i32, i32, P, sz,
@@ -108,6 +113,18 @@ def lib() -> ctypes.CDLL:
         L.dgq_workspace_init.restype = ctypes.c_int
         L.dgq_workspace_error.argtypes = [P, P, ctypes.POINTER(i32)]
         L.dgq_workspace_error.restype = ctypes.c_int
+        L.dgq_prompt_attn.argtypes = [P, P, P, i32, i32, P, P, i32, i32, i32, i32, P, P, sz, P]
+        L.dgq_prompt_attn.restype = ctypes.c_int
+        L.dgq_prompt_attn_paged.argtypes = [P, i32, P, P, P, i32, P, i32, P, i32, i32, i32, i32, i32, P, P, sz, P]
+        L.dgq_prompt_attn_paged.restype = ctypes.c_int
+        L.dgq_prompt_attn_workspace_size.argtypes = [i32, i32, i32]
+        L.dgq_prompt_attn_workspace_size.restype = sz
+        L.dgq_copy_pages.argtypes = [P, i32, ctypes.c_int64, i32, P, i32, P, sz, P]
+        L.dgq_copy_pages.restype = ctypes.c_int
+        L.dgq_copy_pages_workspace_size.argtypes = []
+        L.dgq_copy_pages_workspace_size.restype = sz
+        L.dgq_remap_tables.argtypes = [P, ctypes.c_int64, P, i32, P, P, sz, P]
+        L.dgq_remap_tables.restype = ctypes.c_int
         L.dgq_pool_create.argtypes = [i32]
         L.dgq_pool_create.restype = P
         L.dgq_pool_destroy.argtypes = [P]
@@ -120,6 +137,18 @@ def lib() -> ctypes.CDLL:
         L.dgq_pool_num_free.restype = i32
         L.dgq_pool_alloc_table_row.argtypes = [P, i32, i32, P, i32, i32]
         L.dgq_pool_alloc_table_row.restype = ctypes.c_int
+        L.dgq_pool_share.argtypes = [P, P, i32]
+        L.dgq_pool_share.restype = ctypes.c_int
+        L.dgq_pool_references.argtypes = [P, i32]
+        L.dgq_pool_references.restype = i32
+        L.dgq_pool_fork_row.argtypes = [P, i32, i32, P, i32, i32, i32, P, P]
+        L.dgq_pool_fork_row.restype = ctypes.c_int
+        L.dgq_pool_own_row.argtypes = [P, P, i32, i32, i32, i32, P, P]
+        L.dgq_pool_own_row.restype = ctypes.c_int
+        L.dgq_pool_free_row.argtypes = [P, P, i32, i32, i32]
+        L.dgq_pool_free_row.restype = ctypes.c_int
+        L.dgq_pool_compact.argtypes = [P, P, P, P]
+        L.dgq_pool_compact.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -149,6 +178,18 @@ def _stream(stream) -> int:
 def _check(status: int, what: str) -> None:
     if status != 0:
         raise DGQError(status, what)
+
+
+def _operands(what: str, *specs) -> None:
+    """Refuses operands the raw pointers would misread: each spec is (tensor, dtype name, shape) with
+    None for a free extent; tensors must be contiguous and on the current CUDA device."""
+    import torch
+    current = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for x, dtype, shape in specs:
+        if x.dtype != getattr(torch, dtype) or x.dim() != len(shape) or not x.is_contiguous() or \
+                any(want is not None and have != want for have, want in zip(x.shape, shape)) or \
+                (x.is_cuda and x.device.index != current):
+            raise DGQError(-1, what)
 
 
 def seg_record_dtype():
@@ -342,6 +383,24 @@ def dgq_paged_decode_attn_split(q, k_new, v_new, k_pool, v_pool, k_seg_table, v_
                                              _nbytes(workspace), _stream(stream)), "dgq_paged_decode_attn_split")
 
 
+def dgq_paged_decode_attn_bf16(q, k_new, v_new, k_src, v_src, src_block_tables, seq_lens, max_seqlen, out, workspace,
+                               stream=None) -> None:
+    """dgq_paged_decode_attn over an unquantised cache: k_src, v_src bf16 paged cache
+    [num_src_blocks, Hkv, bs, 128] with src_block_tables int32 [B, max_src_blocks]; the other
+    arguments and the workspace (dgq_attn_workspace_size) as there."""
+    B, Hq, D = q.shape
+    blocks, Hkv, bs, _ = k_src.shape
+    _operands("dgq_paged_decode_attn_bf16", (q, "bfloat16", (B, Hq, D)), (k_new, "bfloat16", (B, Hkv, D)),
+              (v_new, "bfloat16", (B, Hkv, D)), (k_src, "bfloat16", (blocks, Hkv, bs, D)),
+              (v_src, "bfloat16", (blocks, Hkv, bs, D)), (src_block_tables, "int32", (B, None)),
+              (seq_lens, "int32", (B,)), (out, "bfloat16", (B, Hq, D)))
+    _check(lib().dgq_paged_decode_attn_bf16(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_src), _ptr(v_src), blocks,
+                                            _ptr(src_block_tables), src_block_tables.shape[1],
+                                            _ptr(seq_lens), int(max_seqlen), B, Hq, Hkv, D, bs, _ptr(out),
+                                            _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "dgq_paged_decode_attn_bf16")
+
+
 def _format_id(fmt) -> int:
     return FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
 
@@ -390,10 +449,83 @@ def dgq_paged_decode_attn_noalloc(q, k_new, v_new, k_pool, v_pool, seg_table, bl
            "dgq_paged_decode_attn_noalloc")
 
 
+def dgq_prompt_attn_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int) -> int:
+    return int(lib().dgq_prompt_attn_workspace_size(batch, num_q_heads, num_kv_heads))
+
+
+def dgq_prompt_attn(q, k, v, cu_q, cu_kv, out, workspace, stream=None) -> None:
+    """Causal attention of packed prompts: q, out bf16 [Tq, Hq, 128]; k, v bf16 [Tkv, Hkv, 128]; cu_q,
+    cu_kv int32 [B+1] (queries and keys of a request end at the same token); workspace uint8
+    (dgq_prompt_attn_workspace_size bytes).  All CUDA tensors."""
+    Tq, Hq, D = q.shape
+    T, Hkv, _ = k.shape
+    B = cu_q.shape[0] - 1
+    _operands("dgq_prompt_attn", (q, "bfloat16", (Tq, Hq, D)), (k, "bfloat16", (T, Hkv, D)),
+              (v, "bfloat16", (T, Hkv, D)), (cu_q, "int32", (B + 1,)), (cu_kv, "int32", (B + 1,)),
+              (out, "bfloat16", (Tq, Hq, D)))
+    _check(lib().dgq_prompt_attn(_ptr(q), _ptr(k), _ptr(v), Tq, T, _ptr(cu_q), _ptr(cu_kv),
+                                 B, Hq, Hkv, D, _ptr(out), _ptr(workspace),
+                                 _nbytes(workspace), _stream(stream)), "dgq_prompt_attn")
+
+
+def dgq_prompt_attn_paged(q, cu_q, k_src, v_src, src_block_tables, seq_lens, out, workspace, stream=None) -> None:
+    """dgq_prompt_attn over a bf16 paged cache: k_src, v_src bf16 [num_src_blocks, Hkv, bs, 128],
+    src_block_tables int32 [B, max_src_blocks], seq_lens int32 [B] (keys of each request, the chunk's
+    own among them); the rest as dgq_prompt_attn."""
+    Tq, Hq, D = q.shape
+    blocks, Hkv, bs, _ = k_src.shape
+    B = seq_lens.shape[0]
+    _operands("dgq_prompt_attn_paged", (q, "bfloat16", (Tq, Hq, D)), (k_src, "bfloat16", (blocks, Hkv, bs, D)),
+              (v_src, "bfloat16", (blocks, Hkv, bs, D)), (cu_q, "int32", (B + 1,)), (seq_lens, "int32", (B,)),
+              (src_block_tables, "int32", (B, None)), (out, "bfloat16", (Tq, Hq, D)))
+    _check(lib().dgq_prompt_attn_paged(_ptr(q), Tq, _ptr(cu_q), _ptr(k_src), _ptr(v_src), blocks,
+                                       _ptr(src_block_tables), src_block_tables.shape[1], _ptr(seq_lens), B, Hq, Hkv, D, bs, _ptr(out), _ptr(workspace),
+                                       _nbytes(workspace), _stream(stream)), "dgq_prompt_attn_paged")
+
+
+def dgq_copy_pages_workspace_size() -> int:
+    return int(lib().dgq_copy_pages_workspace_size())
+
+
+def dgq_copy_pages(arrays, pairs, workspace, stream=None) -> None:
+    """Pages copied inside every array of `arrays` (contiguous CUDA tensors with the pages along the
+    first dimension: pools of any layers, or segment tables [B, Hkv, 128]; all with the same number
+    and size of pages).  pairs: int32 CUDA tensor [n, 2] of (source, destination) ids, destinations
+    distinct and none of them a source; workspace uint8 (dgq_copy_pages_workspace_size bytes)."""
+    arrays = list(arrays)
+    n = arrays[0].shape[0] if arrays else 1
+    size = _nbytes(arrays[0]) // max(n, 1) if arrays else 16
+    for a in arrays:
+        if a.shape[0] != n or _nbytes(a) != n * size or not a.is_contiguous():
+            raise DGQError(-1, "dgq_copy_pages")
+    _operands("dgq_copy_pages", (pairs, "int32", (None, 2)))
+    ptrs = (ctypes.c_void_p * max(len(arrays), 1))(*[_ptr(a) for a in arrays])
+    _check(lib().dgq_copy_pages(ptrs, len(arrays), size, n, _ptr(pairs), pairs.shape[0], _ptr(workspace),
+                                _nbytes(workspace), _stream(stream)), "dgq_copy_pages")
+
+
+def dgq_remap_tables(tables, remap, out, workspace, stream=None) -> None:
+    """out[...] = remap[tables[...]]: contiguous int32 CUDA tensors (out may be tables); remap int32
+    [num_pages] as BlockPool.compact returns it; workspace as for dgq_copy_pages."""
+    _operands("dgq_remap_tables", (tables, "int32", tuple(tables.shape)), (out, "int32", tuple(tables.shape)),
+              (remap, "int32", (None,)))
+    _check(lib().dgq_remap_tables(_ptr(tables), tables.numel(), _ptr(remap), remap.numel(), _ptr(out),
+                                  _ptr(workspace), _nbytes(workspace), _stream(stream)), "dgq_remap_tables")
+
+
+def _host_table(table, *rows):
+    """Address of a C-contiguous int32 numpy block table that has these rows."""
+    if table.dtype != "int32" or table.ndim != 2 or not table.flags.c_contiguous or \
+            not all(0 <= r < table.shape[0] for r in rows):
+        raise DGQError(-1, "block table")
+    return table.ctypes.data
+
+
 class BlockPool:
-    """Host free list of physical block ids (dgq_pool_*)."""
+    """Host free list of physical block ids with references (dgq_pool_*)."""
 
     def __init__(self, num_blocks: int):
+        self.num_blocks = num_blocks
         self._h = lib().dgq_pool_create(num_blocks)
         if not self._h:
             raise DGQError(-1, "dgq_pool_create")
@@ -426,3 +558,46 @@ class BlockPool:
         """table: C-contiguous int32 numpy array [rows, max_blocks]."""
         _check(lib().dgq_pool_alloc_table_row(self._h, length, block_size, table.ctypes.data, row,
                                               table.shape[1]), "dgq_pool_alloc_table_row")
+
+    def share(self, ids) -> None:
+        """One more reference to each block."""
+        ids = list(ids)
+        buf = (ctypes.c_int32 * max(len(ids), 1))(*ids)
+        _check(lib().dgq_pool_share(self._h, buf, len(ids)), "dgq_pool_share")
+
+    def references(self, block: int) -> int:
+        return int(lib().dgq_pool_references(self._h, block))
+
+    def fork_row(self, length: int, block_size: int, table, src_row: int, dst_row: int):
+        """Row dst_row of the host table becomes a fork of src_row's first `length` tokens; returns the
+        pages to copy, int32 numpy [0 or 1, 2] (source, destination)."""
+        import numpy as np
+        pairs, n = np.zeros((1, 2), dtype=np.int32), ctypes.c_int32(0)
+        _check(lib().dgq_pool_fork_row(self._h, length, block_size, _host_table(table, src_row, dst_row), src_row,
+                                       dst_row, table.shape[1], pairs.ctypes.data, ctypes.byref(n)),
+               "dgq_pool_fork_row")
+        return pairs[:n.value]
+
+    def own_row(self, table, row: int, first_block: int, num_row_blocks: int):
+        """The row's shared blocks among [first_block, first_block + num_row_blocks) replaced by its own;
+        returns the pages to copy, int32 numpy [n, 2]."""
+        import numpy as np
+        pairs, n = np.zeros((max(num_row_blocks, 1), 2), dtype=np.int32), ctypes.c_int32(0)
+        _check(lib().dgq_pool_own_row(self._h, _host_table(table, row), row, table.shape[1], first_block,
+                                      num_row_blocks, pairs.ctypes.data, ctypes.byref(n)), "dgq_pool_own_row")
+        return pairs[:n.value]
+
+    def free_row(self, table, row: int, num_row_blocks: int) -> None:
+        """Drops the row's references to its first num_row_blocks blocks and zeroes the row."""
+        _check(lib().dgq_pool_free_row(self._h, _host_table(table, row), row, table.shape[1], num_row_blocks),
+               "dgq_pool_free_row")
+
+    def compact(self):
+        """Draws the live blocks together into the lowest ids.  Returns (remap [num_blocks], pairs [n, 2]),
+        int32 numpy: new name of every block, and the pages to copy."""
+        import numpy as np
+        remap = np.zeros(self.num_blocks, dtype=np.int32)
+        pairs, n = np.zeros((max(self.num_blocks // 2, 1), 2), dtype=np.int32), ctypes.c_int32(0)
+        _check(lib().dgq_pool_compact(self._h, remap.ctypes.data, pairs.ctypes.data, ctypes.byref(n)),
+               "dgq_pool_compact")
+        return remap, pairs[:n.value]

@@ -1,4 +1,4 @@
-"""Builds libdgq.so in-tree with nvcc for sm_103a (one -gencode; the eight translation units
+"""Builds libdgq.so in-tree with nvcc for sm_103a (one -gencode; the translation units
 of csrc/ compiled in parallel).  Used by ``__graft_entry__.build()`` and by the binding when the
 library is missing or older than its sources."""
 from __future__ import annotations
@@ -27,6 +27,8 @@ UNITS = {
     "dgq_attn.cu": [],
     "dgq_host.cu": [],
     "dgq_noalloc.cu": [],
+    "dgq_pages.cu": [],
+    "dgq_prompt.cu": [],
 }
 
 

@@ -42,6 +42,9 @@
 //    dequantised to fp16 in registers, code * scale + min per (token, half row), from per-token
 //    parameters copied into the ring beside each tile.  Both of the latter feed the tensor
 //    cores the decoded values themselves, so their per-tile fold is the identity.
+//  * An unquantised bf16 paged cache is one more instance: tiles of 16 rows of 256 bytes, keys fed
+//    to the tensor cores as they are, values transposed on the way out of shared memory
+//    (ldmatrix.trans), weights rounded to bf16.
 #include "dgq_device.cuh"
 #include "dgq.h"
 #include "dgq_launch.h"
@@ -58,16 +61,22 @@ constexpr int kWarpsPerCta = 4;
 constexpr int kAttnThreads = kWarpsPerCta * 32;
 constexpr int kMaxCtasPerSm = 3;
 constexpr int kDepth = 3;                          // tiles in flight per warp (3 CTAs of 4 warps fit per SM)
-constexpr int kTileBytes = kTile * kD;            // 16 rows of 128 codes = 2 KB
-constexpr int kTileSmem = 2 * kTileBytes;          // K tile + V tile
 constexpr int kParBytes = kTile * 16;              // fixed groups: a tile's (min0, scale0, min1, scale1) per token
 
 // Code formats of the decode kernel's instances.
-enum : int { kDecAffine = 0, kDecFp8 = 1, kDecFixed = 2, kDecSplitV = 3 };
+enum : int { kDecAffine = 0, kDecFp8 = 1, kDecFixed = 2, kDecSplitV = 3, kDecBf16 = 4, kNumDec = 5 };
+
+// Bytes of a token's row of one head in the pools: 128 codes, or 128 bf16 values.
+template <int Fmt>
+__host__ __device__ constexpr int row_bytes() { return Fmt == kDecBf16 ? 2 * kD : kD; }
 
 // Bytes of one ring stage: the K and V tiles, and for fixed groups their K and V parameters.
 template <int Fmt>
-__host__ __device__ constexpr int stage_bytes() { return kTileSmem + (Fmt == kDecFixed ? 2 * kParBytes : 0); }
+__host__ __device__ constexpr int stage_bytes() { return 2 * kTile * row_bytes<Fmt>() + (Fmt == kDecFixed ? 2 * kParBytes : 0); }
+
+// CTAs per SM an instance is built for: a bf16 ring takes twice the shared memory.
+template <int Fmt>
+__host__ __device__ constexpr int ctas_per_sm() { return Fmt == kDecBf16 ? 2 : kMaxCtasPerSm; }
 constexpr int kPartStride = 132;                   // floats per (piece, head) partial: m, l, pad, pad, O[128]
 constexpr int32_t kMaxGroup = 8;                   // largest query-head group the entry points accept
 constexpr float kLog2eOverSqrtD = 0.12751743074570180f;  // log2(e) / sqrt(128)
@@ -152,6 +161,27 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sc2, uint32_t mn
             return x;
         }
     }
+}
+
+// The same product on bf16 operands (the bf16 cache: values reach the tensor cores as stored).
+__device__ __forceinline__ void mma16816_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four 8 x 8 tiles of 16-bit values read from shared memory transposed: lane l names row l % 8 of
+// tile l / 8 and receives of each tile the elements (row 2 (l % 4), column l / 4) and the one below.
+__device__ __forceinline__ uint4 ldmatrix_x4_trans(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
 }
 
 // 8-byte shared-memory load by 32-bit shared address (volatile: stays after the copy wait)
@@ -321,8 +351,11 @@ __host__ __device__ constexpr int piece_bytes() { return kPbRecV + (Fmt == kDecS
 
 
 template <int Fmt>
-__global__ void __launch_bounds__(kAttnThreads, kMaxCtasPerSm) attn_kernel(AttnArgs a)
+__global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(AttnArgs a)
 {
+    constexpr int kRow = row_bytes<Fmt>();
+    constexpr int kTileBytes = kTile * kRow;   // 16 rows of one head: 2 KB of codes, 4 KB of bf16
+    constexpr int kTileSmem = 2 * kTileBytes;  // K tile + V tile
     constexpr int kStage = stage_bytes<Fmt>();
     constexpr int kWarpSmem = kDepth * kStage;
     constexpr int kPieceBytes = piece_bytes<Fmt>();
@@ -395,8 +428,10 @@ __global__ void __launch_bounds__(kAttnThreads, kMaxCtasPerSm) attn_kernel(AttnA
     }
     auto stage_piece = [&](const Piece &pz, int buf) {  // thread 0 only
         uint8_t *dst = pbuf + buf * kPieceBytes;
-        mbar_arrive_expect_tx(&pbar[buf], (uint32_t)(kPbQ + 256 * G + (Fmt == kDecSplitV ? 128 : 0)));
-        bulk_load(dst + kPbRec, a.table + (int64_t)pz.b * Hkv + pz.h, 128, &pbar[buf]);
+        mbar_arrive_expect_tx(&pbar[buf], (uint32_t)(kPbQ + 256 * G + (Fmt == kDecSplitV ? 128 : 0) -
+                                                     (Fmt == kDecBf16 ? kPbKnew : 0)));
+        if constexpr (Fmt != kDecBf16)  // (a bf16 cache has no records)
+            bulk_load(dst + kPbRec, a.table + (int64_t)pz.b * Hkv + pz.h, 128, &pbar[buf]);
         if constexpr (Fmt == kDecSplitV) bulk_load(dst + kPbRecV, a.vtable + (int64_t)pz.b * Hkv + pz.h, 128, &pbar[buf]);
         bulk_load(dst + kPbKnew, a.knew + ((int64_t)pz.b * Hkv + pz.h) * kD, 256, &pbar[buf]);
         bulk_load(dst + kPbVnew, a.vnew + ((int64_t)pz.b * Hkv + pz.h) * kD, 256, &pbar[buf]);
@@ -447,17 +482,19 @@ __global__ void __launch_bounds__(kAttnThreads, kMaxCtasPerSm) attn_kernel(AttnA
         const int32_t blk = __shfl_sync(0xffffffffu, bq_cur, (kn - kb) & 31);
         if (kn < nmine && ic.L > 0) {
             const int64_t row0 = ((int64_t)blk * Hkv + ic.h) * a.bs + pow2_mod(ic.j, per_blk) * kTile;
-            const uint8_t *kp = a.kpool + row0 * kD;
-            const uint8_t *vp = a.vpool + row0 * kD;
+            const uint8_t *kp = a.kpool + row0 * kRow;
+            const uint8_t *vp = a.vpool + row0 * kRow;
             // whole 128-byte rows: lane l copies 16-byte column l % 8 of rows 4i + l / 8, stored
             // at column (l % 8) ^ (row % 8) so the fragment reads below hit 8 distinct columns
+            // (a bf16 row has 16 columns: lane l copies column l % 16 of rows 2i + l / 16)
             const uint32_t dst = ring + st * kStage;
+            constexpr int kCols = kRow / 16, kRowsPer = 32 / kCols;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 4 * i + (lane >> 3), col = lane & 7;
-                const uint32_t off = row * kD + ((col ^ (row & 7)) << 4);
-                cp_async16(dst + off, kp + row * kD + col * 16);
-                cp_async16(dst + kTileBytes + off, vp + row * kD + col * 16);
+            for (int i = 0; i < kTile / kRowsPer; ++i) {
+                const int row = kRowsPer * i + lane / kCols, col = lane % kCols;
+                const uint32_t off = row * kRow + ((col ^ (row & 7)) << 4);
+                cp_async16(dst + off, kp + row * kRow + col * 16);
+                cp_async16(dst + kTileBytes + off, vp + row * kRow + col * 16);
             }
             if constexpr (Fmt == kDecFixed) {  // lanes 0-15: K parameters of token lane; 16-31: V
                 const float4 *src = (lane < 16 ? a.kpar : a.vpar) + row0 + (lane & 15);
@@ -486,12 +523,22 @@ __global__ void __launch_bounds__(kAttnThreads, kMaxCtasPerSm) attn_kernel(AttnA
         if (!mbar_wait_bounded(&pbar[buf], (uint32_t)(n >> 1) & 1u)) record_error(a.hdr, kErrFullWait);
 
         // piece start (per warp): record word, Q fragments of head g = r, state
-        const uint32_t recw = reinterpret_cast<const uint32_t *>(pb + kPbRec)[lane];
+        const uint32_t recw = Fmt != kDecBf16 ? reinterpret_cast<const uint32_t *>(pb + kPbRec)[lane] : 0u;
         const uint32_t recw_v = Fmt == kDecSplitV ? reinterpret_cast<const uint32_t *>(pb + kPbRecV)[lane] : 0u;
         float qsum;
         {
             float qs = 0.0f;
-            if (gvalid) {  // columns d = 16cq + 64(jj/4) + 4(jj%4) + {0,1 | 2,3}
+            if (Fmt == kDecBf16 && gvalid) {  // 16-byte columns cq + 4m: two k-steps each, as K below
+                const uint32_t qrow = smem_u32(pb + kPbQ) + r * 256;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint4 u = ld_shared_v4(qrow + 16 * (cq + 4 * m));
+                    qa0[2 * m] = u.x;
+                    qa2[2 * m] = u.y;
+                    qa0[2 * m + 1] = u.z;
+                    qa2[2 * m + 1] = u.w;
+                }
+            } else if (gvalid) {  // columns d = 16cq + 64(jj/4) + 4(jj%4) + {0,1 | 2,3}
                 const uint32_t qrow = smem_u32(pb + kPbQ) + r * 256;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -541,7 +588,7 @@ __global__ void __launch_bounds__(kAttnThreads, kMaxCtasPerSm) attn_kernel(AttnA
                     sgv = __popc(__ballot_sync(0xffffffffu, lane >= 3 && lane <= 6 && (int32_t)recw_v <= tok0));
                     sg = sgk * 8 + sgv;
                 }
-                if ((Fmt == kDecFp8 || Fmt == kDecFixed) && sg != seg) {  // decoded values: identity fold
+                if ((Fmt == kDecFp8 || Fmt == kDecFixed || Fmt == kDecBf16) && sg != seg) {  // decoded values: identity fold
                     seg = sg;
                     vflat = false;
                     ak = kLog2eOverSqrtD;
@@ -603,13 +650,25 @@ __global__ void __launch_bounds__(kAttnThreads, kMaxCtasPerSm) attn_kernel(AttnA
                     vsc_cd = half2_bits(__uint_as_float(pc.y), __uint_as_float(pd.y));
                 }
                 // S^T = Q K^T: two n-tiles of 8 tokens x 8 k-steps, four accumulator chains;
-                // this lane supplies rows tau(r) and 8 + tau(r), columns cq and cq + 4
-                const uint32_t kr0 = tile + tr * kD, kr1 = tile + (8 + tr) * kD;
-                const uint4 k0 = ld_shared_v4(kr0 + ((cq ^ tr) << 4)), k1 = ld_shared_v4(kr0 + (((cq + 4) ^ tr) << 4));
-                const uint4 k2 = ld_shared_v4(kr1 + ((cq ^ tr) << 4)), k3 = ld_shared_v4(kr1 + (((cq + 4) ^ tr) << 4));
+                // this lane supplies rows tau(r) and 8 + tau(r), columns cq and cq + 4 (of a bf16
+                // row's 16 columns cq, cq + 4, cq + 8 and cq + 12, two k-steps each)
+                const uint32_t kr0 = tile + tr * kRow, kr1 = tile + (8 + tr) * kRow;
                 float sa[2][4], sb[2][4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sa[0][e] = sa[1][e] = sb[0][e] = sb[1][e] = 0.0f;
+                if constexpr (Fmt == kDecBf16) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const uint32_t col = ((cq + 4 * m) ^ tr) << 4;
+                        const uint4 x0 = ld_shared_v4(kr0 + col), x1 = ld_shared_v4(kr1 + col);
+                        mma16816_bf16(sa[0], qa0[2 * m], 0u, qa2[2 * m], 0u, x0.x, x0.y);
+                        mma16816_bf16(sa[1], qa0[2 * m], 0u, qa2[2 * m], 0u, x1.x, x1.y);
+                        mma16816_bf16(sb[0], qa0[2 * m + 1], 0u, qa2[2 * m + 1], 0u, x0.z, x0.w);
+                        mma16816_bf16(sb[1], qa0[2 * m + 1], 0u, qa2[2 * m + 1], 0u, x1.z, x1.w);
+                    }
+                } else {
+                const uint4 k0 = ld_shared_v4(kr0 + ((cq ^ tr) << 4)), k1 = ld_shared_v4(kr0 + (((cq + 4) ^ tr) << 4));
+                const uint4 k2 = ld_shared_v4(kr1 + ((cq ^ tr) << 4)), k3 = ld_shared_v4(kr1 + (((cq + 4) ^ tr) << 4));
 #pragma unroll
                 for (int jj = 0; jj < 8; jj += 2) {
                     const uint4 &lo0 = jj < 4 ? k0 : k1;  // n-tile 0: row tau(r), columns cq | cq + 4
@@ -624,6 +683,7 @@ __global__ void __launch_bounds__(kAttnThreads, kMaxCtasPerSm) attn_kernel(AttnA
                              codes2<Fmt, true>(w01, s0, m0));
                     mma16816(sb[1], qa0[jj + 1], 0u, qa2[jj + 1], 0u, codes2<Fmt, false>(w11, s1, m1),
                              codes2<Fmt, true>(w11, s1, m1));
+                }
                 }
                 // lane scores for head r: tokens cq, cq+4 (n-tile 0) and 8+cq, 12+cq (n-tile 1)
                 float z[4];
@@ -657,15 +717,44 @@ __global__ void __launch_bounds__(kAttnThreads, kMaxCtasPerSm) attn_kernel(AttnA
 #pragma unroll
                 for (int e = 0; e < 4; ++e) pr[e] = gvalid ? ex2(z[e] - m_run) : 0.0f;
                 // the tensor cores see p rounded to fp16; the sums use the same rounded weights so
-                // the 1024 offset of the codes cancels exactly against bsum
-                const uint32_t pb0 = f32x2_to_f16x2(pr[0], pr[1]);
-                const uint32_t pb1 = f32x2_to_f16x2(pr[2], pr[3]);
-                const float psum = (f16lo(pb0) + f16hi(pb0)) + (f16lo(pb1) + f16hi(pb1));
+                // the 1024 offset of the codes cancels exactly against bsum.  (bf16 cache: p rounded
+                // to bf16, since one product's operands share a type and bf16 values do not fit fp16;
+                // summing the rounded weights keeps each row a true weighted mean.)
+                uint32_t pb0, pb1;
+                float psum;
+                if constexpr (Fmt == kDecBf16) {
+                    pb0 = pack_bf16x2(pr[0], pr[1]);
+                    pb1 = pack_bf16x2(pr[2], pr[3]);
+                    psum = (bf16lo_to_f32(pb0) + bf16hi_to_f32(pb0)) + (bf16lo_to_f32(pb1) + bf16hi_to_f32(pb1));
+                } else {
+                    pb0 = f32x2_to_f16x2(pr[0], pr[1]);
+                    pb1 = f32x2_to_f16x2(pr[2], pr[3]);
+                    psum = (f16lo(pb0) + f16hi(pb0)) + (f16lo(pb1) + f16hi(pb1));
+                }
                 l_run += psum;
                 bsum = fmaf(cv, psum, bsum);
 
                 // O^T += V^T P^T: rows (d) 16*tr + 2i (+1), k = tokens cq, cq+4, 8+cq, 12+cq
-                if (!vflat) {
+                if constexpr (Fmt == kDecBf16) {
+                    // lane l names row tau(l % 8) (+ 8 for tiles 2, 3), 16-byte column 2i + (l / 8) % 2;
+                    // with the rows in tau order the lane's k-pair (2cq, 2cq + 1) is tokens cq, cq + 4,
+                    // and the transposed tiles are rows d = 16i + r and 16i + 8 + r of V^T
+                    const int vr = tau(lane & 7), vrow = vr + 8 * (lane >> 4);
+                    const uint32_t vrb = tile + kTileBytes + vrow * kRow;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint4 x = ldmatrix_x4_trans(vrb + (((2 * i + ((lane >> 3) & 1)) ^ vr) << 4));
+                        if (valid < kTile) {  // slots past the end hold anything, NaN too: they become 0
+                            const uint32_t lo = (cq < valid ? 0xFFFFu : 0u) | (cq + 4 < valid ? 0xFFFF0000u : 0u);
+                            const uint32_t hi = (cq + 8 < valid ? 0xFFFFu : 0u) | (cq + 12 < valid ? 0xFFFF0000u : 0u);
+                            x.x &= lo;
+                            x.y &= lo;
+                            x.z &= hi;
+                            x.w &= hi;
+                        }
+                        mma16816_bf16(o[i], x.x, x.y, x.z, x.w, pb0, pb1);
+                    }
+                } else if (!vflat) {
                     // rows cq, cq + 4, cq + 8, cq + 12, column tau(r)
                     const uint32_t vt = tile + kTileBytes;  // rows cq + 4i, column tau(r)
                     uint4 va = ld_shared_v4(vt + cq * kD + ((tr ^ cq) << 4));
@@ -717,6 +806,18 @@ __global__ void __launch_bounds__(kAttnThreads, kMaxCtasPerSm) attn_kernel(AttnA
             const float b0 = __shfl_sync(0xffffffffu, bs_, 8 * cq), b1 = __shfl_sync(0xffffffffu, bs_, 8 * cq + 4);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
+                if constexpr (Fmt == kDecBf16) {  // rows d = 16i + r, 16i + 8 + r; heads g0, g1
+                    const int d = 16 * i + r;
+                    if (g0 < G) {
+                        cw[g0 * kPartStride + 4 + d] = o[i][0];
+                        cw[g0 * kPartStride + 12 + d] = o[i][2];
+                    }
+                    if (g1 < G) {
+                        cw[g1 * kPartStride + 4 + d] = o[i][1];
+                        cw[g1 * kPartStride + 12 + d] = o[i][3];
+                    }
+                    continue;
+                }
                 const int d = 16 * tr + 2 * i;
                 if (g0 < G)
                     *reinterpret_cast<float2 *>(cw + g0 * kPartStride + 4 + d) =
@@ -1001,7 +1102,9 @@ namespace dgq {
 
 size_t attn_smem_bytes(int dec, int32_t B, int32_t G)
 {
-    const int stage = dec == kDecFixed ? stage_bytes<kDecFixed>() : stage_bytes<kDecAffine>();
+    const int stage = dec == kDecBf16    ? stage_bytes<kDecBf16>()
+                      : dec == kDecFixed ? stage_bytes<kDecFixed>()
+                                         : stage_bytes<kDecAffine>();
     const int piece = dec == kDecSplitV ? piece_bytes<kDecSplitV>() : piece_bytes<kDecAffine>();
     return 1024 + (size_t)kWarpsPerCta * kDepth * stage + 2 * (size_t)piece + 16 + (size_t)kWarpsPerCta * G * kPartStride * 4 +
            8 * 4 + (size_t)(2 * B + 1) * 4;
@@ -1062,11 +1165,13 @@ cudaError_t launch_attn(int32_t format, const void *q, const void *knew, const v
     a.num_blocks = num_blocks;
 
     // the kernel instance for the code format (the symmetric INT8 cache is an affine one)
-    const int dec = vtable != nullptr ? kDecSplitV
+    const int dec = format == kFormatBf16Cache ? kDecBf16
+                    : vtable != nullptr ? kDecSplitV
                                       : (format == DGQ_FORMAT_FP8_E4M3 ? kDecFp8
                                                                        : (format == DGQ_FORMAT_FIXED64 ? kDecFixed
                                                                                                        : kDecAffine));
-    void (*kern)(AttnArgs) = dec == kDecFp8 ? attn_kernel<kDecFp8>
+    void (*kern)(AttnArgs) = dec == kDecBf16 ? attn_kernel<kDecBf16>
+                             : dec == kDecFp8 ? attn_kernel<kDecFp8>
                              : dec == kDecFixed ? attn_kernel<kDecFixed>
                              : dec == kDecSplitV ? attn_kernel<kDecSplitV>
                                                  : attn_kernel<kDecAffine>;
@@ -1074,10 +1179,10 @@ cudaError_t launch_attn(int32_t format, const void *q, const void *knew, const v
     // per-device launch shape, computed once per (instance, device, shared-memory size) and host
     // thread; the kernel's shared-memory limit is raised once per device and host thread to what
     // the largest call needs (every thread sets the same value, so none lowers it under another)
-    static thread_local int limit_dev[4] = {-1, -1, -1, -1};
-    static thread_local int cached_dev[4] = {-1, -1, -1, -1};
-    static thread_local size_t cached_smem[4] = {0, 0, 0, 0};
-    static thread_local int cached_occ[4] = {0, 0, 0, 0};
+    static thread_local int limit_dev[kNumDec] = {-1, -1, -1, -1, -1};
+    static thread_local int cached_dev[kNumDec] = {-1, -1, -1, -1, -1};
+    static thread_local size_t cached_smem[kNumDec] = {0, 0, 0, 0, 0};
+    static thread_local int cached_occ[kNumDec] = {0, 0, 0, 0, 0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

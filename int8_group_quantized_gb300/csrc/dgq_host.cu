@@ -7,6 +7,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <new>
 #include <vector>
 
 #include "dgq_launch.h"
@@ -291,9 +292,27 @@ dgq_status dgq_paged_decode_attn_format(int32_t format, const void *q_bf16, cons
                                         int32_t block_size, int32_t max_blocks_per_seq, int32_t num_blocks,
                                         void *out_bf16, void *workspace, size_t workspace_bytes, void *cuda_stream)
 {
+    if (format != DGQ_FORMAT_DGQ && format != DGQ_FORMAT_FIXED64 && format != DGQ_FORMAT_SYM_INT8 &&
+        format != DGQ_FORMAT_FP8_E4M3)
+        return DGQ_ERR_INVALID_ARG;
     return attn_impl(format, q_bf16, k_new_bf16, v_new_bf16, k_pool, v_pool, seg_table, nullptr, k_group_params,
                      v_group_params, block_tables_dev, seq_lens_dev, max_seqlen, batch, num_q_heads, num_kv_heads,
                      head_dim, block_size, max_blocks_per_seq, num_blocks, out_bf16, workspace, workspace_bytes,
+                     cuda_stream);
+}
+
+dgq_status dgq_paged_decode_attn_bf16(const void *q_bf16, const void *k_new_bf16, const void *v_new_bf16,
+                                      const void *k_src_bf16, const void *v_src_bf16, int32_t num_src_blocks,
+                                      const int32_t *src_block_tables_dev, int32_t max_src_blocks_per_seq,
+                                      const int32_t *seq_lens_dev, int32_t max_seqlen, int32_t batch,
+                                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t block_size, void *out_bf16, void *workspace, size_t workspace_bytes,
+                                      void *cuda_stream)
+{
+    return attn_impl(dgq::kFormatBf16Cache, q_bf16, k_new_bf16, v_new_bf16, static_cast<const uint8_t *>(k_src_bf16),
+                     static_cast<const uint8_t *>(v_src_bf16), nullptr, nullptr, nullptr, nullptr,
+                     src_block_tables_dev, seq_lens_dev, max_seqlen, batch, num_q_heads, num_kv_heads, head_dim,
+                     block_size, max_src_blocks_per_seq, num_src_blocks, out_bf16, workspace, workspace_bytes,
                      cuda_stream);
 }
 
@@ -306,9 +325,6 @@ dgq_status attn_impl(int32_t format, const void *q_bf16, const void *k_new_bf16,
                      int32_t max_blocks_per_seq, int32_t num_blocks, void *out_bf16, void *workspace,
                      size_t workspace_bytes, void *cuda_stream)
 {
-    if (format != DGQ_FORMAT_DGQ && format != DGQ_FORMAT_FIXED64 && format != DGQ_FORMAT_SYM_INT8 &&
-        format != DGQ_FORMAT_FP8_E4M3)
-        return DGQ_ERR_INVALID_ARG;
     if (format == DGQ_FORMAT_FIXED64 && (!k_group_params || !v_group_params || !aligned16(k_group_params) ||
                                          !aligned16(v_group_params)))
         return DGQ_ERR_INVALID_ARG;
@@ -323,8 +339,8 @@ dgq_status attn_impl(int32_t format, const void *q_bf16, const void *k_new_bf16,
     const int64_t chunks = (int64_t)batch * num_kv_heads * ((max_seqlen + 63) / 64 + 1);
     if (chunks >= INT32_MAX || (int64_t)num_blocks * num_kv_heads * block_size >= INT32_MAX)
         return DGQ_ERR_UNSUPPORTED;
-    if (!q_bf16 || !k_new_bf16 || !v_new_bf16 || !k_pool || !v_pool || !seg_table || !block_tables_dev ||
-        !seq_lens_dev || !out_bf16)
+    if (!q_bf16 || !k_new_bf16 || !v_new_bf16 || !k_pool || !v_pool ||
+        (!seg_table && format != dgq::kFormatBf16Cache) || !block_tables_dev || !seq_lens_dev || !out_bf16)
         return DGQ_ERR_INVALID_ARG;
     if (!aligned16(q_bf16) || !aligned16(k_new_bf16) || !aligned16(v_new_bf16) || !aligned16(k_pool) ||
         !aligned16(v_pool) || !aligned16(seg_table) || !aligned16(out_bf16) || !aligned16(block_tables_dev) ||
@@ -527,12 +543,132 @@ dgq_status dgq_workspace_error(const void *workspace, void *cuda_stream, int32_t
     return word ? DGQ_ERR_DEVICE : DGQ_OK;
 }
 
+// ---- prompt attention -------------------------------------------------------------------
+
+size_t dgq_prompt_attn_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads)
+{
+    if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads) return 0;
+    int nsm = 0;
+    if (device_sm_count(&nsm) != 0) return 0;
+    return dgq::prompt_workspace_bytes(batch, num_q_heads, num_kv_heads, nsm);
+}
+
+namespace {
+// Checks and launch shared by the packed and the paged entry point (bt null: packed).
+dgq_status prompt_impl(const void *q, const void *k, const void *v, int32_t total_q, int32_t total_kv,
+                       const int32_t *cu_q, const int32_t *kv, bool paged, const int32_t *bt, int32_t block_size,
+                       int32_t max_blocks, int32_t num_blocks, int32_t batch, int32_t num_q_heads,
+                       int32_t num_kv_heads, int32_t head_dim, void *out, void *workspace, size_t workspace_bytes,
+                       void *cuda_stream)
+{
+    if (head_dim != DGQ_HEAD_DIM || (paged && !block_size_ok(block_size))) return DGQ_ERR_UNSUPPORTED;
+    if (batch <= 0 || batch > kMaxBatch || total_q < 0 || total_kv < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+        num_q_heads % num_kv_heads)
+        return DGQ_ERR_INVALID_ARG;
+    const int32_t G = num_q_heads / num_kv_heads;
+    if (G != 1 && G != 2 && G != 4 && G != 8) return DGQ_ERR_UNSUPPORTED;
+    // grid: one row per KV head; keys, query rows and their heads are counted in 32 bits
+    if (num_kv_heads > 65535 || (int64_t)total_q * num_q_heads >= INT32_MAX ||
+        (int64_t)total_kv * num_kv_heads >= INT32_MAX)
+        return DGQ_ERR_UNSUPPORTED;
+    if (paged) {
+        if (num_blocks <= 0 || max_blocks <= 0 || !bt || !aligned16(bt)) return DGQ_ERR_INVALID_ARG;
+        if ((int64_t)num_blocks * num_kv_heads * block_size >= INT32_MAX ||
+            (int64_t)max_blocks * block_size >= INT32_MAX)
+            return DGQ_ERR_UNSUPPORTED;
+    }
+    // an empty buffer has no address
+    if ((!q && total_q) || (!out && total_q) || ((!k || !v) && (paged || total_kv)) || !cu_q || !kv)
+        return DGQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(cu_q) || !aligned16(kv))
+        return DGQ_ERR_INVALID_ARG;
+    int nsm = 0;
+    if (device_sm_count(&nsm) != 0) return DGQ_ERR_CUDA;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < dgq::prompt_workspace_bytes(batch, num_q_heads, num_kv_heads, nsm))
+        return DGQ_ERR_WORKSPACE;
+    if (total_q == 0) return DGQ_OK;
+    bool map_failed = false;
+    const cudaError_t e = dgq::launch_prompt(q, k, v, total_q, total_kv, cu_q, kv, paged ? bt : nullptr, block_size,
+                                             max_blocks, num_blocks, batch, num_q_heads, num_kv_heads, out, workspace,
+                                             nsm, &map_failed, static_cast<cudaStream_t>(cuda_stream));
+    if (map_failed) return DGQ_ERR_INVALID_ARG;
+    return e == cudaSuccess ? DGQ_OK : DGQ_ERR_CUDA;
+}
+}  // namespace
+
+dgq_status dgq_prompt_attn(const void *q_bf16, const void *k_bf16, const void *v_bf16, int32_t total_q,
+                           int32_t total_kv, const int32_t *cu_q_dev, const int32_t *cu_kv_dev, int32_t batch,
+                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, void *out_bf16,
+                           void *workspace, size_t workspace_bytes, void *cuda_stream)
+{
+    return prompt_impl(q_bf16, k_bf16, v_bf16, total_q, total_kv, cu_q_dev, cu_kv_dev, false, nullptr, 0, 0, 0, batch,
+                       num_q_heads, num_kv_heads, head_dim, out_bf16, workspace, workspace_bytes, cuda_stream);
+}
+
+dgq_status dgq_prompt_attn_paged(const void *q_bf16, int32_t total_q, const int32_t *cu_q_dev, const void *k_src_bf16,
+                                 const void *v_src_bf16, int32_t num_src_blocks, const int32_t *src_block_tables_dev,
+                                 int32_t max_src_blocks_per_seq, const int32_t *seq_lens_dev, int32_t batch,
+                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                 void *out_bf16, void *workspace, size_t workspace_bytes, void *cuda_stream)
+{
+    return prompt_impl(q_bf16, k_src_bf16, v_src_bf16, total_q, 0, cu_q_dev, seq_lens_dev, true, src_block_tables_dev,
+                       block_size, max_src_blocks_per_seq, num_src_blocks, batch, num_q_heads, num_kv_heads, head_dim,
+                       out_bf16, workspace, workspace_bytes, cuda_stream);
+}
+
+// ---- pages ------------------------------------------------------------------------------
+
+size_t dgq_copy_pages_workspace_size(void) { return 256; }  // the workspace header alone
+
+dgq_status dgq_copy_pages(void *const *arrays, int32_t num_arrays, int64_t page_bytes, int32_t num_pages,
+                          const int32_t *pairs_dev, int32_t num_pairs, void *workspace, size_t workspace_bytes,
+                          void *cuda_stream)
+{
+    if (num_arrays < 0 || num_pairs < 0 || page_bytes <= 0 || (page_bytes & 15) || num_pages <= 0)
+        return DGQ_ERR_INVALID_ARG;
+    // units of 4 KB in a page are counted in 32 bits, bytes of an array in 64
+    if (page_bytes > ((int64_t)1 << 40) || page_bytes > INT64_MAX / num_pages) return DGQ_ERR_UNSUPPORTED;
+    if ((num_arrays > 0 && !arrays) || (num_pairs > 0 && !pairs_dev) || !aligned16(pairs_dev))
+        return DGQ_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < num_arrays; ++i)
+        if (!arrays[i] || !aligned16(arrays[i])) return DGQ_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < dgq_copy_pages_workspace_size())
+        return DGQ_ERR_WORKSPACE;
+    if (num_arrays == 0 || num_pairs == 0) return DGQ_OK;
+    int nsm = 0;
+    if (device_sm_count(&nsm) != 0) return DGQ_ERR_CUDA;
+    const cudaError_t e = dgq::launch_copy_pages(arrays, num_arrays, page_bytes, num_pages, pairs_dev, num_pairs,
+                                                 workspace, nsm, static_cast<cudaStream_t>(cuda_stream));
+    return e == cudaSuccess ? DGQ_OK : DGQ_ERR_CUDA;
+}
+
+dgq_status dgq_remap_tables(const int32_t *tables_dev, int64_t num_entries, const int32_t *remap_dev,
+                            int32_t num_pages, int32_t *out_dev, void *workspace, size_t workspace_bytes,
+                            void *cuda_stream)
+{
+    if (num_entries < 0 || num_pages <= 0) return DGQ_ERR_INVALID_ARG;
+    if (num_entries > 0 && (!tables_dev || !remap_dev || !out_dev)) return DGQ_ERR_INVALID_ARG;
+    if (!aligned16(tables_dev) || !aligned16(remap_dev) || !aligned16(out_dev)) return DGQ_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < dgq_copy_pages_workspace_size())
+        return DGQ_ERR_WORKSPACE;
+    if (num_entries == 0) return DGQ_OK;
+    int nsm = 0;
+    if (device_sm_count(&nsm) != 0) return DGQ_ERR_CUDA;
+    const cudaError_t e = dgq::launch_remap_tables(tables_dev, num_entries, remap_dev, num_pages, out_dev, workspace,
+                                                   nsm, static_cast<cudaStream_t>(cuda_stream));
+    return e == cudaSuccess ? DGQ_OK : DGQ_ERR_CUDA;
+}
+
 // ---- host block pool --------------------------------------------------------------------
 
+// A block is free (no reference) or held by one reference per table row (or caller) that names it.
+// All storage is taken at creation, so no later call allocates or throws.
 struct dgq_pool {
     int32_t num_blocks;
-    std::vector<int32_t> free_list;  // stack of free ids
-    std::vector<uint8_t> is_free;
+    std::vector<int32_t> free_list;  // stack of free ids, capacity num_blocks
+    std::vector<int32_t> refs;       // references per block, 0 when free
+    std::vector<uint8_t> mark;       // all 0 between calls
 };
 
 dgq_pool *dgq_pool_create(int32_t num_blocks)
@@ -540,59 +676,180 @@ dgq_pool *dgq_pool_create(int32_t num_blocks)
     if (num_blocks <= 0) return nullptr;
     dgq_pool *p = new (std::nothrow) dgq_pool;
     if (!p) return nullptr;
-    p->num_blocks = num_blocks;
-    p->free_list.resize(num_blocks);
-    p->is_free.assign(num_blocks, 1);
+    try {
+        p->num_blocks = num_blocks;
+        p->free_list.resize(num_blocks);
+        p->refs.assign(num_blocks, 0);
+        p->mark.assign(num_blocks, 0);
+    } catch (const std::bad_alloc &) {
+        delete p;
+        return nullptr;
+    }
     for (int32_t i = 0; i < num_blocks; ++i) p->free_list[i] = num_blocks - 1 - i;  // pops 0, 1, 2, ...
     return p;
 }
 
 void dgq_pool_destroy(dgq_pool *pool) { delete pool; }
 
+namespace {
+
+bool pool_live(const dgq_pool *pool, int32_t id) { return id >= 0 && id < pool->num_blocks && pool->refs[id] > 0; }
+
+int32_t pool_take(dgq_pool *pool)  // one free block, its first reference (the list is not empty)
+{
+    const int32_t id = pool->free_list.back();
+    pool->free_list.pop_back();
+    pool->refs[id] = 1;
+    return id;
+}
+
+// Every id live and none named twice.
+bool pool_ids_ok(dgq_pool *pool, const int32_t *ids, int32_t n)
+{
+    int32_t i = 0;
+    bool ok = true;
+    for (; i < n && ok; ++i) {
+        if (!pool_live(pool, ids[i]) || pool->mark[ids[i]]) {
+            ok = false;
+            break;
+        }
+        pool->mark[ids[i]] = 1;
+    }
+    for (int32_t j = 0; j < i; ++j) pool->mark[ids[j]] = 0;
+    return ok;
+}
+
+}  // namespace
+
 dgq_status dgq_pool_alloc(dgq_pool *pool, int32_t n, int32_t *out_ids)
 {
     if (!pool || n < 0 || (n > 0 && !out_ids)) return DGQ_ERR_INVALID_ARG;
     if ((size_t)n > pool->free_list.size()) return DGQ_ERR_POOL_EXHAUSTED;
-    for (int32_t i = 0; i < n; ++i) {
-        int32_t id = pool->free_list.back();
-        pool->free_list.pop_back();
-        pool->is_free[id] = 0;
-        out_ids[i] = id;
-    }
+    for (int32_t i = 0; i < n; ++i) out_ids[i] = pool_take(pool);
     return DGQ_OK;
 }
 
 dgq_status dgq_pool_free(dgq_pool *pool, const int32_t *ids, int32_t n)
 {
     if (!pool || n < 0 || (n > 0 && !ids)) return DGQ_ERR_INVALID_ARG;
-    std::vector<uint8_t> seen;
-    for (int32_t i = 0; i < n; ++i) {  // validate all first: nothing is freed on error
-        int32_t id = ids[i];
-        if (id < 0 || id >= pool->num_blocks || pool->is_free[id]) return DGQ_ERR_INVALID_ARG;
-        if (seen.empty()) seen.assign(pool->num_blocks, 0);
-        if (seen[id]) return DGQ_ERR_INVALID_ARG;
-        seen[id] = 1;
-    }
-    for (int32_t i = 0; i < n; ++i) {
-        pool->is_free[ids[i]] = 1;
-        pool->free_list.push_back(ids[i]);
-    }
+    if (!pool_ids_ok(pool, ids, n)) return DGQ_ERR_INVALID_ARG;  // validated first: nothing is freed on error
+    for (int32_t i = 0; i < n; ++i)
+        if (--pool->refs[ids[i]] == 0) pool->free_list.push_back(ids[i]);
+    return DGQ_OK;
+}
+
+dgq_status dgq_pool_share(dgq_pool *pool, const int32_t *ids, int32_t n)
+{
+    if (!pool || n < 0 || (n > 0 && !ids)) return DGQ_ERR_INVALID_ARG;
+    if (!pool_ids_ok(pool, ids, n)) return DGQ_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < n; ++i)
+        if (pool->refs[ids[i]] == INT32_MAX) return DGQ_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < n; ++i) ++pool->refs[ids[i]];
     return DGQ_OK;
 }
 
 int32_t dgq_pool_num_free(const dgq_pool *pool) { return pool ? (int32_t)pool->free_list.size() : -1; }
+
+int32_t dgq_pool_references(const dgq_pool *pool, int32_t id)
+{
+    return pool && id >= 0 && id < pool->num_blocks ? pool->refs[id] : -1;
+}
 
 dgq_status dgq_pool_alloc_table_row(dgq_pool *pool, int32_t len, int32_t block_size, int32_t *table, int32_t row,
                                     int32_t max_blocks_per_seq)
 {
     if (!pool || !table || len < 0 || row < 0 || max_blocks_per_seq <= 0 || block_size <= 0)
         return DGQ_ERR_INVALID_ARG;
-    const int32_t n = (len + block_size - 1) / block_size;
+    const int32_t n = (int32_t)(((int64_t)len + block_size - 1) / block_size);
     if (n > max_blocks_per_seq) return DGQ_ERR_INVALID_ARG;
     int32_t *dst = table + (int64_t)row * max_blocks_per_seq;
     dgq_status s = dgq_pool_alloc(pool, n, dst);
     if (s != DGQ_OK) return s;
     for (int32_t i = n; i < max_blocks_per_seq; ++i) dst[i] = 0;
+    return DGQ_OK;
+}
+
+dgq_status dgq_pool_fork_row(dgq_pool *pool, int32_t len, int32_t block_size, int32_t *table, int32_t src_row,
+                             int32_t dst_row, int32_t max_blocks_per_seq, int32_t *out_pair, int32_t *num_pairs)
+{
+    if (!pool || !table || !out_pair || !num_pairs || len < 0 || src_row < 0 || dst_row < 0 || src_row == dst_row ||
+        max_blocks_per_seq <= 0 || block_size <= 0)
+        return DGQ_ERR_INVALID_ARG;
+    const int32_t n = (int32_t)(((int64_t)len + block_size - 1) / block_size), whole = len / block_size;
+    if (n > max_blocks_per_seq) return DGQ_ERR_INVALID_ARG;
+    const int32_t *src = table + (int64_t)src_row * max_blocks_per_seq;
+    int32_t *dst = table + (int64_t)dst_row * max_blocks_per_seq;
+    if (!pool_ids_ok(pool, src, n)) return DGQ_ERR_INVALID_ARG;
+    if (n > whole && pool->free_list.empty()) return DGQ_ERR_POOL_EXHAUSTED;
+    const dgq_status s = dgq_pool_share(pool, src, whole);
+    if (s != DGQ_OK) return s;
+    for (int32_t i = 0; i < whole; ++i) dst[i] = src[i];
+    *num_pairs = 0;
+    if (n > whole) {
+        out_pair[0] = src[whole];
+        out_pair[1] = dst[whole] = pool_take(pool);
+        *num_pairs = 1;
+    }
+    for (int32_t i = n; i < max_blocks_per_seq; ++i) dst[i] = 0;
+    return DGQ_OK;
+}
+
+dgq_status dgq_pool_own_row(dgq_pool *pool, int32_t *table, int32_t row, int32_t max_blocks_per_seq,
+                            int32_t first_block, int32_t num_row_blocks, int32_t *out_pairs, int32_t *num_pairs)
+{
+    if (!pool || !table || !num_pairs || row < 0 || max_blocks_per_seq <= 0 || first_block < 0 ||
+        num_row_blocks < 0 || first_block > max_blocks_per_seq - num_row_blocks || (num_row_blocks > 0 && !out_pairs))
+        return DGQ_ERR_INVALID_ARG;
+    int32_t *ids = table + (int64_t)row * max_blocks_per_seq + first_block;
+    if (!pool_ids_ok(pool, ids, num_row_blocks)) return DGQ_ERR_INVALID_ARG;
+    int32_t shared = 0;
+    for (int32_t i = 0; i < num_row_blocks; ++i) shared += pool->refs[ids[i]] > 1;
+    if ((size_t)shared > pool->free_list.size()) return DGQ_ERR_POOL_EXHAUSTED;
+    int32_t n = 0;
+    for (int32_t i = 0; i < num_row_blocks; ++i) {
+        if (pool->refs[ids[i]] == 1) continue;
+        const int32_t id = pool_take(pool);
+        out_pairs[2 * n] = ids[i];
+        out_pairs[2 * n + 1] = id;
+        ++n;
+        --pool->refs[ids[i]];
+        ids[i] = id;
+    }
+    *num_pairs = n;
+    return DGQ_OK;
+}
+
+dgq_status dgq_pool_free_row(dgq_pool *pool, int32_t *table, int32_t row, int32_t max_blocks_per_seq,
+                             int32_t num_row_blocks)
+{
+    if (!pool || !table || row < 0 || max_blocks_per_seq <= 0 || num_row_blocks < 0 ||
+        num_row_blocks > max_blocks_per_seq)
+        return DGQ_ERR_INVALID_ARG;
+    int32_t *ids = table + (int64_t)row * max_blocks_per_seq;
+    const dgq_status s = dgq_pool_free(pool, ids, num_row_blocks);
+    if (s != DGQ_OK) return s;
+    for (int32_t i = 0; i < max_blocks_per_seq; ++i) ids[i] = 0;
+    return DGQ_OK;
+}
+
+dgq_status dgq_pool_compact(dgq_pool *pool, int32_t *remap, int32_t *out_pairs, int32_t *num_pairs)
+{
+    if (!pool || !remap || !num_pairs || (pool->num_blocks > 1 && !out_pairs)) return DGQ_ERR_INVALID_ARG;
+    const int32_t live = pool->num_blocks - (int32_t)pool->free_list.size();
+    int32_t n = 0, hole = 0;
+    for (int32_t id = 0; id < pool->num_blocks; ++id) remap[id] = id;
+    for (int32_t id = live; id < pool->num_blocks; ++id) {  // ascending ids into ascending holes
+        if (pool->refs[id] == 0) continue;
+        while (pool->refs[hole] != 0) ++hole;
+        out_pairs[2 * n] = id;
+        out_pairs[2 * n + 1] = hole;
+        ++n;
+        remap[id] = hole;
+        pool->refs[hole] = pool->refs[id];
+        pool->refs[id] = 0;
+    }
+    for (int32_t i = 0; i < pool->num_blocks - live; ++i) pool->free_list[i] = pool->num_blocks - 1 - i;
+    *num_pairs = n;
     return DGQ_OK;
 }
 

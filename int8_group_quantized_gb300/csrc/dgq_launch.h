@@ -52,7 +52,10 @@ struct AttnLayout {
     size_t off_count, off_held, off_part, total;
 };
 AttnLayout attn_layout(int32_t batch, int32_t Hq, int32_t Hkv, int nsm);
-// format: a dgq_format (DGQ and SYM_INT8 decode through the records; kpar / vpar are read for
+// Decode over an unquantised bf16 paged cache (pools bf16, no records): beside the dgq_format values.
+constexpr int32_t kFormatBf16Cache = 16;
+
+// format: a dgq_format or kFormatBf16Cache (DGQ and SYM_INT8 decode through the records; kpar / vpar are read for
 // FIXED64 only).  vtable non-null (DGQ only): independent V segmentation, V's records there.
 cudaError_t launch_attn(int32_t format, const void *q, const void *knew, const void *vnew, const uint8_t *kpool,
                         const uint8_t *vpool, const dgq_seg_record *table, const dgq_seg_record *vtable,
@@ -86,6 +89,20 @@ cudaError_t launch_prefill_finish(const SourceDesc &src, const int32_t *seq_lens
                                   int32_t num_blocks, dgq_seg_record *table, dgq_seg_record *vtable,
                                   GroupSettings gs, const int32_t *sel, int32_t sel_mask, void *ws, int nsm,
                                   bool *map_failed, cudaStream_t stream);
+
+// Causal attention of prompts over bf16 K and V: packed rows (bt null, kv = cumulative lengths) or a
+// paged cache (kv = lengths).
+size_t prompt_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int nsm);
+cudaError_t launch_prompt(const void *q, const void *k, const void *v, int32_t total_q, int32_t total_kv,
+                          const int32_t *cu_q, const int32_t *kv, const int32_t *bt, int32_t bs, int32_t max_blocks,
+                          int32_t num_blocks, int32_t B, int32_t Hq, int32_t Hkv, void *out, void *ws, int nsm,
+                          bool *map_failed, cudaStream_t stream);
+
+// Pages copied by a list of (source, destination) ids in every array; table entries renamed.
+cudaError_t launch_copy_pages(void *const *arrays, int32_t num_arrays, int64_t page_bytes, int32_t num_pages,
+                              const int32_t *pairs, int32_t num_pairs, void *ws, int nsm, cudaStream_t stream);
+cudaError_t launch_remap_tables(const int32_t *in, int64_t n, const int32_t *remap, int32_t num_pages, int32_t *out,
+                                void *ws, int nsm, cudaStream_t stream);
 
 // cuTensorMapEncodeTiled from the driver (through the runtime's entry-point query), or null.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
