@@ -4,11 +4,32 @@
 // Request b has n = cu_q[b+1] - cu_q[b] query rows and m keys; query row i sits at position
 // m - n + i and sees the keys t <= m - n + i:
 //   out[i] = sum_t softmax_t(q_i . k_t / sqrt(128)) v_t, zeros where the row sees no key (m < n).
-// The G query heads of a KV head are packed into the rows of one product: row r of a tile is token
-// r / G, head r % G, so a K and V tile is read once for the whole group.
 //
-// First form: one CTA of four warps per 64 packed rows of a KV head, keys in tiles of 64 through
-// shared memory, mma.sync m16n8k16, online softmax in the log2 domain.
+// GPU design.
+//  * Rows: the G query heads of a KV head are packed into the rows of one product (row r of a tile is
+//    token r / G, head r % G), so a K and V tile is read once for the whole group.  A unit is two
+//    tiles of 128 rows (256 / G tokens of one KV head).
+//  * Products: S = Q K^T and O += P V on the fifth-generation tensor cores (tcgen05.mma, 128 x 128 x 16
+//    per instruction, fp32 accumulators in tensor memory).  Tensor memory holds S and O of both tiles
+//    (4 x 128 columns); P, rounded to bf16, overwrites the S it came from and is the A operand of the
+//    second product, so no weight passes through shared memory.  V is read as it lies (keys by
+//    values), a transposed B operand.
+//  * Roles: warp 8 loads (TMA, a ring of five 32 KB K or V tiles, 128-byte swizzle), one thread of warp
+//    9 issues every product, warps 0-3 and 4-7 are the softmax of tile 0 and of tile 1, one row per
+//    thread.  While one tile's softmax runs, the tensor cores work on the other's products.
+//  * Softmax: online, log2 domain, the reference maximum moving only when a tile exceeds it by 8 (lazy
+//    rescaling: O in tensor memory is then multiplied in place; the softmax threads may do that
+//    between products because S of the next key tile is complete only after O's product is).
+//  * Work: all units lie in one flat list by cost, a unit costing the keys it sees plus a constant, and
+//    each CTA (one per SM) takes an equal slice; a slice may begin and end inside a unit, at a key
+//    tile.  A unit cut that way leaves its parts' maxima, sums and unnormalised O in the workspace, and
+//    a merge kernel chained with programmatic dependent launch folds them in order (bitwise
+//    repeatable on a given GPU).  Cuts within kSnap key tiles of a unit's end move there.
+//  * What cannot be seen: columns past a row's limit get weight 0; V rows behind a request's end are
+//    zeroed in shared memory, so that values of other requests or of unused slots (NaN too) never
+//    meet a weight.
+//  * Every wait is bounded (two seconds): a wait that runs out records an error and raises a flag at which
+//    all roles leave.
 #include "dgq_device.cuh"
 #include "dgq.h"
 #include "dgq_launch.h"
@@ -18,16 +39,36 @@
 
 namespace dgq {
 
-constexpr float kPromptScale = 0.12751743074570180f;  // log2(e) / sqrt(128)
-constexpr int kPmRows = 64, kPmKeys = 64;
+constexpr float kPmScale = 0.12751743074570180f;  // log2(e) / sqrt(128)
+constexpr float kPmLazy = 8.0f / kPmScale;        // the maximum moves when exceeded by 8 in the log2 domain
+constexpr int kPmTile = 128;                      // rows of a tile, keys of a key tile
+constexpr int kPmStages = 5;
+constexpr int kPmTileBytes = kPmTile * kD * 2;    // 32 KB: two halves of 64 columns, [row][64] each
+constexpr int kPmHalf = kPmTileBytes / 2;
+constexpr int kPmThreads = 320;
+constexpr int kPmLoadWarp = 8, kPmMmaWarp = 9;
+constexpr int kPmUnitCost = 2 * kPmTile;          // a unit's fixed cost, in keys
+constexpr int kPmSnap = 4;                        // key tiles: no part of a cut unit is smaller
+constexpr int kPmRows = 2 * kPmTile;              // packed rows of a unit
+constexpr unsigned long long kPmWaitNs = 2000000000ull;
+
+// Tensor-memory columns of the 512 a CTA takes: S (and P) of tile 0 and 1, O of tile 0 and 1.
+constexpr uint32_t kPmColS = 0, kPmColO = 256;
 
 struct PromptArgs {
-    const uint16_t *q, *k, *v;
     uint16_t *out;
     const int32_t *cu_q, *kv;  // kv: cu_kv (packed) or sequence lengths (paged)
     const int32_t *bt;         // null: packed
     WsHeader *hdr;
+    int4 *head;    // per CTA: the unit its slice ends inside of and begins (x: 1 + slot parity, or 0)
+    int32_t *cont; // per CTA: 1 its first piece continues a unit, 2 and ends it there
+    float2 *ml;    // per slot and row: maximum and sum
+    float *part;   // per slot: O [256][128], unnormalised
     int32_t B, Hq, Hkv, G, total_q, total_kv, bs, max_blocks, num_blocks;
+};
+
+struct PromptMaps {
+    CUtensorMap q, k, v;
 };
 
 struct PromptSeq {
@@ -59,13 +100,182 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs &a, int32_t b, 
     return s;
 }
 
-__device__ __forceinline__ void pm_mma(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
+// ---- the flat list of units ---------------------------------------------------------------------
+
+// A position in the list: request, KV head, unit, key tile.
+struct PromptPos {
+    int32_t b, h, i, j;
+};
+
+__device__ __forceinline__ bool same_unit(const PromptPos &x, const PromptPos &y)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    return x.b == y.b && x.h == y.h && x.i == y.i;
 }
+
+__device__ __forceinline__ int32_t prompt_units(const PromptSeq &s, int32_t U) { return (s.n + U - 1) / U; }
+
+// Keys that the tokens before `tok` of the request see (the last of them sees all of these).
+__device__ __forceinline__ int32_t keys_before(const PromptSeq &s, int32_t tok)
+{
+    return max(0, s.m - s.n + min(tok, s.n));
+}
+
+__device__ __forceinline__ int32_t key_tiles(int32_t keys) { return (keys + kPmTile - 1) / kPmTile; }
+
+// Cost of a head's first i units: kPmUnitCost each and max(0, off + x U) for x = 1 .. i (the last unit
+// counted as if it were full).
+__device__ __forceinline__ int64_t unit_cost(const PromptSeq &s, int32_t U, int32_t i)
+{
+    const int32_t off = s.m - s.n;
+    const int64_t x0 = off >= 0 ? 0 : min(i, -off / U);  // units that see no key
+    const int64_t c = (int64_t)i - x0;
+    return (int64_t)i * kPmUnitCost + c * off + U * (((int64_t)i * (i + 1) - x0 * (x0 + 1)) / 2);
+}
+
+__device__ __forceinline__ void next_unit(const PromptArgs &a, int32_t U, PromptPos &p, PromptSeq &s)
+{
+    p.j = 0;
+    if (++p.i < prompt_units(s, U)) return;
+    p.i = 0;
+    if (++p.h < a.Hkv) return;
+    p.h = 0;
+    while (++p.b < a.B) {
+        s = prompt_seq(a, p.b, false);
+        if (s.n > 0) return;
+    }
+}
+
+// The unit and key tile at cost position pos (pre: cost prefix over requests, [B + 1]).
+__device__ PromptPos cut_at(const PromptArgs &a, int32_t U, int64_t pos, const int64_t *pre)
+{
+    PromptPos p = {a.B, 0, 0, 0};
+    if (pos >= pre[a.B]) return p;
+    int32_t lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= pos) lo = mid;
+        else hi = mid - 1;
+    }
+    PromptSeq s = prompt_seq(a, lo, false);  // has units: the next prefix is larger
+    const int32_t nu = prompt_units(s, U);
+    const int64_t per_head = unit_cost(s, U, nu);
+    int64_t r = pos - pre[lo];
+    p.b = lo;
+    p.h = (int32_t)(r / per_head);
+    r -= p.h * per_head;
+    lo = 0;
+    hi = nu - 1;
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (unit_cost(s, U, mid) <= r) lo = mid;
+        else hi = mid - 1;
+    }
+    p.i = lo;
+    r -= unit_cost(s, U, lo) + kPmUnitCost;
+    const int32_t tiles = key_tiles(keys_before(s, (lo + 1) * U));
+    int32_t j = r > 0 ? (int32_t)(r / kPmTile) : 0;
+    if (j > tiles - kPmSnap) {
+        if (j >= kPmSnap || r > 0) next_unit(a, U, p, s);
+        return p;
+    }
+    p.j = j < kPmSnap ? 0 : j;
+    return p;
+}
+
+// ---- tcgen05 ------------------------------------------------------------------------------------
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+// 32 columns of the warp's 32 lanes: thread l receives lane l's columns.
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// D (fp32, 128 x 128) (+)= A B, 16 deep, bf16 operands; B n-by-k (K-major) in shared memory.
+constexpr uint32_t kIdescQK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+// the same with B k-by-n as it lies (MN-major: bit 16)
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
+
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t atmem, uint64_t bdesc, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(atmem), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Shared-memory operand descriptors of a [128][64] half tile pair under the 128-byte swizzle: address
+// and strides in units of 16 bytes, version 1 (bit 46), swizzle mode 2 (bit 61).
+// K-major: 8-row groups 1024 bytes apart (the leading stride is not used).
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr)
+{
+    return (uint64_t)(addr >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// MN-major: 64-column atoms kPmHalf apart, 8-key groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr)
+{
+    return (uint64_t)(addr >> 4) | ((uint64_t)(kPmHalf >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void tma_tile_4d(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
+                                            int32_t c3, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_tile_2d(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// ---- small arithmetic -----------------------------------------------------------------------------
 
 __device__ __forceinline__ float pm_ex2(float x)
 {
@@ -74,154 +284,615 @@ __device__ __forceinline__ float pm_ex2(float x)
     return y;
 }
 
-__global__ void __launch_bounds__(128) prompt_simple_kernel(PromptArgs a)
+__device__ __forceinline__ float max3(float a, float b, float c)
 {
-    __shared__ __align__(16) uint16_t sk[kPmKeys][kD + 8], sv[kPmKeys][kD + 8];
-    __shared__ int32_t s_b, s_unit;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, cq = lane & 3;
-    const int32_t h = blockIdx.y, G = a.G, tok_per = kPmRows / G;
-    if (tid == 0) {
-        int32_t u = blockIdx.x, b = 0;
-        for (; b < a.B; ++b) {
-            const int32_t nu = (prompt_seq(a, b, true).n + tok_per - 1) / tok_per;
-            if (u < nu) break;
-            u -= nu;
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t pm_pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// ---- the kernel -----------------------------------------------------------------------------------
+
+struct PromptBars {
+    uint64_t full[kPmStages], empty[kPmStages];
+    uint64_t q_full[2], s_full[2], p_ready[2], o_full[2];
+    uint64_t q_empty, v_part, drain;
+    uint32_t tmem;
+    volatile uint32_t abort;
+    PromptPos cut[2];
+    int64_t wsum[kPmThreads / 32];
+};
+
+constexpr size_t kPmSmem = 1024 + (size_t)(2 + kPmStages) * kPmTileBytes + sizeof(PromptBars);
+static_assert(kPmSmem <= 232448, "shared memory of a CTA");
+static_assert((size_t)(kMaxCallBatch + 1) * 8 <= (size_t)kPmStages * kPmTileBytes, "the request prefix uses the ring");
+
+// Bounded wait, with one answer for all `mask` lanes.  False: the wait ran out, here or elsewhere.
+__device__ __forceinline__ bool pm_wait(uint64_t *bar, uint32_t parity, PromptBars *sb, WsHeader *hdr, uint32_t mask)
+{
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(mask, ok)) {
+        unsigned long long t0, t;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+        for (uint32_t i = 1;; ++i) {
+            if (!ok) ok = mbar_try_wait(bar, parity);
+            if (__all_sync(mask, ok)) break;
+            if ((i & 63u) == 0) {
+                bool over = sb->abort != 0;
+                asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+                if (t - t0 > kPmWaitNs) {
+                    over = true;
+                    sb->abort = 1;
+                    record_error(hdr, kErrFullWait);
+                }
+                if (__any_sync(mask, over)) return false;
+            }
         }
-        s_b = b;
-        s_unit = u;
+    }
+    return true;
+}
+
+// A unit's tiles in the piece [j0, j1): per tile the key tiles to go through, and its keys.
+struct PromptPiece {
+    int32_t j1;        // end of the piece
+    int32_t e0, e1;    // key tiles of tile 0, 1 inside the piece (from j0)
+    int32_t steps;     // key tiles loaded
+};
+
+__device__ __forceinline__ PromptPiece piece_of(const PromptSeq &s, const PromptPos &p, const PromptPos &end, int32_t U)
+{
+    PromptPiece z;
+    const int32_t half = U / 2, tok = p.i * U;
+    const int32_t k0 = keys_before(s, tok + half), k1 = keys_before(s, tok + U);
+    const bool two = tok + half < s.n;  // tile 1 has rows
+    z.j1 = same_unit(p, end) ? end.j : key_tiles(k1);
+    z.e0 = max(0, min(z.j1, key_tiles(k0)) - p.j);
+    z.e1 = two ? max(0, z.j1 - p.j) : 0;
+    z.steps = max(z.e0, z.e1);
+    return z;
+}
+
+__device__ __forceinline__ bool before(const PromptPos &x, const PromptPos &end)
+{
+    if (x.b != end.b) return x.b < end.b;
+    if (x.h != end.h) return x.h < end.h;
+    if (x.i != end.i) return x.i < end.i;
+    return x.j < end.j;
+}
+
+__global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs a, const __grid_constant__ PromptMaps maps)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_smem_1024(smem_raw);
+    PromptBars *sb = reinterpret_cast<PromptBars *>(smem + (2 + kPmStages) * kPmTileBytes);
+    const uint32_t sq = smem_u32(smem), sring = sq + 2 * kPmTileBytes;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t G = a.G, U = kPmRows / G;
+
+    pdl_launch_dependents();  // the merge may be scheduled while this kernel runs
+
+    // ---- this CTA's slice of the flat list
+    {
+        int64_t *pre = reinterpret_cast<int64_t *>(smem + 2 * kPmTileBytes);  // the ring is not in use yet
+        int64_t carry = 0;
+        for (int32_t base = 0; base < a.B; base += kPmThreads) {
+            const int32_t b = base + tid;
+            int64_t c = 0;
+            if (b < a.B) {
+                const PromptSeq s = prompt_seq(a, b, blockIdx.x == 0);
+                c = a.Hkv * unit_cost(s, U, prompt_units(s, U));
+            }
+            int64_t x = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) sb->wsum[warp] = x;
+            __syncthreads();
+            int64_t before_warp = 0, all = 0;
+#pragma unroll
+            for (int w = 0; w < kPmThreads / 32; ++w) {
+                if (w < warp) before_warp += sb->wsum[w];
+                all += sb->wsum[w];
+            }
+            if (b < a.B) pre[b] = carry + before_warp + x - c;
+            carry += all;
+            __syncthreads();
+        }
+        if (tid == 0) {
+            pre[a.B] = carry;
+            for (int i = 0; i < kPmStages; ++i) {
+                mbar_init(&sb->full[i], 1);
+                mbar_init(&sb->empty[i], 1);
+            }
+            for (int t = 0; t < 2; ++t) {
+                mbar_init(&sb->q_full[t], 1);
+                mbar_init(&sb->s_full[t], 1);
+                mbar_init(&sb->p_ready[t], 4);
+                mbar_init(&sb->o_full[t], 1);
+            }
+            mbar_init(&sb->q_empty, 1);
+            mbar_init(&sb->v_part, 1);
+            mbar_init(&sb->drain, 1);
+            sb->abort = 0;
+            fence_barrier_init();
+        }
+        __syncthreads();
+        if (lane == 0 && warp < 2) {
+            const int64_t c = blockIdx.x + warp;
+            sb->cut[warp] = c == 0 ? cut_at(a, U, 0, pre)
+                                   : (c == gridDim.x ? PromptPos{a.B, 0, 0, 0}
+                                                     : cut_at(a, U, (int64_t)((carry / gridDim.x) * c + (carry % gridDim.x) * c / gridDim.x), pre));
+        }
+        __syncthreads();
+    }
+    const PromptPos begin = sb->cut[0], end = sb->cut[1];
+    const bool work = before(begin, end);
+    if (tid == 0) {  // read by the merge
+        const bool one = same_unit(begin, end);
+        int4 head = make_int4(0, 0, 0, 0);
+        if (work && end.j > 0 && !(one && begin.j > 0)) head = make_int4(one ? 1 : 2, end.b, end.h, end.i);
+        a.head[blockIdx.x] = head;
+        a.cont[blockIdx.x] = work && begin.j > 0 ? (one ? 1 : 2) : 0;
+    }
+    if (!work) return;  // the whole CTA: no barrier follows for it
+    if (warp == kPmMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(&sb->tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        tc_fence_before();
     }
     __syncthreads();
-    const int32_t b = s_b;
-    if (b >= a.B) return;
-    const PromptSeq s = prompt_seq(a, b, false);
-    const int32_t t0 = s_unit * tok_per, off = s.m - s.n;
-    // this lane's rows: 16 warp + r and + 8
-    int32_t tok[2], hd[2], lim[2];
-    const uint16_t *qrow[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int row = 16 * warp + r + 8 * e;
-        tok[e] = t0 + row / G;
-        hd[e] = h * G + row % G;
-        const bool ok = row < tok_per * G && tok[e] < s.n;
-        lim[e] = ok ? min(s.m, off + tok[e] + 1) : 0;  // keys the row sees
-        if (!ok) tok[e] = -1;
-        qrow[e] = a.q + ((int64_t)(s.q0 + max(tok[e], 0)) * a.Hq + hd[e]) * kD;
-    }
-    uint32_t qf[8][4];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            qf[k][e] = *reinterpret_cast<const uint32_t *>(qrow[e & 1] + 16 * k + 2 * cq + 8 * (e >> 1));
-    float o[16][4], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    const int32_t keys = min(s.m, off + min(s.n, t0 + tok_per));
-    for (int32_t j0 = 0; j0 < keys; j0 += kPmKeys) {
-        __syncthreads();
-        for (int i = tid; i < kPmKeys * 16; i += 128) {  // 16-byte columns; rows past the end as zeros
-            const int row = i >> 4, col = i & 15;
-            const int32_t t = j0 + row;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-            if (t < s.m) {
-                int64_t kr;
-                if (a.bt) {
-                    int32_t blk = __ldg(a.bt + (int64_t)b * a.max_blocks + pow2_div(t, a.bs));
-                    if ((uint32_t)blk >= (uint32_t)a.num_blocks) {
-                        record_error(a.hdr, kErrBadBlock);
+    tc_fence_after();
+    const uint32_t tmem = sb->tmem;
+
+    PromptPos pos = begin;
+    PromptSeq s = prompt_seq(a, pos.b, false);
+
+    if (warp == kPmLoadWarp) {
+        // ======================================== loads
+        fence_proxy_async_smem();  // the prefix was read from the ring by ordinary loads
+        const int32_t pages = a.bt ? kPmTile / a.bs : 0;  // pages of a key tile
+        uint32_t it = 0, nv = 0;
+        uint32_t nq[2] = {0, 0};  // Q tiles loaded
+        bool ok = true, v_flight = false;
+        uint32_t q_loaded = 0;  // pieces with a Q load
+        for (; ok && before(pos, end); next_unit(a, U, pos, s)) {
+            const PromptPiece z = piece_of(s, pos, end, U);
+            if (z.steps == 0) continue;
+            if (q_loaded > 0 && !pm_wait(&sb->q_empty, (q_loaded - 1) & 1u, sb, a.hdr, 0xffffffffu)) break;
+            ++q_loaded;
+            if (lane == 0) {
+                const int32_t tok = s.q0 + pos.i * U;
+                if (z.e0 > 0) {
+                    ++nq[0];
+                    mbar_arrive_expect_tx(&sb->q_full[0], kPmTileBytes);
+                    tma_tile_4d(sq, &maps.q, 0, pos.h * G, tok, 0, &sb->q_full[0]);
+                }
+                if (z.e1 > 0) {
+                    ++nq[1];
+                    mbar_arrive_expect_tx(&sb->q_full[1], kPmTileBytes);
+                    tma_tile_4d(sq + kPmTileBytes, &maps.q, 0, pos.h * G, tok + U / 2, 0, &sb->q_full[1]);
+                }
+            }
+            // lane l copies half l % 2 of page l / 2 of the key tile
+            auto block_of = [&](int32_t j) -> int32_t {
+                int32_t blk = 0;
+                const int32_t t = j * kPmTile + (lane >> 1) * a.bs;
+                if (lane < 2 * pages && t < s.m) {
+                    blk = __ldg(a.bt + (int64_t)pos.b * a.max_blocks + pow2_div(t, a.bs));
+                    if ((uint32_t)blk >= (uint32_t)a.num_blocks) {  // not a block of the cache: flagged,
+                        record_error(a.hdr, kErrBadBlock);          // and block 0 read instead
                         blk = 0;
                     }
-                    kr = ((int64_t)blk * a.Hkv + h) * a.bs + pow2_mod(t, a.bs);
-                } else {
-                    kr = (int64_t)(s.kv0 + t) * a.Hkv + h;
                 }
-                x = __ldg(reinterpret_cast<const uint4 *>(a.k + kr * kD) + col);
-                y = __ldg(reinterpret_cast<const uint4 *>(a.v + kr * kD) + col);
+                return blk;
+            };
+            int32_t blk = a.bt ? block_of(pos.j) : 0;
+            for (int32_t j = pos.j; j < pos.j + z.steps; ++j) {
+                const int32_t valid = min(kPmTile, s.m - j * kPmTile);  // keys of the tile
+                const int32_t blk_next = a.bt && j + 1 < pos.j + z.steps ? block_of(j + 1) : 0;
+                const int32_t used = a.bt ? (valid + a.bs - 1) / a.bs : 0;
+                const uint32_t bytes = a.bt ? (uint32_t)used * a.bs * kD * 2 : (uint32_t)kPmTileBytes;
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t st = it % kPmStages, dst = sring + st * kPmTileBytes;
+                    if (it >= kPmStages && !pm_wait(&sb->empty[st], (it / kPmStages - 1) & 1u, sb, a.hdr, 0xffffffffu)) {
+                        ok = false;
+                        break;
+                    }
+                    const CUtensorMap *map = kv ? &maps.v : &maps.k;
+                    const bool part = kv == 1 && valid < kPmTile;  // V rows to clear behind the end
+                    uint64_t *bar = part ? &sb->v_part : &sb->full[st];
+                    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                    __syncwarp();
+                    if (a.bt) {
+                        if (lane < 2 * used) {
+                            const int32_t row = (blk * a.Hkv + pos.h) * a.bs;
+                            tma_tile_2d(dst + (lane & 1) * kPmHalf + (lane >> 1) * a.bs * 128, map, (lane & 1) * 64, row,
+                                        bar);
+                        }
+                    } else if (lane == 0) {
+                        tma_tile_4d(dst, map, 0, s.kv0 + j * kPmTile, pos.h, 0, bar);
+                    }
+                    v_flight = part;
+                    if (part) {
+                        if (!pm_wait(&sb->v_part, nv & 1u, sb, a.hdr, 0xffffffffu)) {
+                            ok = false;
+                            break;
+                        }
+                        ++nv;
+                        v_flight = false;
+                        uint8_t *t = smem + 2 * kPmTileBytes + st * kPmTileBytes;
+                        for (int32_t x = valid * 8 + lane; x < kPmTile * 8; x += 32) {
+                            *reinterpret_cast<uint4 *>(t + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4 *>(t + kPmHalf + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sb->full[st]);
+                    }
+                    ++it;
+                }
+                if (!ok) break;
+                blk = blk_next;
             }
-            *reinterpret_cast<uint4 *>(&sk[row][col * 8]) = x;
-            *reinterpret_cast<uint4 *>(&sv[row][col * 8]) = y;
         }
-        __syncthreads();
-        float z[8][4];
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-            z[nt][0] = z[nt][1] = z[nt][2] = z[nt][3] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint16_t *kp = &sk[8 * nt + r][16 * k + 2 * cq];
-                pm_mma(z[nt], qf[k], *reinterpret_cast<const uint32_t *>(kp),
-                       *reinterpret_cast<const uint32_t *>(kp + 8));
-            }
+        if (sb->abort != 0 && lane == 0) {  // some wait ran out: no copy may still be in flight when the CTA ends
+            auto drain = [](uint64_t *bar, uint32_t parity) {
+                for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(bar, parity); ++i) {}
+            };
+            for (uint32_t k = it > kPmStages ? it - kPmStages : 0; k < it; ++k)
+                drain(&sb->full[k % kPmStages], (k / kPmStages) & 1u);
+            for (int t = 0; t < 2; ++t)
+                if (nq[t] > 0) drain(&sb->q_full[t], (nq[t] - 1) & 1u);
+            if (v_flight) drain(&sb->v_part, nv & 1u);
         }
-        float mt[2] = {-INFINITY, -INFINITY};
+        __syncwarp();
+    } else if (warp == kPmMmaWarp) {
+        // ======================================== products, one thread
+        if (lane == 0) {
+            uint32_t it = 0;                    // ring position
+            uint32_t nq[2] = {0, 0};            // Q tiles taken
+            uint32_t npr[2] = {0, 0};           // P tiles taken
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return pm_wait(bar, parity, sb, a.hdr, 1u); };
+            for (; ok && before(pos, end); next_unit(a, U, pos, s)) {
+                const PromptPiece z = piece_of(s, pos, end, U);
+                if (z.steps == 0) continue;
+                // S of key tile k (its K tile at ring position kt) for tile t
+                auto qk = [&](int t, uint32_t kt) {
+                    const uint32_t qa = sq + t * kPmTileBytes, kb = sring + (kt % kPmStages) * kPmTileBytes;
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t o = (k >> 2) * kPmHalf + (k & 3) * 32;
+                        tc_mma_ss(tmem + kPmColS + t * 128, desc_k(qa + o), desc_k(kb + o), kIdescQK, k > 0);
+                    }
+                    tc_commit(&sb->s_full[t]);
+                };
+                // first key tile
+                if (!wait(&sb->full[it % kPmStages], (it / kPmStages) & 1u)) break;
+                for (int t = 0; t < 2; ++t) {
+                    if ((t ? z.e1 : z.e0) == 0) continue;
+                    if (!wait(&sb->q_full[t], nq[t] & 1u)) { ok = false; break; }
+                    ++nq[t];
+                    qk(t, it);
+                }
+                if (!ok) break;
+                tc_commit(&sb->empty[it % kPmStages]);
+                if (z.steps == 1) tc_commit(&sb->q_empty);
+                for (int32_t j = 0; ok && j < z.steps; ++j) {
+                    const uint32_t vt = it + 1, kt = it + 2;  // V of this key tile, K of the next
+                    const bool more = j + 1 < z.steps;
+                    if (!wait(&sb->full[vt % kPmStages], (vt / kPmStages) & 1u)) { ok = false; break; }
+                    bool have_k = false;
+                    for (int t = 0; t < 2; ++t) {
+                        const int32_t e = t ? z.e1 : z.e0;
+                        if (j < e) {
+                            if (!wait(&sb->p_ready[t], npr[t] & 1u)) { ok = false; break; }
+                            ++npr[t];
+                            tc_fence_after();
+                            const uint32_t vb = sring + (vt % kPmStages) * kPmTileBytes;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int32_t t = j0 + 8 * nt + 2 * cq + (e & 1);
-                z[nt][e] = t < lim[e >> 1] ? z[nt][e] * kPromptScale : -INFINITY;
-                mt[e >> 1] = fmaxf(mt[e >> 1], z[nt][e]);
+                            for (int k = 0; k < 8; ++k)
+                                tc_mma_ts(tmem + kPmColO + t * 128, tmem + kPmColS + t * 128 + k * 8,
+                                          desc_mn(vb + k * 2048), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
+                            if (j + 1 == e) tc_commit(&sb->o_full[t]);
+                        }
+                        if (j + 1 < e) {
+                            if (!have_k) {
+                                if (!wait(&sb->full[kt % kPmStages], (kt / kPmStages) & 1u)) { ok = false; break; }
+                                have_k = true;
+                            }
+                            qk(t, kt);
+                        }
+                    }
+                    if (!ok) break;
+                    tc_commit(&sb->empty[vt % kPmStages]);
+                    if (more) tc_commit(&sb->empty[kt % kPmStages]);
+                    if (j + 2 == z.steps) tc_commit(&sb->q_empty);
+                    it += 2;
+                }
+                if (!ok) break;
             }
-        float al[2], mu[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], 1));
-            mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], 2));
-            const float mn = fmaxf(mx[e], mt[e]);
-            mu[e] = mn == -INFINITY ? 0.0f : mn;
-            al[e] = pm_ex2(mx[e] - mu[e]);
-            mx[e] = mn;
-            sum[e] *= al[e];
+            // the ring's last releases have no reader: wait for every product before the CTA ends
+            tc_commit(&sb->drain);
+            for (uint32_t i = 0; i < (1u << 24) && !mbar_try_wait(&sb->drain, 0); ++i) {}
         }
+        __syncwarp();
+    } else {
+        // ======================================== softmax: tile t, this thread's row
+        const int t = warp >> 2;
+        const int32_t row = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + kPmColS + t * 128, to = tmem + lanes + kPmColO + t * 128;
+        const int32_t rtok = t * (U / 2) + row / G, rhead = row % G;
+        uint32_t ns = 0, no = 0;  // S tiles and O tiles taken
+        bool ok = true;
+        for (bool first = true; ok && before(pos, end); next_unit(a, U, pos, s), first = false) {
+            const PromptPiece z = piece_of(s, pos, end, U);
+            const int32_t e = t ? z.e1 : z.e0, tok = pos.i * U + rtok;
+            const bool has_row = tok < s.n;
+            const int32_t lim = has_row ? max(0, s.m - s.n + tok + 1) : 0;  // keys the row sees
+            float m = -INFINITY, l = 0.0f;
+            for (int32_t j = 0; j < e; ++j) {
+                if (!pm_wait(&sb->s_full[t], ns & 1u, sb, a.hdr, 0xffffffffu)) { ok = false; break; }
+                ++ns;
+                tc_fence_after();
+                uint32_t x[128];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+                for (int c = 0; c < 4; ++c) tc_ld32(ts + 32 * c, x + 32 * c);
+                tc_wait_ld();
+                const int32_t left = lim - (pos.j + j) * kPmTile;  // columns of this tile the row sees
+                if (__any_sync(0xffffffffu, left < kPmTile)) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] *= al[e >> 1];
-        uint32_t p[8][2];
+                    for (int c = 0; c < 128; ++c)
+                        if (c >= left) x[c] = 0xff800000u;  // -inf
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
+                for (int c = 0; c < 128; c += 8)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float x = pm_ex2(z[nt][2 * e] - mu[e]), y = pm_ex2(z[nt][2 * e + 1] - mu[e]);
-                const __nv_bfloat162 w = __floats2bfloat162_rn(x, y);
-                p[nt][e] = *reinterpret_cast<const uint32_t *>(&w);
-                sum[e] += x + y;
+                    for (int i = 0; i < 4; ++i)
+                        mx[i] = max3(mx[i], __uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const bool need = top > m + kPmLazy;
+                if (__any_sync(0xffffffffu, need)) {
+                    float alpha = 1.0f;
+                    if (need) {
+                        alpha = pm_ex2((m - top) * kPmScale);  // 0 from -inf
+                        m = top;
+                        l *= alpha;
+                    }
+                    if (j > 0) {  // O holds the earlier key tiles, complete before this S was
+                        const uint64_t al = pack2(alpha, alpha);
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[32];
+                            tc_ld32(to + 32 * c, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                float lo, hi;
+                                unpack2(mul2(pack2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), al), lo, hi);
+                                o[i] = __float_as_uint(lo);
+                                o[i + 1] = __float_as_uint(hi);
+                            }
+                            tc_st32(to + 32 * c, o);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.0f : -m * kPmScale;
+                const uint64_t sc2 = pack2(kPmScale, kPmScale), ref2 = pack2(ref, ref);
+                uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                for (int c = 0; c < 128; c += 2) {
+                    float lo, hi;
+                    unpack2(fma2(pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, ref2), lo, hi);
+                    lo = pm_ex2(lo);
+                    hi = pm_ex2(hi);
+                    sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(lo, hi));
+                    x[c >> 1] = pm_pack_bf16(lo, hi);
+                }
+                tc_st32(ts, x);
+                tc_st32(ts + 32, x + 32);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sb->p_ready[t]);
+                float lo, hi;
+                unpack2(add2(sum[0], sum[1]), lo, hi);
+                l += lo + hi;
             }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t pa[4] = {p[2 * k][0], p[2 * k][1], p[2 * k + 1][0], p[2 * k + 1][1]};
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int row = 16 * k + 2 * cq, d = 8 * i + r;
-                const uint32_t b0 = (uint32_t)sv[row][d] | ((uint32_t)sv[row + 1][d] << 16);
-                const uint32_t b1 = (uint32_t)sv[row + 8][d] | ((uint32_t)sv[row + 9][d] << 16);
-                pm_mma(o[i], pa, b0, b1);
+            if (!ok) break;
+            // ---- the piece's end: the rows, or their part for the merge
+            const bool partial = pos.j > 0 || (same_unit(pos, end) && end.j > 0);
+            if (e > 0) {
+                if (!pm_wait(&sb->o_full[t], no & 1u, sb, a.hdr, 0xffffffffu)) break;
+                ++no;
+                tc_fence_after();
             }
+            if (partial) {
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (first ? 0 : 1);
+                const int64_t prow = slot * kPmRows + t * kPmTile + row;
+                if (has_row) __stcg(a.ml + prow, make_float2(m, l));
+                if (e > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tc_ld32(to + 32 * c, o);
+                        tc_wait_ld();
+                        if (has_row) {
+                            float4 *dst = reinterpret_cast<float4 *>(a.part + prow * kD + 32 * c);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                __stcg(dst + i, make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                            __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3])));
+                        }
+                    }
+                }
+            } else {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                uint4 *dst = reinterpret_cast<uint4 *>(
+                    a.out + ((int64_t)(s.q0 + tok) * a.Hq + pos.h * G + rhead) * kD);
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    if (e > 0) {
+                        tc_ld32(to + 32 * c, o);
+                        tc_wait_ld();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                        if (e > 0 && lim > 0) {
+                            w.x = pm_pack_bf16(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
+                            w.y = pm_pack_bf16(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
+                            w.z = pm_pack_bf16(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
+                            w.w = pm_pack_bf16(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
+                        }
+                        if (has_row) dst[4 * c + i] = w;
+                    }
+                }
+            }
+            tc_fence_before();  // the reads of O above come before the next piece's first product
         }
     }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
-        sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
-        if (tok[e] < 0) continue;
-        const float inv = sum[e] > 0.0f ? 1.0f / sum[e] : 0.0f;
-        uint16_t *orow = a.out + ((int64_t)(s.q0 + tok[e]) * a.Hq + hd[e]) * kD;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat162 w = __floats2bfloat162_rn(o[i][2 * e] * inv, o[i][2 * e + 1] * inv);
-            *reinterpret_cast<__nv_bfloat162 *>(orow + 8 * i + 2 * cq) = w;
-        }
+    __syncthreads();
+    if (warp == kPmMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
 }
+
+// Merge of the units cut between CTAs: block (c, part) folds 32 rows of the unit whose first part is
+// CTA c's last piece, in CTA order: a warp takes a row at a time, four columns per lane.
+constexpr int kPmMergeParts = 8, kPmMergeWarps = 4;
+
+__global__ void __launch_bounds__(kPmMergeWarps * 32) prompt_merge_kernel(const PromptArgs a, int32_t ctas)
+{
+    pdl_wait_primary();
+    const int4 head = __ldcg(a.head + blockIdx.x);
+    if (head.x == 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t G = a.G, U = kPmRows / G;
+    const PromptSeq s = prompt_seq(a, head.y, false);
+    const int64_t first = 2 * (int64_t)blockIdx.x + (head.x - 1);
+    constexpr int kRows = kPmRows / kPmMergeParts / kPmMergeWarps;
+    for (int i = 0; i < kRows; ++i) {
+        const int32_t row = blockIdx.y * (kPmRows / kPmMergeParts) + i * kPmMergeWarps + warp;
+        const int32_t tok = head.w * U + row / G;
+        if (tok >= s.n) continue;
+        float M = -INFINITY, L = 0.0f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        int64_t slot = first;
+        for (int32_t c = blockIdx.x;;) {
+            const int64_t p = slot * kPmRows + row;
+            const float2 ml = __ldcg(a.ml + p);
+            const float4 o = __ldcg(reinterpret_cast<const float4 *>(a.part + p * kD) + lane);
+            const float Mn = fmaxf(M, ml.x);
+            if (ml.x != -INFINITY) {  // (a part whose keys the row does not see wrote no O)
+                const float fo = M == -INFINITY ? 0.0f : pm_ex2((M - Mn) * kPmScale), fn = pm_ex2((ml.x - Mn) * kPmScale);
+                L = L * fo + ml.y * fn;
+                O.x = O.x * fo + o.x * fn;
+                O.y = O.y * fo + o.y * fn;
+                O.z = O.z * fo + o.z * fn;
+                O.w = O.w * fo + o.w * fn;
+                M = Mn;
+            }
+            int32_t flag = 0;
+            while (++c < ctas && (flag = __ldcg(a.cont + c)) == 0) {}  // CTAs without a piece
+            if (c >= ctas) break;
+            slot = 2 * (int64_t)c;
+            if (flag == 2) {  // the unit's last part
+                const int64_t pl = slot * kPmRows + row;
+                const float2 e = __ldcg(a.ml + pl);
+                const float4 oe = __ldcg(reinterpret_cast<const float4 *>(a.part + pl * kD) + lane);
+                if (e.x != -INFINITY) {
+                    const float Me = fmaxf(M, e.x);
+                    const float fo = M == -INFINITY ? 0.0f : pm_ex2((M - Me) * kPmScale), fn = pm_ex2((e.x - Me) * kPmScale);
+                    L = L * fo + e.y * fn;
+                    O.x = O.x * fo + oe.x * fn;
+                    O.y = O.y * fo + oe.y * fn;
+                    O.z = O.z * fo + oe.z * fn;
+                    O.w = O.w * fo + oe.w * fn;
+                }
+                break;
+            }
+        }
+        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        uint2 w;
+        w.x = pm_pack_bf16(O.x * inv, O.y * inv);
+        w.y = pm_pack_bf16(O.z * inv, O.w * inv);
+        reinterpret_cast<uint2 *>(a.out + ((int64_t)(s.q0 + tok) * a.Hq + head.z * G + row % G) * kD)[lane] = w;
+    }
+}
+
+// ---- host -------------------------------------------------------------------------------------------
+
+namespace {
+struct PromptLayout {
+    size_t off_head, off_cont, off_ml, off_part, total;
+};
+PromptLayout prompt_layout(int nsm)
+{
+    PromptLayout l;
+    size_t off = sizeof(WsHeader);
+    l.off_head = off;
+    off = (off + (size_t)nsm * sizeof(int4) + 255) & ~size_t(255);
+    l.off_cont = off;
+    off = (off + (size_t)nsm * sizeof(int32_t) + 255) & ~size_t(255);
+    l.off_ml = off;
+    off += (size_t)nsm * 2 * kPmRows * sizeof(float2);
+    l.off_part = off;
+    off += (size_t)nsm * 2 * kPmRows * kD * sizeof(float);
+    l.total = off;
+    return l;
+}
+}  // namespace
 
 size_t prompt_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int nsm)
 {
     (void)B;
     (void)Hq;
     (void)Hkv;
-    (void)nsm;
-    return sizeof(WsHeader);
+    return prompt_layout(nsm).total;
 }
 
 cudaError_t launch_prompt(const void *q, const void *k, const void *v, int32_t total_q, int32_t total_kv,
@@ -229,30 +900,92 @@ cudaError_t launch_prompt(const void *q, const void *k, const void *v, int32_t t
                           int32_t num_blocks, int32_t B, int32_t Hq, int32_t Hkv, void *out, void *ws, int nsm,
                           bool *map_failed, cudaStream_t stream)
 {
+    *map_failed = true;
+    const int32_t G = Hq / Hkv;
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    PromptMaps maps;
+    {
+        // a tile's rows as two halves of 64 columns: (column, head, token, half) for Q, (column, token,
+        // head, half) for packed K and V; (column, row) of one half of a page for the paged cache
+        const cuuint32_t one[4] = {1, 1, 1, 1};
+        const cuuint64_t qd[4] = {64, (cuuint64_t)Hq, (cuuint64_t)total_q, 2};
+        const cuuint64_t qs[3] = {256, (cuuint64_t)Hq * 256, 128};
+        const cuuint32_t qb[4] = {64, (cuuint32_t)G, (cuuint32_t)(kPmTile / G), 2};
+        if (enc(&maps.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), qd, qs, qb, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+        const void *src[2] = {k, v};
+        CUtensorMap *dst[2] = {&maps.k, &maps.v};
+        for (int i = 0; i < 2; ++i) {
+            CUresult r;
+            if (bt) {
+                const cuuint64_t d[2] = {kD, (cuuint64_t)num_blocks * Hkv * bs};
+                const cuuint64_t st[1] = {256};
+                const cuuint32_t box[2] = {64, (cuuint32_t)bs};
+                r = enc(dst[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(src[i]), d, st, box, one,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+            } else {
+                // no keys at all: a map of one row that no copy reads
+                const cuuint64_t d[4] = {64, (cuuint64_t)(total_kv > 0 ? total_kv : 1), (cuuint64_t)Hkv, 2};
+                const cuuint64_t st[3] = {(cuuint64_t)Hkv * 256, 256, 128};
+                const cuuint32_t box[4] = {64, kPmTile, 1, 2};
+                r = enc(dst[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(total_kv > 0 ? src[i] : q), d, st,
+                        box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+            }
+            if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+        }
+    }
     *map_failed = false;
-    (void)nsm;
+
+    const PromptLayout l = prompt_layout(nsm);
+    char *base = static_cast<char *>(ws);
     PromptArgs a;
-    a.q = static_cast<const uint16_t *>(q);
-    a.k = static_cast<const uint16_t *>(k);
-    a.v = static_cast<const uint16_t *>(v);
     a.out = static_cast<uint16_t *>(out);
     a.cu_q = cu_q;
     a.kv = kv;
     a.bt = bt;
-    a.hdr = static_cast<WsHeader *>(ws);
+    a.hdr = reinterpret_cast<WsHeader *>(base);
+    a.head = reinterpret_cast<int4 *>(base + l.off_head);
+    a.cont = reinterpret_cast<int32_t *>(base + l.off_cont);
+    a.ml = reinterpret_cast<float2 *>(base + l.off_ml);
+    a.part = reinterpret_cast<float *>(base + l.off_part);
     a.B = B;
     a.Hq = Hq;
     a.Hkv = Hkv;
-    a.G = Hq / Hkv;
+    a.G = G;
     a.total_q = total_q;
     a.total_kv = total_kv;
     a.bs = bs;
     a.max_blocks = max_blocks;
     a.num_blocks = num_blocks;
-    const int32_t tok_per = kPmRows / a.G;
-    const int32_t units = total_q / tok_per + B;  // upper bound: every request rounds up once
-    prompt_simple_kernel<<<dim3((unsigned)units, (unsigned)Hkv), 128, 0, stream>>>(a);
-    return cudaGetLastError();
+
+    static thread_local int limit_dev = -1;  // the shared-memory limit is raised once per device and host thread
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev != limit_dev) {
+        e = cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPmSmem);
+        if (e != cudaSuccess) return e;
+        limit_dev = dev;
+    }
+    prompt_kernel<<<(unsigned)nsm, kPmThreads, kPmSmem, stream>>>(a, maps);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)nsm, kPmMergeParts);
+    cfg.blockDim = dim3(kPmMergeWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prompt_merge_kernel, a, (int32_t)nsm);
 }
 
 }  // namespace dgq
