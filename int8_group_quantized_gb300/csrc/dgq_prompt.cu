@@ -45,7 +45,11 @@ constexpr int kPmTile = 128;                      // rows of a tile, keys of a k
 constexpr int kPmStages = 5;
 constexpr int kPmTileBytes = kPmTile * kD * 2;    // 32 KB: two halves of 64 columns, [row][64] each
 constexpr int kPmHalf = kPmTileBytes / 2;
-constexpr int kPmThreads = 320;
+constexpr int kPmThreads = 384;  // two softmax warpgroups; a third of which two warps work
+// Registers a thread after the split (multiples of 8): the softmax holds a row of 128 scores.  The
+// three warpgroups together take what the CTA was launched with (384 threads of 168).
+constexpr int kPmRegsSoftmax = 216, kPmRegsOther = 72;
+static_assert(2 * kPmRegsSoftmax + kPmRegsOther <= 3 * 168, "the split stays inside the launch's registers");
 constexpr int kPmLoadWarp = 8, kPmMmaWarp = 9;
 constexpr int kPmUnitCost = 2 * kPmTile;          // a unit's fixed cost, in keys
 constexpr int kPmSnap = 4;                        // key tiles: no part of a cut unit is smaller
@@ -486,6 +490,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
     PromptPos pos = begin;
     PromptSeq s = prompt_seq(a, pos.b, false);
 
+    if (warp >= kPmLoadWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPmRegsOther));
     if (warp == kPmLoadWarp) {
         // ======================================== loads
         fence_proxy_async_smem();  // the prefix was read from the ring by ordinary loads
@@ -656,7 +662,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             for (uint32_t i = 0; i < (1u << 24) && !mbar_try_wait(&sb->drain, 0); ++i) {}
         }
         __syncwarp();
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPmRegsSoftmax));
         // ======================================== softmax: tile t, this thread's row
         const int t = warp >> 2;
         const int32_t row = tid & 127;
