@@ -45,11 +45,7 @@ constexpr int kPmTile = 128;                      // rows of a tile, keys of a k
 constexpr int kPmStages = 5;
 constexpr int kPmTileBytes = kPmTile * kD * 2;    // 32 KB: two halves of 64 columns, [row][64] each
 constexpr int kPmHalf = kPmTileBytes / 2;
-constexpr int kPmThreads = 384;  // two softmax warpgroups; a third of which two warps work
-// Registers a thread after the split (multiples of 8): the softmax holds a row of 128 scores.  The
-// three warpgroups together take what the CTA was launched with (384 threads of 168).
-constexpr int kPmRegsSoftmax = 216, kPmRegsOther = 72;
-static_assert(2 * kPmRegsSoftmax + kPmRegsOther <= 3 * 168, "the split stays inside the launch's registers");
+constexpr int kPmThreads = 320;  // two softmax warpgroups, a load warp, a product warp
 constexpr int kPmLoadWarp = 8, kPmMmaWarp = 9;
 constexpr int kPmUnitCost = 2 * kPmTile;          // a unit's fixed cost, in keys
 constexpr int kPmSnap = 4;                        // key tiles: no part of a cut unit is smaller
@@ -224,40 +220,46 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r)
         : "memory");
 }
 
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 // D (fp32, 128 x 128) (+)= A B, 16 deep, bf16 operands; B n-by-k (K-major) in shared memory.
 constexpr uint32_t kIdescQK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 // the same with B k-by-n as it lies (MN-major: bit 16)
 constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
 
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc)
+// Shared-memory operand descriptors of a pair of [128][64] halves under the 128-byte swizzle: address
+// and strides in units of 16 bytes, version 1 (bit 46), swizzle mode 2 (bit 61); 8-row groups 1024
+// bytes apart.  Only the low word differs between operands: the address and the other stride, which
+// K-major operands do not use and MN-major ones take as the distance of their 64-column atoms.
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr) { return (addr >> 4) | ((uint32_t)(kPmHalf >> 4) << 16); }
+
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(idesc), "r"(acc), "r"(kDescHi)
         : "memory");
 }
 
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t atmem, uint64_t bdesc, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t atmem, uint32_t blo, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(atmem), "l"(bdesc), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(atmem), "r"(blo), "r"(idesc), "r"(acc), "r"(kDescHi)
         : "memory");
-}
-
-// Shared-memory operand descriptors of a [128][64] half tile pair under the 128-byte swizzle: address
-// and strides in units of 16 bytes, version 1 (bit 46), swizzle mode 2 (bit 61).
-// K-major: 8-row groups 1024 bytes apart (the leading stride is not used).
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr)
-{
-    return (uint64_t)(addr >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-// MN-major: 64-column atoms kPmHalf apart, 8-key groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr)
-{
-    return (uint64_t)(addr >> 4) | ((uint64_t)(kPmHalf >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
 __device__ __forceinline__ void tma_tile_4d(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
@@ -490,14 +492,12 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
     PromptPos pos = begin;
     PromptSeq s = prompt_seq(a, pos.b, false);
 
-    if (warp >= kPmLoadWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPmRegsOther));
     if (warp == kPmLoadWarp) {
         // ======================================== loads
         fence_proxy_async_smem();  // the prefix was read from the ring by ordinary loads
         const int32_t pages = a.bt ? kPmTile / a.bs : 0;  // pages of a key tile
         uint32_t it = 0, nv = 0;
-        uint32_t nq[2] = {0, 0};  // Q tiles loaded
+        uint32_t nq0 = 0, nq1 = 0;  // Q tiles loaded
         bool ok = true, v_flight = false;
         uint32_t q_loaded = 0;  // pieces with a Q load
         for (; ok && before(pos, end); next_unit(a, U, pos, s)) {
@@ -508,12 +508,12 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             if (lane == 0) {
                 const int32_t tok = s.q0 + pos.i * U;
                 if (z.e0 > 0) {
-                    ++nq[0];
+                    ++nq0;
                     mbar_arrive_expect_tx(&sb->q_full[0], kPmTileBytes);
                     tma_tile_4d(sq, &maps.q, 0, pos.h * G, tok, 0, &sb->q_full[0]);
                 }
                 if (z.e1 > 0) {
-                    ++nq[1];
+                    ++nq1;
                     mbar_arrive_expect_tx(&sb->q_full[1], kPmTileBytes);
                     tma_tile_4d(sq + kPmTileBytes, &maps.q, 0, pos.h * G, tok + U / 2, 0, &sb->q_full[1]);
                 }
@@ -586,8 +586,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             };
             for (uint32_t k = it > kPmStages ? it - kPmStages : 0; k < it; ++k)
                 drain(&sb->full[k % kPmStages], (k / kPmStages) & 1u);
-            for (int t = 0; t < 2; ++t)
-                if (nq[t] > 0) drain(&sb->q_full[t], (nq[t] - 1) & 1u);
+            if (nq0 > 0) drain(&sb->q_full[0], (nq0 - 1) & 1u);
+            if (nq1 > 0) drain(&sb->q_full[1], (nq1 - 1) & 1u);
             if (v_flight) drain(&sb->v_part, nv & 1u);
         }
         __syncwarp();
@@ -595,8 +595,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         // ======================================== products, one thread
         if (lane == 0) {
             uint32_t it = 0;                    // ring position
-            uint32_t nq[2] = {0, 0};            // Q tiles taken
-            uint32_t npr[2] = {0, 0};           // P tiles taken
+            uint32_t qpar = 0, ppar = 0;        // bit t: parity of the next Q and P tile of tile t
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t parity) { return pm_wait(bar, parity, sb, a.hdr, 1u); };
             for (; ok && before(pos, end); next_unit(a, U, pos, s)) {
@@ -614,10 +613,11 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 };
                 // first key tile
                 if (!wait(&sb->full[it % kPmStages], (it / kPmStages) & 1u)) break;
+#pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
                     if ((t ? z.e1 : z.e0) == 0) continue;
-                    if (!wait(&sb->q_full[t], nq[t] & 1u)) { ok = false; break; }
-                    ++nq[t];
+                    if (!wait(&sb->q_full[t], (qpar >> t) & 1u)) { ok = false; break; }
+                    qpar ^= 1u << t;
                     qk(t, it);
                 }
                 if (!ok) break;
@@ -628,11 +628,12 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                     const bool more = j + 1 < z.steps;
                     if (!wait(&sb->full[vt % kPmStages], (vt / kPmStages) & 1u)) { ok = false; break; }
                     bool have_k = false;
+#pragma unroll 1
                     for (int t = 0; t < 2; ++t) {
                         const int32_t e = t ? z.e1 : z.e0;
                         if (j < e) {
-                            if (!wait(&sb->p_ready[t], npr[t] & 1u)) { ok = false; break; }
-                            ++npr[t];
+                            if (!wait(&sb->p_ready[t], (ppar >> t) & 1u)) { ok = false; break; }
+                            ppar ^= 1u << t;
                             tc_fence_after();
                             const uint32_t vb = sring + (vt % kPmStages) * kPmTileBytes;
 #pragma unroll
@@ -662,9 +663,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             for (uint32_t i = 0; i < (1u << 24) && !mbar_try_wait(&sb->drain, 0); ++i) {}
         }
         __syncwarp();
-    }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPmRegsSoftmax));
         // ======================================== softmax: tile t, this thread's row
         const int t = warp >> 2;
         const int32_t row = tid & 127;
@@ -683,63 +682,87 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 if (!pm_wait(&sb->s_full[t], ns & 1u, sb, a.hdr, 0xffffffffu)) { ok = false; break; }
                 ++ns;
                 tc_fence_after();
-                uint32_t x[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tc_ld32(ts + 32 * c, x + 32 * c);
-                tc_wait_ld();
                 const int32_t left = lim - (pos.j + j) * kPmTile;  // columns of this tile the row sees
-                if (__any_sync(0xffffffffu, left < kPmTile)) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= left) x[c] = 0xff800000u;  // -inf
-                }
+                const bool cut = __any_sync(0xffffffffu, left < kPmTile);
+                // the row's maximum; the first 64 scores stay in registers, the others are read again
+                // below (in tensor memory P overwrites the first 64 columns only)
+                uint32_t x[64], y[32];
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto hide = [&](uint32_t *v, int c0, int n) {
 #pragma unroll
-                for (int c = 0; c < 128; c += 8)
+                    for (int c = 0; c < n; ++c)
+                        if (c0 + c >= left) v[c] = 0xff800000u;  // -inf
+                };
+                auto maxima = [&](const uint32_t *v, int n) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mx[i] = max3(mx[i], __uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1]));
+                    for (int c = 0; c < n; c += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mx[i] = max3(mx[i], __uint_as_float(v[c + 2 * i]), __uint_as_float(v[c + 2 * i + 1]));
+                };
+                tc_ld32(ts, x);
+                tc_ld32(ts + 32, x + 32);
+                tc_wait_ld();
+                tc_ld32(ts + 64, y);
+                if (cut) hide(x, 0, 64);
+                maxima(x, 64);
+                tc_wait_ld();
+                if (cut) hide(y, 64, 32);
+                maxima(y, 32);
+                tc_ld32(ts + 96, y);
+                tc_wait_ld();
+                if (cut) hide(y, 96, 32);
+                maxima(y, 32);
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const bool need = top > m + kPmLazy;
-                if (__any_sync(0xffffffffu, need)) {
-                    float alpha = 1.0f;
-                    if (need) {
-                        alpha = pm_ex2((m - top) * kPmScale);  // 0 from -inf
-                        m = top;
-                        l *= alpha;
-                    }
-                    if (j > 0) {  // O holds the earlier key tiles, complete before this S was
-                        const uint64_t al = pack2(alpha, alpha);
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t o[32];
-                            tc_ld32(to + 32 * c, o);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float lo, hi;
-                                unpack2(mul2(pack2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), al), lo, hi);
-                                o[i] = __float_as_uint(lo);
-                                o[i + 1] = __float_as_uint(hi);
-                            }
-                            tc_st32(to + 32 * c, o);
-                        }
-                    }
+                float alpha = 1.0f;
+                if (need) {
+                    alpha = pm_ex2((m - top) * kPmScale);  // 0 from -inf
+                    m = top;
+                    l *= alpha;
                 }
                 const float ref = m == -INFINITY ? 0.0f : -m * kPmScale;
                 const uint64_t sc2 = pack2(kPmScale, kPmScale), ref2 = pack2(ref, ref);
                 uint64_t sum[2] = {0ull, 0ull};
+                auto weights = [&](const uint32_t *v, int c) {
+                    uint32_t p[16];
 #pragma unroll
-                for (int c = 0; c < 128; c += 2) {
-                    float lo, hi;
-                    unpack2(fma2(pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, ref2), lo, hi);
-                    lo = pm_ex2(lo);
-                    hi = pm_ex2(hi);
-                    sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(lo, hi));
-                    x[c >> 1] = pm_pack_bf16(lo, hi);
+                    for (int i = 0; i < 32; i += 2) {
+                        float lo, hi;
+                        unpack2(fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, ref2), lo, hi);
+                        lo = pm_ex2(lo);
+                        hi = pm_ex2(hi);
+                        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(lo, hi));
+                        p[i >> 1] = pm_pack_bf16(lo, hi);
+                    }
+                    tc_st16(ts + c / 2, p);
+                };
+                // (y still holds columns 96 .. 127)
+                weights(y, 96);
+                tc_ld32(ts + 64, y);
+                weights(x, 0);
+                weights(x + 32, 32);
+                tc_wait_ld();
+                if (cut) hide(y, 64, 32);
+                weights(y, 64);
+                if (j > 0 && __any_sync(0xffffffffu, need)) {
+                    // O holds the earlier key tiles, complete before this S was
+                    const uint64_t al = pack2(alpha, alpha);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tc_ld32(to + 32 * c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float lo, hi;
+                            unpack2(mul2(pack2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), al), lo, hi);
+                            o[i] = __float_as_uint(lo);
+                            o[i + 1] = __float_as_uint(hi);
+                        }
+                        tc_st32(to + 32 * c, o);
+                    }
                 }
-                tc_st32(ts, x);
-                tc_st32(ts + 32, x + 32);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
