@@ -281,6 +281,14 @@ __device__ __forceinline__ void tma_tile_2d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// True in one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ---- small arithmetic -----------------------------------------------------------------------------
 
 __device__ __forceinline__ float pm_ex2(float x)
@@ -592,76 +600,93 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         }
         __syncwarp();
     } else if (warp == kPmMmaWarp) {
-        // ======================================== products, one thread
-        if (lane == 0) {
-            uint32_t it = 0;                    // ring position
-            uint32_t qpar = 0, ppar = 0;        // bit t: parity of the next Q and P tile of tile t
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) { return pm_wait(bar, parity, sb, a.hdr, 1u); };
-            for (; ok && before(pos, end); next_unit(a, U, pos, s)) {
-                const PromptPiece z = piece_of(s, pos, end, U);
-                if (z.steps == 0) continue;
-                // S of key tile k (its K tile at ring position kt) for tile t
-                auto qk = [&](int t, uint32_t kt) {
-                    const uint32_t qa = sq + t * kPmTileBytes, kb = sring + (kt % kPmStages) * kPmTileBytes;
+        // ======================================== products: the warp walks, one lane issues
+        // (operands go through a shuffle so that the compiler sees them uniform over the warp)
+        uint32_t it = 0;                // ring position
+        uint32_t qpar = 0, ppar = 0;    // bit t: parity of the next Q and P tile of tile t
+        bool ok = true;
+        const uint32_t d0 = __shfl_sync(0xffffffffu, tmem, 0);
+        auto wait = [&](uint64_t *bar, uint32_t parity) { return pm_wait(bar, parity, sb, a.hdr, 0xffffffffu); };
+        for (; ok && before(pos, end); next_unit(a, U, pos, s)) {
+            const PromptPiece z = piece_of(s, pos, end, U);
+            if (z.steps == 0) continue;
+            // S of a key tile (its K tile at ring position kt) for tile t
+            auto qk = [&](int t, uint32_t kt) {
+                const uint32_t qa = __shfl_sync(0xffffffffu, desc_k(sq + t * kPmTileBytes), 0);
+                const uint32_t kb = __shfl_sync(0xffffffffu, desc_k(sring + (kt % kPmStages) * kPmTileBytes), 0);
+                const uint32_t d = __shfl_sync(0xffffffffu, d0 + kPmColS + t * 128, 0);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const uint32_t o = (k >> 2) * kPmHalf + (k & 3) * 32;
-                        tc_mma_ss(tmem + kPmColS + t * 128, desc_k(qa + o), desc_k(kb + o), kIdescQK, k > 0);
+                        const uint32_t o = ((k >> 2) * kPmHalf + (k & 3) * 32) >> 4;
+                        tc_mma_ss(d, qa + o, kb + o, kIdescQK, k > 0);
                     }
                     tc_commit(&sb->s_full[t]);
-                };
-                // first key tile
-                if (!wait(&sb->full[it % kPmStages], (it / kPmStages) & 1u)) break;
+                }
+                __syncwarp();
+            };
+            auto pv = [&](int t, uint32_t vt, bool first, bool last) {
+                const uint32_t vb = __shfl_sync(0xffffffffu, desc_mn(sring + (vt % kPmStages) * kPmTileBytes), 0);
+                const uint32_t d = __shfl_sync(0xffffffffu, d0 + kPmColO + t * 128, 0);
+                const uint32_t p = __shfl_sync(0xffffffffu, d0 + kPmColS + t * 128, 0);
+                const uint32_t acc = __shfl_sync(0xffffffffu, first ? 0u : 1u, 0);
+                if (elect_one()) {
+                    tc_mma_ts(d, p, vb, kIdescPV, acc);
+#pragma unroll
+                    for (int k = 1; k < 8; ++k) tc_mma_ts(d, p + k * 8, vb + k * (2048 >> 4), kIdescPV, 1u);
+                    if (last) tc_commit(&sb->o_full[t]);
+                }
+                __syncwarp();
+            };
+            auto release = [&](uint64_t *bar) {  // arrives once every product issued so far is done
+                if (elect_one()) tc_commit(bar);
+                __syncwarp();
+            };
+            // first key tile
+            if (!wait(&sb->full[it % kPmStages], (it / kPmStages) & 1u)) break;
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+                if ((t ? z.e1 : z.e0) == 0) continue;
+                if (!wait(&sb->q_full[t], (qpar >> t) & 1u)) { ok = false; break; }
+                qpar ^= 1u << t;
+                qk(t, it);
+            }
+            if (!ok) break;
+            release(&sb->empty[it % kPmStages]);
+            if (z.steps == 1) release(&sb->q_empty);
+            for (int32_t j = 0; ok && j < z.steps; ++j) {
+                const uint32_t vt = it + 1, kt = it + 2;  // V of this key tile, K of the next
+                const bool more = j + 1 < z.steps;
+                if (!wait(&sb->full[vt % kPmStages], (vt / kPmStages) & 1u)) { ok = false; break; }
+                bool have_k = false;
 #pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
-                    if ((t ? z.e1 : z.e0) == 0) continue;
-                    if (!wait(&sb->q_full[t], (qpar >> t) & 1u)) { ok = false; break; }
-                    qpar ^= 1u << t;
-                    qk(t, it);
-                }
-                if (!ok) break;
-                tc_commit(&sb->empty[it % kPmStages]);
-                if (z.steps == 1) tc_commit(&sb->q_empty);
-                for (int32_t j = 0; ok && j < z.steps; ++j) {
-                    const uint32_t vt = it + 1, kt = it + 2;  // V of this key tile, K of the next
-                    const bool more = j + 1 < z.steps;
-                    if (!wait(&sb->full[vt % kPmStages], (vt / kPmStages) & 1u)) { ok = false; break; }
-                    bool have_k = false;
-#pragma unroll 1
-                    for (int t = 0; t < 2; ++t) {
-                        const int32_t e = t ? z.e1 : z.e0;
-                        if (j < e) {
-                            if (!wait(&sb->p_ready[t], (ppar >> t) & 1u)) { ok = false; break; }
-                            ppar ^= 1u << t;
-                            tc_fence_after();
-                            const uint32_t vb = sring + (vt % kPmStages) * kPmTileBytes;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                tc_mma_ts(tmem + kPmColO + t * 128, tmem + kPmColS + t * 128 + k * 8,
-                                          desc_mn(vb + k * 2048), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
-                            if (j + 1 == e) tc_commit(&sb->o_full[t]);
-                        }
-                        if (j + 1 < e) {
-                            if (!have_k) {
-                                if (!wait(&sb->full[kt % kPmStages], (kt / kPmStages) & 1u)) { ok = false; break; }
-                                have_k = true;
-                            }
-                            qk(t, kt);
-                        }
+                    const int32_t e = t ? z.e1 : z.e0;
+                    if (j < e) {
+                        if (!wait(&sb->p_ready[t], (ppar >> t) & 1u)) { ok = false; break; }
+                        ppar ^= 1u << t;
+                        tc_fence_after();
+                        pv(t, vt, j == 0, j + 1 == e);
                     }
-                    if (!ok) break;
-                    tc_commit(&sb->empty[vt % kPmStages]);
-                    if (more) tc_commit(&sb->empty[kt % kPmStages]);
-                    if (j + 2 == z.steps) tc_commit(&sb->q_empty);
-                    it += 2;
+                    if (j + 1 < e) {
+                        if (!have_k) {
+                            if (!wait(&sb->full[kt % kPmStages], (kt / kPmStages) & 1u)) { ok = false; break; }
+                            have_k = true;
+                        }
+                        qk(t, kt);
+                    }
                 }
                 if (!ok) break;
+                release(&sb->empty[vt % kPmStages]);
+                if (more) release(&sb->empty[kt % kPmStages]);
+                if (j + 2 == z.steps) release(&sb->q_empty);
+                it += 2;
             }
-            // the ring's last releases have no reader: wait for every product before the CTA ends
-            tc_commit(&sb->drain);
-            for (uint32_t i = 0; i < (1u << 24) && !mbar_try_wait(&sb->drain, 0); ++i) {}
         }
+        // the ring's last releases have no reader: wait for every product before the CTA ends
+        if (elect_one()) tc_commit(&sb->drain);
+        __syncwarp();
+        for (uint32_t i = 0; i < (1u << 24) && !mbar_try_wait(&sb->drain, 0); ++i) {}
         __syncwarp();
     } else {
         // ======================================== softmax: tile t, this thread's row
