@@ -357,28 +357,25 @@ static_assert(kPmSmem <= 232448, "shared memory of a CTA");
 static_assert((size_t)(kMaxCallBatch + 1) * 8 <= (size_t)kPmStages * kPmTileBytes, "the request prefix uses the ring");
 
 // Bounded wait, with one answer for all `mask` lanes.  False: the wait ran out, here or elsewhere.
+// (The clock is read once in 1024 polls only: a read takes as long as a short wait.)
 __device__ __forceinline__ bool pm_wait(uint64_t *bar, uint32_t parity, PromptBars *sb, WsHeader *hdr, uint32_t mask)
 {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!__all_sync(mask, ok)) {
-        unsigned long long t0, t;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-        for (uint32_t i = 1;; ++i) {
-            if (!ok) ok = mbar_try_wait(bar, parity);
-            if (__all_sync(mask, ok)) break;
-            if ((i & 63u) == 0) {
-                bool over = sb->abort != 0;
-                asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-                if (t - t0 > kPmWaitNs) {
-                    over = true;
-                    sb->abort = 1;
-                    record_error(hdr, kErrFullWait);
-                }
-                if (__any_sync(mask, over)) return false;
+    unsigned long long t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(mask, mbar_try_wait(bar, parity))) return true;
+        if ((i & 1023u) == 0) {
+            bool over = sb->abort != 0;
+            unsigned long long t;
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kPmWaitNs) {
+                over = true;
+                sb->abort = 1;
+                record_error(hdr, kErrFullWait);
             }
+            if (__any_sync(mask, over)) return false;
         }
     }
-    return true;
 }
 
 // A unit's tiles in the piece [j0, j1): per tile the key tiles to go through, and its keys.
