@@ -189,9 +189,9 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void tc_commit(uint64_t *bar)
+__device__ __forceinline__ void tc_commit(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                  : "memory");
 }
 
@@ -205,6 +205,15 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t *r)
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(addr));
 }
 
@@ -289,6 +298,34 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// Whether the phase of that parity is complete (1 or 0): after a short wait, and without waiting.
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ uint32_t bar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok;
+}
+
+// Offset of k-step k (16 columns) in a K-major operand, in descriptor units.
+__device__ __forceinline__ constexpr uint32_t kstep(int k) { return ((k >> 2) * kPmHalf + (k & 3) * 32) >> 4; }
+
 // ---- small arithmetic -----------------------------------------------------------------------------
 
 __device__ __forceinline__ float pm_ex2(float x)
@@ -344,7 +381,7 @@ __device__ __forceinline__ uint32_t pm_pack_bf16(float lo, float hi)
 
 struct PromptBars {
     uint64_t full[kPmStages], empty[kPmStages];
-    uint64_t q_full[2], s_full[2], p_ready[2], o_full[2];
+    uint64_t q_full[2], s_full[2], p_most[2], p_ready[2], o_full[2];
     uint64_t q_empty, v_part, drain;
     uint32_t tmem;
     volatile uint32_t abort;
@@ -358,11 +395,11 @@ static_assert((size_t)(kMaxCallBatch + 1) * 8 <= (size_t)kPmStages * kPmTileByte
 
 // Bounded wait, with one answer for all `mask` lanes.  False: the wait ran out, here or elsewhere.
 // (The clock is read once in 1024 polls only: a read takes as long as a short wait.)
-__device__ __forceinline__ bool pm_wait(uint64_t *bar, uint32_t parity, PromptBars *sb, WsHeader *hdr, uint32_t mask)
+__device__ __forceinline__ bool pm_wait(uint32_t bar, uint32_t parity, PromptBars *sb, WsHeader *hdr, uint32_t mask)
 {
     unsigned long long t0 = 0;
     for (uint32_t i = 1;; ++i) {
-        if (__all_sync(mask, mbar_try_wait(bar, parity))) return true;
+        if (__all_sync(mask, bar_try(bar, parity))) return true;
         if ((i & 1023u) == 0) {
             bool over = sb->abort != 0;
             unsigned long long t;
@@ -455,6 +492,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             for (int t = 0; t < 2; ++t) {
                 mbar_init(&sb->q_full[t], 1);
                 mbar_init(&sb->s_full[t], 1);
+                mbar_init(&sb->p_most[t], 4);
                 mbar_init(&sb->p_ready[t], 4);
                 mbar_init(&sb->o_full[t], 1);
             }
@@ -508,7 +546,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         for (; ok && before(pos, end); next_unit(a, U, pos, s)) {
             const PromptPiece z = piece_of(s, pos, end, U);
             if (z.steps == 0) continue;
-            if (q_loaded > 0 && !pm_wait(&sb->q_empty, (q_loaded - 1) & 1u, sb, a.hdr, 0xffffffffu)) break;
+            if (q_loaded > 0 && !pm_wait(smem_u32(&sb->q_empty), (q_loaded - 1) & 1u, sb, a.hdr, 0xffffffffu)) break;
             ++q_loaded;
             if (lane == 0) {
                 const int32_t tok = s.q0 + pos.i * U;
@@ -544,7 +582,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 const uint32_t bytes = a.bt ? (uint32_t)used * a.bs * kD * 2 : (uint32_t)kPmTileBytes;
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t st = it % kPmStages, dst = sring + st * kPmTileBytes;
-                    if (it >= kPmStages && !pm_wait(&sb->empty[st], (it / kPmStages - 1) & 1u, sb, a.hdr, 0xffffffffu)) {
+                    if (it >= kPmStages && !pm_wait(smem_u32(&sb->empty[st]), (it / kPmStages - 1) & 1u, sb, a.hdr, 0xffffffffu)) {
                         ok = false;
                         break;
                     }
@@ -564,7 +602,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                     }
                     v_flight = part;
                     if (part) {
-                        if (!pm_wait(&sb->v_part, nv & 1u, sb, a.hdr, 0xffffffffu)) {
+                        if (!pm_wait(smem_u32(&sb->v_part), nv & 1u, sb, a.hdr, 0xffffffffu)) {
                             ok = false;
                             break;
                         }
@@ -598,90 +636,128 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         __syncwarp();
     } else if (warp == kPmMmaWarp) {
         // ======================================== products: the warp walks, one lane issues
-        // (operands go through a shuffle so that the compiler sees them uniform over the warp)
-        uint32_t it = 0;                // ring position
+        // Two products fit into the tensor cores' queue, so whatever the warp does between the last
+        // product of a turn and the first of the next leaves them idle.  A turn is one tile's O += P V
+        // of key tile j and S = Q K^T of key tile j + 1; the barriers that the next turn needs are
+        // polled between this turn's products, and waited for only when a poll found them open.
+        // (Operands go through a shuffle so that the compiler sees them uniform over the warp.)
+        uint32_t st = 0, ph = 0;        // ring stage and parity of the next K tile
         uint32_t qpar = 0, ppar = 0;    // bit t: parity of the next Q and P tile of tile t
         bool ok = true;
-        const uint32_t d0 = __shfl_sync(0xffffffffu, tmem, 0);
-        auto wait = [&](uint64_t *bar, uint32_t parity) { return pm_wait(bar, parity, sb, a.hdr, 0xffffffffu); };
+        const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t q_desc = __shfl_sync(0xffffffffu, desc_k(sq), 0);
+        const uint32_t k_desc = desc_k(sring), v_desc = desc_mn(sring);
+        const uint32_t full0 = smem_u32(&sb->full[0]), empty0 = smem_u32(&sb->empty[0]);
+        auto wait = [&](uint32_t bar, uint32_t parity) { return pm_wait(bar, parity, sb, a.hdr, 0xffffffffu); };
+        auto wrap = [](uint32_t x) { return x >= kPmStages ? x - kPmStages : x; };
         for (; ok && before(pos, end); next_unit(a, U, pos, s)) {
             const PromptPiece z = piece_of(s, pos, end, U);
             if (z.steps == 0) continue;
-            // S of a key tile (its K tile at ring position kt) for tile t
-            auto qk = [&](int t, uint32_t kt) {
-                const uint32_t qa = __shfl_sync(0xffffffffu, desc_k(sq + t * kPmTileBytes), 0);
-                const uint32_t kb = __shfl_sync(0xffffffffu, desc_k(sring + (kt % kPmStages) * kPmTileBytes), 0);
-                const uint32_t d = __shfl_sync(0xffffffffu, d0 + kPmColS + t * 128, 0);
-                if (elect_one()) {
+            // S of the first key tile
+            if (!wait(full0 + 8 * st, ph)) break;
+            uint32_t kb = __shfl_sync(0xffffffffu, k_desc + st * (kPmTileBytes >> 4), 0);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t o = ((k >> 2) * kPmHalf + (k & 3) * 32) >> 4;
-                        tc_mma_ss(d, qa + o, kb + o, kIdescQK, k > 0);
-                    }
-                    tc_commit(&sb->s_full[t]);
-                }
-                __syncwarp();
-            };
-            auto pv = [&](int t, uint32_t vt, bool first, bool last) {
-                const uint32_t vb = __shfl_sync(0xffffffffu, desc_mn(sring + (vt % kPmStages) * kPmTileBytes), 0);
-                const uint32_t d = __shfl_sync(0xffffffffu, d0 + kPmColO + t * 128, 0);
-                const uint32_t p = __shfl_sync(0xffffffffu, d0 + kPmColS + t * 128, 0);
-                const uint32_t acc = __shfl_sync(0xffffffffu, first ? 0u : 1u, 0);
-                if (elect_one()) {
-                    tc_mma_ts(d, p, vb, kIdescPV, acc);
-#pragma unroll
-                    for (int k = 1; k < 8; ++k) tc_mma_ts(d, p + k * 8, vb + k * (2048 >> 4), kIdescPV, 1u);
-                    if (last) tc_commit(&sb->o_full[t]);
-                }
-                __syncwarp();
-            };
-            auto release = [&](uint64_t *bar) {  // arrives once every product issued so far is done
-                if (elect_one()) tc_commit(bar);
-                __syncwarp();
-            };
-            // first key tile
-            if (!wait(&sb->full[it % kPmStages], (it / kPmStages) & 1u)) break;
-#pragma unroll 1
             for (int t = 0; t < 2; ++t) {
                 if ((t ? z.e1 : z.e0) == 0) continue;
-                if (!wait(&sb->q_full[t], (qpar >> t) & 1u)) { ok = false; break; }
+                if (!wait(smem_u32(&sb->q_full[t]), (qpar >> t) & 1u)) { ok = false; break; }
                 qpar ^= 1u << t;
-                qk(t, it);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tc_mma_ss(base + kPmColS + t * 128, q_desc + t * (kPmTileBytes >> 4) + kstep(k), kb + kstep(k),
+                                  kIdescQK, k > 0);
+                    tc_commit(smem_u32(&sb->s_full[t]));
+                }
+                __syncwarp();
             }
             if (!ok) break;
-            release(&sb->empty[it % kPmStages]);
-            if (z.steps == 1) release(&sb->q_empty);
-            for (int32_t j = 0; ok && j < z.steps; ++j) {
-                const uint32_t vt = it + 1, kt = it + 2;  // V of this key tile, K of the next
+            if (elect_one()) {
+                tc_commit(empty0 + 8 * st);
+                if (z.steps == 1) tc_commit(smem_u32(&sb->q_empty));
+            }
+            __syncwarp();
+            // stage and parity of V of key tile j, and of K of the next
+            uint32_t sv = wrap(st + 1), sk = wrap(st + 2);
+            uint32_t hv = ph ^ (sv < st), hk = ph ^ (sk < st);
+            uint32_t vb = __shfl_sync(0xffffffffu, v_desc + sv * (kPmTileBytes >> 4), 0);
+            kb = __shfl_sync(0xffffffffu, k_desc + sk * (kPmTileBytes >> 4), 0);
+            uint32_t got = 0;  // bit 0: V and K of the next step are known to be there, bit 1 + t: P of tile t
+            for (int32_t j = 0; j < z.steps; ++j) {
                 const bool more = j + 1 < z.steps;
-                if (!wait(&sb->full[vt % kPmStages], (vt / kPmStages) & 1u)) { ok = false; break; }
-                bool have_k = false;
-#pragma unroll 1
+                if (!(got & 1u) && (!wait(full0 + 8 * sv, hv) || (more && !wait(full0 + 8 * sk, hk)))) { ok = false; break; }
+                const uint32_t acc = __shfl_sync(0xffffffffu, j > 0 ? 1u : 0u, 0);
+                uint32_t vn = 0, kn = 0;
+#pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const int32_t e = t ? z.e1 : z.e0;
-                    if (j < e) {
-                        if (!wait(&sb->p_ready[t], (ppar >> t) & 1u)) { ok = false; break; }
-                        ppar ^= 1u << t;
-                        tc_fence_after();
-                        pv(t, vt, j == 0, j + 1 == e);
-                    }
-                    if (j + 1 < e) {
-                        if (!have_k) {
-                            if (!wait(&sb->full[kt % kPmStages], (kt / kPmStages) & 1u)) { ok = false; break; }
-                            have_k = true;
+                    if (j >= e) continue;
+                    const uint32_t pbar = smem_u32(&sb->p_ready[t]), par = (ppar >> t) & 1u;
+                    if (!(got & (2u << t)) && !wait(smem_u32(&sb->p_most[t]), par)) { ok = false; break; }
+                    tc_fence_after();
+                    uint32_t g = 0;
+                    if (elect_one()) {
+                        // keys 96 .. 127 and 0 .. 63, then 64 .. 95, as the softmax stores them
+#pragma unroll
+                        for (int i = 0; i < 6; ++i) {
+                            const int k = (i + 6) & 7;
+                            tc_mma_ts(base + kPmColO + t * 128, base + kPmColS + t * 128 + k * 8, vb + k * (2048 >> 4),
+                                      kIdescPV, i > 0 ? 1u : acc);
                         }
-                        qk(t, kt);
+                        g = bar_test(pbar, par);
                     }
+                    if (!__any_sync(0xffffffffu, g) && !wait(pbar, par)) { ok = false; break; }
+                    tc_fence_after();
+                    g = 0;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 4; k < 6; ++k)
+                            tc_mma_ts(base + kPmColO + t * 128, base + kPmColS + t * 128 + k * 8, vb + k * (2048 >> 4),
+                                      kIdescPV, 1u);
+                        const bool last = t == 1 || j >= z.e1;  // the step's last turn
+                        if (last) {
+                            vn = wrap(sv + 2);
+                            kn = wrap(sk + 2);
+                            g = bar_test(full0 + 8 * vn, hv ^ (vn < sv)) & (j + 2 < z.steps ? bar_test(full0 + 8 * kn, hk ^ (kn < sk)) : 1u);
+                        }
+                        if (j + 1 < e) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                tc_mma_ss(base + kPmColS + t * 128, q_desc + t * (kPmTileBytes >> 4) + kstep(k), kb + kstep(k),
+                                          kIdescQK, k > 0);
+                                if (k == 6) g |= bar_test(smem_u32(&sb->p_most[t ^ 1]), (ppar >> (t ^ 1)) & 1u) << (1 + (t ^ 1));
+                            }
+                            tc_commit(smem_u32(&sb->s_full[t]));
+                        } else {
+                            tc_commit(smem_u32(&sb->o_full[t]));
+                        }
+                        if (last) {
+                            tc_commit(empty0 + 8 * sv);
+                            if (more) tc_commit(empty0 + 8 * sk);
+                            if (j + 2 == z.steps) tc_commit(smem_u32(&sb->q_empty));
+                            vn = v_desc + vn * (kPmTileBytes >> 4);
+                            kn = k_desc + kn * (kPmTileBytes >> 4);
+                        }
+                    }
+                    ppar ^= 1u << t;
+                    got = __reduce_or_sync(0xffffffffu, g);
                 }
                 if (!ok) break;
-                release(&sb->empty[vt % kPmStages]);
-                if (more) release(&sb->empty[kt % kPmStages]);
-                if (j + 2 == z.steps) release(&sb->q_empty);
-                it += 2;
+                vb = __reduce_or_sync(0xffffffffu, vn);
+                kb = __reduce_or_sync(0xffffffffu, kn);
+                const uint32_t v2 = wrap(sv + 2), k2 = wrap(sk + 2);
+                hv ^= v2 < sv;
+                hk ^= k2 < sk;
+                sv = v2;
+                sk = k2;
             }
+            if (!ok) break;
+            // the piece took 2 steps tiles: the next K tile follows the last V, one before sv
+            const uint32_t s1 = sv == 0 ? kPmStages - 1 : sv - 1;
+            ph = hv ^ (s1 > sv);
+            st = s1;
         }
         // the ring's last releases have no reader: wait for every product before the CTA ends
-        if (elect_one()) tc_commit(&sb->drain);
+        if (elect_one()) tc_commit(smem_u32(&sb->drain));
         __syncwarp();
         for (uint32_t i = 0; i < (1u << 24) && !mbar_try_wait(&sb->drain, 0); ++i) {}
         __syncwarp();
@@ -701,7 +777,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             const int32_t lim = has_row ? max(0, s.m - s.n + tok + 1) : 0;  // keys the row sees
             float m = -INFINITY, l = 0.0f;
             for (int32_t j = 0; j < e; ++j) {
-                if (!pm_wait(&sb->s_full[t], ns & 1u, sb, a.hdr, 0xffffffffu)) { ok = false; break; }
+                if (!pm_wait(smem_u32(&sb->s_full[t]), ns & 1u, sb, a.hdr, 0xffffffffu)) { ok = false; break; }
                 ++ns;
                 tc_fence_after();
                 const int32_t left = lim - (pos.j + j) * kPmTile;  // columns of this tile the row sees
@@ -743,6 +819,24 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                     m = top;
                     l *= alpha;
                 }
+                if (j > 0 && __any_sync(0xffffffffu, need)) {
+                    // O holds the earlier key tiles, complete before this S was
+                    const uint64_t al = pack2(alpha, alpha);
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t o[16];
+                        tc_ld16(to + 16 * c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            float lo, hi;
+                            unpack2(mul2(pack2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), al), lo, hi);
+                            o[i] = __float_as_uint(lo);
+                            o[i + 1] = __float_as_uint(hi);
+                        }
+                        tc_st16(to + 16 * c, o);
+                    }
+                }
                 const float ref = m == -INFINITY ? 0.0f : -m * kPmScale;
                 const uint64_t sc2 = pack2(kPmScale, kPmScale), ref2 = pack2(ref, ref);
                 uint64_t sum[2] = {0ull, 0ull};
@@ -759,32 +853,18 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                     }
                     tc_st16(ts + c / 2, p);
                 };
-                // (y still holds columns 96 .. 127)
+                // three quarters of P first (y still holds columns 96 .. 127), announced on their own
                 weights(y, 96);
                 tc_ld32(ts + 64, y);
                 weights(x, 0);
                 weights(x + 32, 32);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sb->p_most[t]);
                 tc_wait_ld();
                 if (cut) hide(y, 64, 32);
                 weights(y, 64);
-                if (j > 0 && __any_sync(0xffffffffu, need)) {
-                    // O holds the earlier key tiles, complete before this S was
-                    const uint64_t al = pack2(alpha, alpha);
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[32];
-                        tc_ld32(to + 32 * c, o);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float lo, hi;
-                            unpack2(mul2(pack2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), al), lo, hi);
-                            o[i] = __float_as_uint(lo);
-                            o[i + 1] = __float_as_uint(hi);
-                        }
-                        tc_st32(to + 32 * c, o);
-                    }
-                }
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -797,7 +877,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             // ---- the piece's end: the rows, or their part for the merge
             const bool partial = pos.j > 0 || (same_unit(pos, end) && end.j > 0);
             if (e > 0) {
-                if (!pm_wait(&sb->o_full[t], no & 1u, sb, a.hdr, 0xffffffffu)) break;
+                if (!pm_wait(smem_u32(&sb->o_full[t]), no & 1u, sb, a.hdr, 0xffffffffu)) break;
                 ++no;
                 tc_fence_after();
             }
