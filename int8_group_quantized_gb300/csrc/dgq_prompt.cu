@@ -543,10 +543,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         uint32_t nq0 = 0, nq1 = 0;  // Q tiles loaded
         bool ok = true, v_flight = false;
         uint32_t q_loaded = 0;  // pieces with a Q load
-        for (; ok && before(pos, end); next_unit(a, U, pos, s)) {
-            const PromptPiece z = piece_of(s, pos, end, U);
-            if (z.steps == 0) continue;
-            if (q_loaded > 0 && !pm_wait(smem_u32(&sb->q_empty), (q_loaded - 1) & 1u, sb, a.hdr, 0xffffffffu)) break;
+        // a unit's Q, behind its first K: its buffer is free once the last unit's last S is done
+        auto load_q = [&](const PromptPiece &z) -> bool {
+            if (q_loaded > 0 && !pm_wait(smem_u32(&sb->q_empty), (q_loaded - 1) & 1u, sb, a.hdr, 0xffffffffu)) return false;
             ++q_loaded;
             if (lane == 0) {
                 const int32_t tok = s.q0 + pos.i * U;
@@ -561,6 +560,11 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                     tma_tile_4d(sq + kPmTileBytes, &maps.q, 0, pos.h * G, tok + U / 2, 0, &sb->q_full[1]);
                 }
             }
+            return true;
+        };
+        for (; ok && before(pos, end); next_unit(a, U, pos, s)) {
+            const PromptPiece z = piece_of(s, pos, end, U);
+            if (z.steps == 0) continue;
             // lane l copies half l % 2 of page l / 2 of the key tile
             auto block_of = [&](int32_t j) -> int32_t {
                 int32_t blk = 0;
@@ -618,6 +622,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                         if (lane == 0) mbar_arrive(&sb->full[st]);
                     }
                     ++it;
+                    if (kv == 0 && j == pos.j && !load_q(z)) {
+                        ok = false;
+                        break;
+                    }
                 }
                 if (!ok) break;
                 blk = blk_next;
@@ -934,59 +942,71 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
     }
 }
 
-// Merge of the units cut between CTAs: block (c, part) folds 32 rows of the unit whose first part is
-// CTA c's last piece, in CTA order: a warp takes a row at a time, four columns per lane.
-constexpr int kPmMergeParts = 8, kPmMergeWarps = 4;
+// Merge of the units cut between CTAs: block (c, part) folds 16 rows of the unit whose first part is
+// CTA c's last piece, in CTA order; a warp takes two rows, four columns per lane, and has the parts
+// of kPmMergeDepth CTAs in flight.
+constexpr int kPmMergeParts = 16, kPmMergeWarps = 8, kPmMergeDepth = 4;
+constexpr int kPmMaxCtas = 1024;
 
 __global__ void __launch_bounds__(kPmMergeWarps * 32) prompt_merge_kernel(const PromptArgs a, int32_t ctas)
 {
+    __shared__ int32_t slots[kPmMaxCtas], s_count;
     pdl_wait_primary();
     const int4 head = __ldcg(a.head + blockIdx.x);
     if (head.x == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t G = a.G, U = kPmRows / G;
+    if (warp == 0) {  // the unit's parts: this CTA's, then the next CTAs' first pieces up to the unit's end
+        int32_t count = 1;
+        if (lane == 0) slots[0] = 2 * blockIdx.x + (head.x - 1);
+        for (int32_t c0 = blockIdx.x + 1; c0 < ctas; c0 += 32) {
+            const int32_t c = c0 + lane;
+            const int32_t flag = c < ctas ? __ldcg(a.cont + c) : 0;
+            const uint32_t ends = __ballot_sync(0xffffffffu, flag == 2);
+            const uint32_t upto = ends ? (ends & (0u - ends)) * 2u - 1u : 0xffffffffu;
+            const uint32_t have = __ballot_sync(0xffffffffu, flag != 0) & upto;  // (a CTA may have no piece)
+            if ((have >> lane) & 1u) slots[count + __popc(have & ((1u << lane) - 1u))] = 2 * c;
+            count += __popc(have);
+            if (ends) break;
+        }
+        if (lane == 0) s_count = count;
+    }
+    __syncthreads();
+    const int32_t count = s_count;
     const PromptSeq s = prompt_seq(a, head.y, false);
-    const int64_t first = 2 * (int64_t)blockIdx.x + (head.x - 1);
     constexpr int kRows = kPmRows / kPmMergeParts / kPmMergeWarps;
+#pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int32_t row = blockIdx.y * (kPmRows / kPmMergeParts) + i * kPmMergeWarps + warp;
         const int32_t tok = head.w * U + row / G;
         if (tok >= s.n) continue;
         float M = -INFINITY, L = 0.0f;
         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-        int64_t slot = first;
-        for (int32_t c = blockIdx.x;;) {
-            const int64_t p = slot * kPmRows + row;
-            const float2 ml = __ldcg(a.ml + p);
-            const float4 o = __ldcg(reinterpret_cast<const float4 *>(a.part + p * kD) + lane);
-            const float Mn = fmaxf(M, ml.x);
-            if (ml.x != -INFINITY) {  // (a part whose keys the row does not see wrote no O)
-                const float fo = M == -INFINITY ? 0.0f : pm_ex2((M - Mn) * kPmScale), fn = pm_ex2((ml.x - Mn) * kPmScale);
-                L = L * fo + ml.y * fn;
-                O.x = O.x * fo + o.x * fn;
-                O.y = O.y * fo + o.y * fn;
-                O.z = O.z * fo + o.z * fn;
-                O.w = O.w * fo + o.w * fn;
-                M = Mn;
-            }
-            int32_t flag = 0;
-            while (++c < ctas && (flag = __ldcg(a.cont + c)) == 0) {}  // CTAs without a piece
-            if (c >= ctas) break;
-            slot = 2 * (int64_t)c;
-            if (flag == 2) {  // the unit's last part
-                const int64_t pl = slot * kPmRows + row;
-                const float2 e = __ldcg(a.ml + pl);
-                const float4 oe = __ldcg(reinterpret_cast<const float4 *>(a.part + pl * kD) + lane);
-                if (e.x != -INFINITY) {
-                    const float Me = fmaxf(M, e.x);
-                    const float fo = M == -INFINITY ? 0.0f : pm_ex2((M - Me) * kPmScale), fn = pm_ex2((e.x - Me) * kPmScale);
-                    L = L * fo + e.y * fn;
-                    O.x = O.x * fo + oe.x * fn;
-                    O.y = O.y * fo + oe.y * fn;
-                    O.z = O.z * fo + oe.z * fn;
-                    O.w = O.w * fo + oe.w * fn;
+        for (int32_t k0 = 0; k0 < count; k0 += kPmMergeDepth) {
+            float2 ml[kPmMergeDepth];
+            float4 o[kPmMergeDepth];
+#pragma unroll
+            for (int k = 0; k < kPmMergeDepth; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.0f);
+                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + k < count) {
+                    const int64_t p = (int64_t)slots[k0 + k] * kPmRows + row;
+                    ml[k] = __ldcg(a.ml + p);
+                    o[k] = __ldcg(reinterpret_cast<const float4 *>(a.part + p * kD) + lane);
                 }
-                break;
+            }
+#pragma unroll
+            for (int k = 0; k < kPmMergeDepth; ++k) {
+                if (ml[k].x == -INFINITY) continue;  // no key of the part is seen by the row: it wrote no O
+                const float Mn = fmaxf(M, ml[k].x);
+                const float fo = M == -INFINITY ? 0.0f : pm_ex2((M - Mn) * kPmScale);
+                const float fn = pm_ex2((ml[k].x - Mn) * kPmScale);
+                L = L * fo + ml[k].y * fn;
+                O.x = O.x * fo + o[k].x * fn;
+                O.y = O.y * fo + o[k].y * fn;
+                O.z = O.z * fo + o[k].z * fn;
+                O.w = O.w * fo + o[k].w * fn;
+                M = Mn;
             }
         }
         const float inv = L > 0.0f ? 1.0f / L : 0.0f;
@@ -1035,6 +1055,7 @@ cudaError_t launch_prompt(const void *q, const void *k, const void *v, int32_t t
 {
     *map_failed = true;
     const int32_t G = Hq / Hkv;
+    if (nsm > kPmMaxCtas) nsm = kPmMaxCtas;
     const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return cudaErrorNotSupported;
     PromptMaps maps;
