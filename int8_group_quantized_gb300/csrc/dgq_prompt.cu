@@ -37,12 +37,14 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace dgq {
 
 constexpr float kPmScale = 0.12751743074570180f;  // log2(e) / sqrt(128)
 constexpr float kPmLazy = 8.0f / kPmScale;        // the maximum moves when exceeded by 8 in the log2 domain
 constexpr int kPmTile = 128;                      // rows of a tile, keys of a key tile
-constexpr int kPmStages = 5;
+constexpr int kPmStages = 4;
 constexpr int kPmTileBytes = kPmTile * kD * 2;    // 32 KB: two halves of 64 columns, [row][64] each
 constexpr int kPmHalf = kPmTileBytes / 2;
 constexpr int kPmThreads = 320;  // two softmax warpgroups, a load warp, a product warp
@@ -50,7 +52,7 @@ constexpr int kPmLoadWarp = 8, kPmMmaWarp = 9;
 constexpr int kPmUnitCost = 2 * kPmTile;          // a unit's fixed cost, in keys
 constexpr int kPmSnap = 4;                        // key tiles: no part of a cut unit is smaller
 constexpr int kPmRows = 2 * kPmTile;              // packed rows of a unit
-constexpr unsigned long long kPmWaitNs = 2000000000ull;
+constexpr uint32_t kPmWaitPolls = 1u << 23;       // polls before a wait gives up: a second or more
 
 // Tensor-memory columns of the 512 a CTA takes: S (and P) of tile 0 and 1, O of tile 0 and 1.
 constexpr uint32_t kPmColS = 0, kPmColO = 256;
@@ -379,40 +381,42 @@ __device__ __forceinline__ uint32_t pm_pack_bf16(float lo, float hi)
 
 // ---- the kernel -----------------------------------------------------------------------------------
 
+// A piece as the load warp hands it to the other roles, through a ring of kPmItems entries.
+struct PromptItem {
+    int32_t e0, e1;  // key tiles of tile 0 and 1 (both < 0: no more pieces)
+    int32_t see;     // keys of the piece that the unit's first token sees: token i of it sees `see` + i
+    int32_t toks;    // the request's tokens from the unit's first on
+    int32_t row;     // row of that token in q and out
+    int32_t h;       // KV head
+    int32_t slot;    // where its part goes, or -1: a whole unit
+};
+constexpr int kPmItems = 4;
+
 struct PromptBars {
+    uint64_t item_full[kPmItems], item_empty[kPmItems];
+    PromptItem items[kPmItems];
     uint64_t full[kPmStages], empty[kPmStages];
     uint64_t q_full[2], s_full[2], p_most[2], p_ready[2], o_full[2];
     uint64_t q_empty, v_part, drain;
     uint32_t tmem;
-    volatile uint32_t abort;
     PromptPos cut[2];
     int64_t wsum[kPmThreads / 32];
 };
 
-constexpr size_t kPmSmem = 1024 + (size_t)(2 + kPmStages) * kPmTileBytes + sizeof(PromptBars);
+constexpr int kPmTurn = 32 * 128;  // a softmax warp's buffer for turning rows
+constexpr size_t kPmSmem = (size_t)(2 + kPmStages) * kPmTileBytes + 8 * kPmTurn + sizeof(PromptBars);
 static_assert(kPmSmem <= 232448, "shared memory of a CTA");
 static_assert((size_t)(kMaxCallBatch + 1) * 8 <= (size_t)kPmStages * kPmTileBytes, "the request prefix uses the ring");
 
-// Bounded wait, with one answer for all `mask` lanes.  False: the wait ran out, here or elsewhere.
-// (The clock is read once in 1024 polls only: a read takes as long as a short wait.)
-__device__ __forceinline__ bool pm_wait(uint32_t bar, uint32_t parity, PromptBars *sb, WsHeader *hdr, uint32_t mask)
+// Bounded wait, with one answer for the warp.  False: the wait ran out; the caller leaves, and whoever
+// waits for it runs out in turn.
+__device__ __forceinline__ bool pm_wait(uint32_t bar, uint32_t parity, WsHeader *hdr)
 {
-    unsigned long long t0 = 0;
-    for (uint32_t i = 1;; ++i) {
-        if (__all_sync(mask, bar_try(bar, parity))) return true;
-        if ((i & 1023u) == 0) {
-            bool over = sb->abort != 0;
-            unsigned long long t;
-            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-            if (t0 == 0) t0 = t;
-            if (t - t0 > kPmWaitNs) {
-                over = true;
-                sb->abort = 1;
-                record_error(hdr, kErrFullWait);
-            }
-            if (__any_sync(mask, over)) return false;
-        }
-    }
+#pragma unroll 1
+    for (uint32_t i = 0; i < kPmWaitPolls; ++i)
+        if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+    record_error(hdr, kErrFullWait);
+    return false;
 }
 
 // A unit's tiles in the piece [j0, j1): per tile the key tiles to go through, and its keys.
@@ -445,11 +449,11 @@ __device__ __forceinline__ bool before(const PromptPos &x, const PromptPos &end)
 
 __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs a, const __grid_constant__ PromptMaps maps)
 {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = align_smem_1024(smem_raw);
-    PromptBars *sb = reinterpret_cast<PromptBars *>(smem + (2 + kPmStages) * kPmTileBytes);
+    extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle repeats every 1024 bytes)
+    PromptBars *sb = reinterpret_cast<PromptBars *>(smem + (2 + kPmStages) * kPmTileBytes + 8 * kPmTurn);
     const uint32_t sq = smem_u32(smem), sring = sq + 2 * kPmTileBytes;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and known to be
     const int32_t G = a.G, U = kPmRows / G;
 
     pdl_launch_dependents();  // the merge may be scheduled while this kernel runs
@@ -496,10 +500,13 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 mbar_init(&sb->p_ready[t], 4);
                 mbar_init(&sb->o_full[t], 1);
             }
+            for (int i = 0; i < kPmItems; ++i) {
+                mbar_init(&sb->item_full[i], 1);
+                mbar_init(&sb->item_empty[i], 9);  // eight softmax warps and the product warp
+            }
             mbar_init(&sb->q_empty, 1);
             mbar_init(&sb->v_part, 1);
             mbar_init(&sb->drain, 1);
-            sb->abort = 0;
             fence_barrier_init();
         }
         __syncthreads();
@@ -532,11 +539,32 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
     tc_fence_after();
     const uint32_t tmem = sb->tmem;
 
-    PromptPos pos = begin;
-    PromptSeq s = prompt_seq(a, pos.b, false);
+    uint32_t ni = 0;  // items taken
+    auto next_item = [&](PromptItem &z) -> bool {
+        const uint32_t i = ni % kPmItems;
+        if (!pm_wait(smem_u32(&sb->item_full[i]), (ni / kPmItems) & 1u, a.hdr)) return false;
+        z = sb->items[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sb->item_empty[i]);
+        ++ni;
+        return z.e0 >= 0;
+    };
 
     if (warp == kPmLoadWarp) {
-        // ======================================== loads
+        // ======================================== pieces and their loads
+        PromptPos pos = begin;
+        PromptSeq s = prompt_seq(a, pos.b, false);
+        auto hand_out = [&](const PromptItem &z) -> bool {
+            const uint32_t i = ni % kPmItems;
+            if (ni >= kPmItems && !pm_wait(smem_u32(&sb->item_empty[i]), (ni / kPmItems - 1) & 1u, a.hdr))
+                return false;
+            if (lane == 0) {
+                sb->items[i] = z;
+                mbar_arrive(&sb->item_full[i]);
+            }
+            ++ni;
+            return true;
+        };
         fence_proxy_async_smem();  // the prefix was read from the ring by ordinary loads
         const int32_t pages = a.bt ? kPmTile / a.bs : 0;  // pages of a key tile
         uint32_t it = 0, nv = 0;
@@ -545,7 +573,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         uint32_t q_loaded = 0;  // pieces with a Q load
         // a unit's Q, behind its first K: its buffer is free once the last unit's last S is done
         auto load_q = [&](const PromptPiece &z) -> bool {
-            if (q_loaded > 0 && !pm_wait(smem_u32(&sb->q_empty), (q_loaded - 1) & 1u, sb, a.hdr, 0xffffffffu)) return false;
+            if (q_loaded > 0 && !pm_wait(smem_u32(&sb->q_empty), (q_loaded - 1) & 1u, a.hdr)) return false;
             ++q_loaded;
             if (lane == 0) {
                 const int32_t tok = s.q0 + pos.i * U;
@@ -562,9 +590,23 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             }
             return true;
         };
-        for (; ok && before(pos, end); next_unit(a, U, pos, s)) {
+        for (bool first = true; ok && before(pos, end); next_unit(a, U, pos, s), first = false) {
             const PromptPiece z = piece_of(s, pos, end, U);
-            if (z.steps == 0) continue;
+            const int32_t toks = s.n - pos.i * U, row0 = s.q0 + pos.i * U;
+            if (z.steps == 0) {  // rows that see no key
+                for (int32_t x = lane; x < min(U, toks) * G * 16; x += 32) {
+                    const int32_t r = x >> 4;
+                    reinterpret_cast<uint4 *>(a.out + ((int64_t)(row0 + r / G) * a.Hq + pos.h * G + r % G) * kD)[x & 15] =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+                continue;
+            }
+            const bool partial = pos.j > 0 || (same_unit(pos, end) && end.j > 0);
+            if (!hand_out(PromptItem{z.e0, z.e1, s.m - s.n + 1 + pos.i * U - pos.j * kPmTile, toks, row0, pos.h,
+                                     partial ? 2 * (int32_t)blockIdx.x + (first ? 0 : 1) : -1})) {
+                ok = false;
+                break;
+            }
             // lane l copies half l % 2 of page l / 2 of the key tile
             auto block_of = [&](int32_t j) -> int32_t {
                 int32_t blk = 0;
@@ -586,7 +628,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 const uint32_t bytes = a.bt ? (uint32_t)used * a.bs * kD * 2 : (uint32_t)kPmTileBytes;
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t st = it % kPmStages, dst = sring + st * kPmTileBytes;
-                    if (it >= kPmStages && !pm_wait(smem_u32(&sb->empty[st]), (it / kPmStages - 1) & 1u, sb, a.hdr, 0xffffffffu)) {
+                    if (it >= kPmStages && !pm_wait(smem_u32(&sb->empty[st]), (it / kPmStages - 1) & 1u, a.hdr)) {
                         ok = false;
                         break;
                     }
@@ -606,7 +648,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                     }
                     v_flight = part;
                     if (part) {
-                        if (!pm_wait(smem_u32(&sb->v_part), nv & 1u, sb, a.hdr, 0xffffffffu)) {
+                        if (!pm_wait(smem_u32(&sb->v_part), nv & 1u, a.hdr)) {
                             ok = false;
                             break;
                         }
@@ -631,8 +673,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 blk = blk_next;
             }
         }
-        if (sb->abort != 0 && lane == 0) {  // some wait ran out: no copy may still be in flight when the CTA ends
+        if (ok) ok = hand_out(PromptItem{-1, -1, 0, 0, 0, 0, -1});
+        if (!ok && lane == 0) {  // a wait ran out: no copy may still be in flight when the CTA ends
             auto drain = [](uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
                 for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(bar, parity); ++i) {}
             };
             for (uint32_t k = it > kPmStages ? it - kPmStages : 0; k < it; ++k)
@@ -656,11 +700,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         const uint32_t q_desc = __shfl_sync(0xffffffffu, desc_k(sq), 0);
         const uint32_t k_desc = desc_k(sring), v_desc = desc_mn(sring);
         const uint32_t full0 = smem_u32(&sb->full[0]), empty0 = smem_u32(&sb->empty[0]);
-        auto wait = [&](uint32_t bar, uint32_t parity) { return pm_wait(bar, parity, sb, a.hdr, 0xffffffffu); };
+        auto wait = [&](uint32_t bar, uint32_t parity) { return pm_wait(bar, parity, a.hdr); };
         auto wrap = [](uint32_t x) { return x >= kPmStages ? x - kPmStages : x; };
-        for (; ok && before(pos, end); next_unit(a, U, pos, s)) {
-            const PromptPiece z = piece_of(s, pos, end, U);
-            if (z.steps == 0) continue;
+        for (PromptItem z; ok && next_item(z);) {
+            const int32_t steps = max(z.e0, z.e1);
             // S of the first key tile
             if (!wait(full0 + 8 * st, ph)) break;
             uint32_t kb = __shfl_sync(0xffffffffu, k_desc + st * (kPmTileBytes >> 4), 0);
@@ -681,7 +724,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             if (!ok) break;
             if (elect_one()) {
                 tc_commit(empty0 + 8 * st);
-                if (z.steps == 1) tc_commit(smem_u32(&sb->q_empty));
+                if (steps == 1) tc_commit(smem_u32(&sb->q_empty));
             }
             __syncwarp();
             // stage and parity of V of key tile j, and of K of the next
@@ -690,8 +733,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             uint32_t vb = __shfl_sync(0xffffffffu, v_desc + sv * (kPmTileBytes >> 4), 0);
             kb = __shfl_sync(0xffffffffu, k_desc + sk * (kPmTileBytes >> 4), 0);
             uint32_t got = 0;  // bit 0: V and K of the next step are known to be there, bit 1 + t: P of tile t
-            for (int32_t j = 0; j < z.steps; ++j) {
-                const bool more = j + 1 < z.steps;
+            for (int32_t j = 0; j < steps; ++j) {
+                const bool more = j + 1 < steps;
                 if (!(got & 1u) && (!wait(full0 + 8 * sv, hv) || (more && !wait(full0 + 8 * sk, hk)))) { ok = false; break; }
                 const uint32_t acc = __shfl_sync(0xffffffffu, j > 0 ? 1u : 0u, 0);
                 uint32_t vn = 0, kn = 0;
@@ -725,7 +768,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                         if (last) {
                             vn = wrap(sv + 2);
                             kn = wrap(sk + 2);
-                            g = bar_test(full0 + 8 * vn, hv ^ (vn < sv)) & (j + 2 < z.steps ? bar_test(full0 + 8 * kn, hk ^ (kn < sk)) : 1u);
+                            g = bar_test(full0 + 8 * vn, hv ^ (vn < sv)) & (j + 2 < steps ? bar_test(full0 + 8 * kn, hk ^ (kn < sk)) : 1u);
                         }
                         if (j + 1 < e) {
 #pragma unroll
@@ -741,7 +784,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                         if (last) {
                             tc_commit(empty0 + 8 * sv);
                             if (more) tc_commit(empty0 + 8 * sk);
-                            if (j + 2 == z.steps) tc_commit(smem_u32(&sb->q_empty));
+                            if (j + 2 == steps) tc_commit(smem_u32(&sb->q_empty));
                             vn = v_desc + vn * (kPmTileBytes >> 4);
                             kn = k_desc + kn * (kPmTileBytes >> 4);
                         }
@@ -767,6 +810,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         // the ring's last releases have no reader: wait for every product before the CTA ends
         if (elect_one()) tc_commit(smem_u32(&sb->drain));
         __syncwarp();
+#pragma unroll 1
         for (uint32_t i = 0; i < (1u << 24) && !mbar_try_wait(&sb->drain, 0); ++i) {}
         __syncwarp();
     } else {
@@ -775,20 +819,19 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         const int32_t row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + kPmColS + t * 128, to = tmem + lanes + kPmColO + t * 128;
-        const int32_t rtok = t * (U / 2) + row / G, rhead = row % G;
+        const int32_t rtok = t * (U / 2) + row / G;
+        uint8_t *turn = smem + (2 + kPmStages) * kPmTileBytes + warp * kPmTurn;
         uint32_t ns = 0, no = 0;  // S tiles and O tiles taken
         bool ok = true;
-        for (bool first = true; ok && before(pos, end); next_unit(a, U, pos, s), first = false) {
-            const PromptPiece z = piece_of(s, pos, end, U);
-            const int32_t e = t ? z.e1 : z.e0, tok = pos.i * U + rtok;
-            const bool has_row = tok < s.n;
-            const int32_t lim = has_row ? max(0, s.m - s.n + tok + 1) : 0;  // keys the row sees
+        for (PromptItem z; ok && next_item(z);) {
+            const int32_t e = t ? z.e1 : z.e0;
+            const bool has_row = rtok < z.toks;
+            int32_t left = has_row ? z.see + rtok : 0;  // columns from this key tile on that the row sees
             float m = -INFINITY, l = 0.0f;
-            for (int32_t j = 0; j < e; ++j) {
-                if (!pm_wait(smem_u32(&sb->s_full[t]), ns & 1u, sb, a.hdr, 0xffffffffu)) { ok = false; break; }
+            for (int32_t j = 0; j < e; ++j, left -= kPmTile) {
+                if (!pm_wait(smem_u32(&sb->s_full[t]), ns & 1u, a.hdr)) { ok = false; break; }
                 ++ns;
                 tc_fence_after();
-                const int32_t left = lim - (pos.j + j) * kPmTile;  // columns of this tile the row sees
                 const bool cut = __any_sync(0xffffffffu, left < kPmTile);
                 // the row's maximum; the first 64 scores stay in registers, the others are read again
                 // below (in tensor memory P overwrites the first 64 columns only)
@@ -882,36 +925,19 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 l += lo + hi;
             }
             if (!ok) break;
-            // ---- the piece's end: the rows, or their part for the merge
-            const bool partial = pos.j > 0 || (same_unit(pos, end) && end.j > 0);
+            // ---- the piece's end: the rows, or their part for the merge.  A thread has a row, so the warp
+            // turns them through shared memory: eight lanes write 128 bytes of one row.  (Stored as they
+            // lie, 16 bytes of 32 rows at a time, a tile took 4000 cycles.)
+            const bool partial = z.slot >= 0;
             if (e > 0) {
-                if (!pm_wait(smem_u32(&sb->o_full[t]), no & 1u, sb, a.hdr, 0xffffffffu)) break;
+                if (!pm_wait(smem_u32(&sb->o_full[t]), no & 1u, a.hdr)) break;
                 ++no;
                 tc_fence_after();
             }
-            if (partial) {
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (first ? 0 : 1);
-                const int64_t prow = slot * kPmRows + t * kPmTile + row;
-                if (has_row) __stcg(a.ml + prow, make_float2(m, l));
-                if (e > 0) {
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[32];
-                        tc_ld32(to + 32 * c, o);
-                        tc_wait_ld();
-                        if (has_row) {
-                            float4 *dst = reinterpret_cast<float4 *>(a.part + prow * kD + 32 * c);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                __stcg(dst + i, make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                            __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3])));
-                        }
-                    }
-                }
-            } else {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                uint4 *dst = reinterpret_cast<uint4 *>(
-                    a.out + ((int64_t)(s.q0 + tok) * a.Hq + pos.h * G + rhead) * kD);
+            const int64_t prow = (int64_t)z.slot * kPmRows + t * kPmTile + (warp & 3) * 32;
+            if (partial && has_row) __stcg(a.ml + prow + lane, make_float2(m, l));
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;  // (a row that sees no key: 0)
+            if (!partial || e > 0) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
@@ -919,16 +945,34 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                         tc_ld32(to + 32 * c, o);
                         tc_wait_ld();
                     }
+                    if (!partial) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                        if (e > 0 && lim > 0) {
-                            w.x = pm_pack_bf16(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
-                            w.y = pm_pack_bf16(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
-                            w.z = pm_pack_bf16(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
-                            w.w = pm_pack_bf16(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
-                        }
-                        if (has_row) dst[4 * c + i] = w;
+                        for (int i = 0; i < 16; ++i)
+                            o[i] = l > 0.0f ? pm_pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
+                    }
+                    // 16-byte unit u of row `lane` at unit u ^ lane % 8: bf16 quarters in two rounds a half
+                    // row, fp32 parts in one
+                    const int u0 = partial ? 0 : 4 * (c & 1);
+                    if (partial || u0 == 0) __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (partial || u < 4)
+                            *reinterpret_cast<uint4 *>(turn + lane * 128 + (((u0 + u) ^ (lane & 7)) << 4)) =
+                                make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                    if (!partial && u0 == 0) continue;
+                    __syncwarp();
+                    const int u = lane & 7;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = 4 * k + (lane >> 3);
+                        const uint4 w = *reinterpret_cast<const uint4 *>(turn + r * 128 + ((u ^ (r & 7)) << 4));
+                        const int32_t tr = (warp & 3) * 32 + r, tok = t * (U / 2) + tr / G;
+                        if (tok >= z.toks) continue;
+                        if (partial)
+                            __stcg(reinterpret_cast<uint4 *>(a.part + (prow + r) * kD + 32 * c) + u, w);
+                        else
+                            reinterpret_cast<uint4 *>(a.out + ((int64_t)(z.row + tok) * a.Hq + z.h * G + tr % G) * kD +
+                                                      64 * (c >> 1))[u] = w;
                     }
                 }
             }
