@@ -66,7 +66,7 @@ struct PromptArgs {
     int32_t *cont; // per CTA: 1 its first piece continues a unit, 2 and ends it there
     float2 *ml;    // per slot and row: maximum and sum
     float *part;   // per slot: O [256][128], unnormalised
-    int32_t B, Hq, Hkv, G, total_q, total_kv, bs, max_blocks, num_blocks;
+    int32_t B, Hq, Hkv, G, lg, total_q, total_kv, bs, max_blocks, num_blocks;
 };
 
 struct PromptMaps {
@@ -114,7 +114,7 @@ __device__ __forceinline__ bool same_unit(const PromptPos &x, const PromptPos &y
     return x.b == y.b && x.h == y.h && x.i == y.i;
 }
 
-__device__ __forceinline__ int32_t prompt_units(const PromptSeq &s, int32_t U) { return (s.n + U - 1) / U; }
+__device__ __forceinline__ int32_t prompt_units(const PromptSeq &s, int32_t U) { return (s.n + U - 1) >> (__ffs(U) - 1); }
 
 // Keys that the tokens before `tok` of the request see (the last of them sees all of these).
 __device__ __forceinline__ int32_t keys_before(const PromptSeq &s, int32_t tok)
@@ -389,7 +389,9 @@ struct PromptItem {
     int32_t row;     // row of that token in q and out
     int32_t h;       // KV head
     int32_t slot;    // where its part goes, or -1: a whole unit
+    int32_t pad;
 };
+static_assert(sizeof(PromptItem) == 32, "eight words, one per lane");
 constexpr int kPmItems = 4;
 
 struct PromptBars {
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
     const uint32_t sq = smem_u32(smem), sring = sq + 2 * kPmTileBytes;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and known to be
-    const int32_t G = a.G, U = kPmRows / G;
+    const int32_t G = a.G, lg = a.lg, U = kPmRows >> lg;
 
     pdl_launch_dependents();  // the merge may be scheduled while this kernel runs
 
@@ -543,8 +545,14 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
     auto next_item = [&](PromptItem &z) -> bool {
         const uint32_t i = ni % kPmItems;
         if (!pm_wait(smem_u32(&sb->item_full[i]), (ni / kPmItems) & 1u, a.hdr)) return false;
-        z = sb->items[i];
-        __syncwarp();
+        const int32_t w = reinterpret_cast<const int32_t *>(&sb->items[i])[lane & 7];
+        z.e0 = __shfl_sync(0xffffffffu, w, 0);
+        z.e1 = __shfl_sync(0xffffffffu, w, 1);
+        z.see = __shfl_sync(0xffffffffu, w, 2);
+        z.toks = __shfl_sync(0xffffffffu, w, 3);
+        z.row = __shfl_sync(0xffffffffu, w, 4);
+        z.h = __shfl_sync(0xffffffffu, w, 5);
+        z.slot = __shfl_sync(0xffffffffu, w, 6);
         if (lane == 0) mbar_arrive(&sb->item_empty[i]);
         ++ni;
         return z.e0 >= 0;
@@ -596,14 +604,14 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             if (z.steps == 0) {  // rows that see no key
                 for (int32_t x = lane; x < min(U, toks) * G * 16; x += 32) {
                     const int32_t r = x >> 4;
-                    reinterpret_cast<uint4 *>(a.out + ((int64_t)(row0 + r / G) * a.Hq + pos.h * G + r % G) * kD)[x & 15] =
+                    reinterpret_cast<uint4 *>(a.out + ((int64_t)(row0 + (r >> lg)) * a.Hq + pos.h * G + (r & (G - 1))) * kD)[x & 15] =
                         make_uint4(0u, 0u, 0u, 0u);
                 }
                 continue;
             }
             const bool partial = pos.j > 0 || (same_unit(pos, end) && end.j > 0);
             if (!hand_out(PromptItem{z.e0, z.e1, s.m - s.n + 1 + pos.i * U - pos.j * kPmTile, toks, row0, pos.h,
-                                     partial ? 2 * (int32_t)blockIdx.x + (first ? 0 : 1) : -1})) {
+                                     partial ? 2 * (int32_t)blockIdx.x + (first ? 0 : 1) : -1, 0})) {
                 ok = false;
                 break;
             }
@@ -673,7 +681,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 blk = blk_next;
             }
         }
-        if (ok) ok = hand_out(PromptItem{-1, -1, 0, 0, 0, 0, -1});
+        if (ok) ok = hand_out(PromptItem{-1, -1, 0, 0, 0, 0, -1, 0});
         if (!ok && lane == 0) {  // a wait ran out: no copy may still be in flight when the CTA ends
             auto drain = [](uint64_t *bar, uint32_t parity) {
 #pragma unroll 1
@@ -819,7 +827,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         const int32_t row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + kPmColS + t * 128, to = tmem + lanes + kPmColO + t * 128;
-        const int32_t rtok = t * (U / 2) + row / G;
+        const int32_t rtok = t * (U / 2) + (row >> lg);
         uint8_t *turn = smem + (2 + kPmStages) * kPmTileBytes + warp * kPmTurn;
         uint32_t ns = 0, no = 0;  // S tiles and O tiles taken
         bool ok = true;
@@ -966,12 +974,12 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                     for (int k = 0; k < 8; ++k) {
                         const int r = 4 * k + (lane >> 3);
                         const uint4 w = *reinterpret_cast<const uint4 *>(turn + r * 128 + ((u ^ (r & 7)) << 4));
-                        const int32_t tr = (warp & 3) * 32 + r, tok = t * (U / 2) + tr / G;
+                        const int32_t tr = (warp & 3) * 32 + r, tok = t * (U / 2) + (tr >> lg);
                         if (tok >= z.toks) continue;
                         if (partial)
                             __stcg(reinterpret_cast<uint4 *>(a.part + (prow + r) * kD + 32 * c) + u, w);
                         else
-                            reinterpret_cast<uint4 *>(a.out + ((int64_t)(z.row + tok) * a.Hq + z.h * G + tr % G) * kD +
+                            reinterpret_cast<uint4 *>(a.out + ((int64_t)(z.row + tok) * a.Hq + z.h * G + (tr & (G - 1))) * kD +
                                                       64 * (c >> 1))[u] = w;
                     }
                 }
@@ -999,7 +1007,7 @@ __global__ void __launch_bounds__(kPmMergeWarps * 32) prompt_merge_kernel(const 
     const int4 head = __ldcg(a.head + blockIdx.x);
     if (head.x == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t G = a.G, U = kPmRows / G;
+    const int32_t G = a.G, U = kPmRows >> a.lg;
     if (warp == 0) {  // the unit's parts: this CTA's, then the next CTAs' first pieces up to the unit's end
         int32_t count = 1;
         if (lane == 0) slots[0] = 2 * blockIdx.x + (head.x - 1);
@@ -1022,7 +1030,7 @@ __global__ void __launch_bounds__(kPmMergeWarps * 32) prompt_merge_kernel(const 
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int32_t row = blockIdx.y * (kPmRows / kPmMergeParts) + i * kPmMergeWarps + warp;
-        const int32_t tok = head.w * U + row / G;
+        const int32_t tok = head.w * U + (row >> a.lg);
         if (tok >= s.n) continue;
         float M = -INFINITY, L = 0.0f;
         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1057,7 +1065,7 @@ __global__ void __launch_bounds__(kPmMergeWarps * 32) prompt_merge_kernel(const 
         uint2 w;
         w.x = pm_pack_bf16(O.x * inv, O.y * inv);
         w.y = pm_pack_bf16(O.z * inv, O.w * inv);
-        reinterpret_cast<uint2 *>(a.out + ((int64_t)(s.q0 + tok) * a.Hq + head.z * G + row % G) * kD)[lane] = w;
+        reinterpret_cast<uint2 *>(a.out + ((int64_t)(s.q0 + tok) * a.Hq + head.z * G + (row & (G - 1))) * kD)[lane] = w;
     }
 }
 
@@ -1155,6 +1163,7 @@ cudaError_t launch_prompt(const void *q, const void *k, const void *v, int32_t t
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.G = G;
+    a.lg = __builtin_ctz((unsigned)G);  // (G is 1, 2, 4 or 8)
     a.total_q = total_q;
     a.total_kv = total_kv;
     a.bs = bs;
