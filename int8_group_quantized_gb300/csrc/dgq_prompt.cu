@@ -328,6 +328,14 @@ __device__ __forceinline__ uint32_t bar_test(uint32_t bar, uint32_t parity)
 // Offset of k-step k (16 columns) in a K-major operand, in descriptor units.
 __device__ __forceinline__ constexpr uint32_t kstep(int k) { return ((k >> 2) * kPmHalf + (k & 3) * 32) >> 4; }
 
+// 16 bytes to global memory where `yes` (a predicated store: no branch).
+__device__ __forceinline__ void st_if(void *p, const uint4 &v, bool yes)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(p),
+                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"((uint32_t)yes)
+                 : "memory");
+}
+
 // ---- small arithmetic -----------------------------------------------------------------------------
 
 __device__ __forceinline__ float pm_ex2(float x)
@@ -840,15 +848,18 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 if (!pm_wait(smem_u32(&sb->s_full[t]), ns & 1u, a.hdr)) { ok = false; break; }
                 ++ns;
                 tc_fence_after();
-                const bool cut = __any_sync(0xffffffffu, left < kPmTile);
+                const int32_t low = __reduce_min_sync(0xffffffffu, left);  // columns that all rows of the warp see
                 // the row's maximum; the first 64 scores stay in registers, the others are read again
                 // below (in tensor memory P overwrites the first 64 columns only)
                 uint32_t x[64], y[32];
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto hide = [&](uint32_t *v, int c0, int n) {
+                auto hide = [&](uint32_t *v, int c0) {  // 32 columns from c0 on, where some row does not see them all
+                    if (low >= c0 + 32) return;
+                    const int32_t n = left - c0;
+                    const uint32_t keep = n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
 #pragma unroll
-                    for (int c = 0; c < n; ++c)
-                        if (c0 + c >= left) v[c] = 0xff800000u;  // -inf
+                    for (int c = 0; c < 32; ++c)
+                        if (!(keep & (1u << c))) v[c] = 0xff800000u;  // -inf
                 };
                 auto maxima = [&](const uint32_t *v, int n) {
 #pragma unroll
@@ -861,14 +872,15 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 tc_ld32(ts + 32, x + 32);
                 tc_wait_ld();
                 tc_ld32(ts + 64, y);
-                if (cut) hide(x, 0, 64);
+                hide(x, 0);
+                hide(x + 32, 32);
                 maxima(x, 64);
                 tc_wait_ld();
-                if (cut) hide(y, 64, 32);
+                hide(y, 64);
                 maxima(y, 32);
                 tc_ld32(ts + 96, y);
                 tc_wait_ld();
-                if (cut) hide(y, 96, 32);
+                hide(y, 96);
                 maxima(y, 32);
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const bool need = top > m + kPmLazy;
@@ -922,7 +934,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sb->p_most[t]);
                 tc_wait_ld();
-                if (cut) hide(y, 64, 32);
+                hide(y, 64);
                 weights(y, 64);
                 tc_wait_st();
                 tc_fence_before();
@@ -945,42 +957,66 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             const int64_t prow = (int64_t)z.slot * kPmRows + t * kPmTile + (warp & 3) * 32;
             if (partial && has_row) __stcg(a.ml + prow + lane, make_float2(m, l));
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;  // (a row that sees no key: 0)
-            if (!partial || e > 0) {
+            uint8_t *mine = turn + lane * 128;  // 16-byte unit u of row r lies at unit u ^ r % 8
+            const int u = lane & 7;
+            if (!partial) {
+                // this lane writes rows r0 + 4k, two steps of which are a whole number of tokens apart
+                const int32_t r0 = (warp & 3) * 32 + (lane >> 3), tok0 = t * (U / 2) + (r0 >> lg);
+                const int32_t tok_odd = 4 >> lg, tok_two = 8 >> lg;
+                const int64_t row_odd = lg < 3 ? (int64_t)tok_odd * a.Hq * kD : 4 * kD, row_two = (int64_t)tok_two * a.Hq * kD;
+                const uint8_t *from = turn + (lane >> 3) * 128;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 128; c += 64) {
                     uint32_t o[32];
-                    if (e > 0) {
-                        tc_ld32(to + 32 * c, o);
-                        tc_wait_ld();
-                    }
-                    if (!partial) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[i] = l > 0.0f ? pm_pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
-                    }
-                    // 16-byte unit u of row `lane` at unit u ^ lane % 8: bf16 quarters in two rounds a half
-                    // row, fp32 parts in one
-                    const int u0 = partial ? 0 : 4 * (c & 1);
-                    if (partial || u0 == 0) __syncwarp();
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        if (partial || u < 4)
-                            *reinterpret_cast<uint4 *>(turn + lane * 128 + (((u0 + u) ^ (lane & 7)) << 4)) =
-                                make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-                    if (!partial && u0 == 0) continue;
                     __syncwarp();
-                    const int u = lane & 7;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int v = 0; v < 8; ++v) {
+                        if (e > 0 && (v & 3) == 0) {
+                            tc_ld32(to + c + 8 * v, o);
+                            tc_wait_ld();
+                        }
+                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                        if (l > 0.0f) {
+                            w.x = pm_pack_bf16(__uint_as_float(o[8 * (v & 3)]) * inv, __uint_as_float(o[8 * (v & 3) + 1]) * inv);
+                            w.y = pm_pack_bf16(__uint_as_float(o[8 * (v & 3) + 2]) * inv, __uint_as_float(o[8 * (v & 3) + 3]) * inv);
+                            w.z = pm_pack_bf16(__uint_as_float(o[8 * (v & 3) + 4]) * inv, __uint_as_float(o[8 * (v & 3) + 5]) * inv);
+                            w.w = pm_pack_bf16(__uint_as_float(o[8 * (v & 3) + 6]) * inv, __uint_as_float(o[8 * (v & 3) + 7]) * inv);
+                        }
+                        *reinterpret_cast<uint4 *>(mine + ((v ^ (lane & 7)) << 4)) = w;
+                    }
+                    __syncwarp();
+                    uint4 w[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        w[k] = *reinterpret_cast<const uint4 *>(from + k * 512 + ((u ^ ((4 * k + (lane >> 3)) & 7)) << 4));
+                    uint16_t *out = a.out + ((int64_t)(z.row + tok0) * a.Hq + z.h * G + (r0 & (G - 1))) * kD + u * 8 + c;
+                    int32_t tok = tok0;
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2) {
+                        st_if(out, w[k], tok < z.toks);
+                        st_if(out + row_odd, w[k + 1], tok + tok_odd < z.toks);
+                        out += row_two;
+                        tok += tok_two;
+                    }
+                }
+            } else if (e > 0) {
+                float *part = a.part + (prow + (lane >> 3)) * kD + u * 4;
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t o[32];
+                    tc_ld32(to + c, o);
+                    tc_wait_ld();
+                    __syncwarp();
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        *reinterpret_cast<uint4 *>(mine + ((v ^ (lane & 7)) << 4)) =
+                            make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                    __syncwarp();
+#pragma unroll 4
+                    for (int k = 0; k < 8; ++k) {  // (rows without a token go along: nobody reads them)
                         const int r = 4 * k + (lane >> 3);
-                        const uint4 w = *reinterpret_cast<const uint4 *>(turn + r * 128 + ((u ^ (r & 7)) << 4));
-                        const int32_t tr = (warp & 3) * 32 + r, tok = t * (U / 2) + (tr >> lg);
-                        if (tok >= z.toks) continue;
-                        if (partial)
-                            __stcg(reinterpret_cast<uint4 *>(a.part + (prow + r) * kD + 32 * c) + u, w);
-                        else
-                            reinterpret_cast<uint4 *>(a.out + ((int64_t)(z.row + tok) * a.Hq + z.h * G + (tr & (G - 1))) * kD +
-                                                      64 * (c >> 1))[u] = w;
+                        __stcg(reinterpret_cast<uint4 *>(part + 4 * k * kD + c),
+                               *reinterpret_cast<const uint4 *>(turn + r * 128 + ((u ^ (r & 7)) << 4)));
                     }
                 }
             }
