@@ -169,7 +169,8 @@ def _nbytes(x) -> int:
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 3 us less than building a Stream object
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -181,14 +182,12 @@ def _check(status: int, what: str) -> None:
 
 
 def _operands(what: str, *specs) -> None:
-    """Refuses operands the raw pointers would misread: each spec is (tensor, dtype name, shape) with
-    None for a free extent; tensors must be contiguous and on the current CUDA device."""
+    """Refuses operands the raw pointers would misread: each spec is (tensor, dtype, shape); tensors must
+    be contiguous and on the current CUDA device."""
     import torch
-    current = torch.cuda.current_device() if torch.cuda.is_available() else None
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
     for x, dtype, shape in specs:
-        if x.dtype != getattr(torch, dtype) or x.dim() != len(shape) or not x.is_contiguous() or \
-                any(want is not None and have != want for have, want in zip(x.shape, shape)) or \
-                (x.is_cuda and x.device.index != current):
+        if x.dtype is not dtype or x.shape != shape or not x.is_contiguous() or x.get_device() != device:
             raise DGQError(-1, what)
 
 
@@ -388,15 +387,17 @@ def dgq_paged_decode_attn_bf16(q, k_new, v_new, k_src, v_src, src_block_tables, 
     """dgq_paged_decode_attn over an unquantised cache: k_src, v_src bf16 paged cache
     [num_src_blocks, Hkv, bs, 128] with src_block_tables int32 [B, max_src_blocks]; the other
     arguments and the workspace (dgq_attn_workspace_size) as there."""
+    from torch import bfloat16, int32
     B, Hq, D = q.shape
     blocks, Hkv, bs, _ = k_src.shape
-    _operands("dgq_paged_decode_attn_bf16", (q, "bfloat16", (B, Hq, D)), (k_new, "bfloat16", (B, Hkv, D)),
-              (v_new, "bfloat16", (B, Hkv, D)), (k_src, "bfloat16", (blocks, Hkv, bs, D)),
-              (v_src, "bfloat16", (blocks, Hkv, bs, D)), (src_block_tables, "int32", (B, None)),
-              (seq_lens, "int32", (B,)), (out, "bfloat16", (B, Hq, D)))
+    columns = src_block_tables.shape[1]
+    _operands("dgq_paged_decode_attn_bf16", (q, bfloat16, (B, Hq, D)), (k_new, bfloat16, (B, Hkv, D)),
+              (v_new, bfloat16, (B, Hkv, D)), (k_src, bfloat16, (blocks, Hkv, bs, D)),
+              (v_src, bfloat16, (blocks, Hkv, bs, D)), (src_block_tables, int32, (B, columns)),
+              (seq_lens, int32, (B,)), (out, bfloat16, (B, Hq, D)))
     _check(lib().dgq_paged_decode_attn_bf16(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_src), _ptr(v_src), blocks,
-                                            _ptr(src_block_tables), src_block_tables.shape[1],
-                                            _ptr(seq_lens), int(max_seqlen), B, Hq, Hkv, D, bs, _ptr(out),
+                                            _ptr(src_block_tables), columns, _ptr(seq_lens),
+                                            int(max_seqlen), B, Hq, Hkv, D, bs, _ptr(out),
                                             _ptr(workspace), _nbytes(workspace), _stream(stream)),
            "dgq_paged_decode_attn_bf16")
 
@@ -457,12 +458,12 @@ def dgq_prompt_attn(q, k, v, cu_q, cu_kv, out, workspace, stream=None) -> None:
     """Causal attention of packed prompts: q, out bf16 [Tq, Hq, 128]; k, v bf16 [Tkv, Hkv, 128]; cu_q,
     cu_kv int32 [B+1] (queries and keys of a request end at the same token); workspace uint8
     (dgq_prompt_attn_workspace_size bytes).  All CUDA tensors."""
+    from torch import bfloat16, int32
     Tq, Hq, D = q.shape
     T, Hkv, _ = k.shape
     B = cu_q.shape[0] - 1
-    _operands("dgq_prompt_attn", (q, "bfloat16", (Tq, Hq, D)), (k, "bfloat16", (T, Hkv, D)),
-              (v, "bfloat16", (T, Hkv, D)), (cu_q, "int32", (B + 1,)), (cu_kv, "int32", (B + 1,)),
-              (out, "bfloat16", (Tq, Hq, D)))
+    _operands("dgq_prompt_attn", (q, bfloat16, (Tq, Hq, D)), (k, bfloat16, (T, Hkv, D)), (v, bfloat16, (T, Hkv, D)),
+              (cu_q, int32, (B + 1,)), (cu_kv, int32, (B + 1,)), (out, bfloat16, (Tq, Hq, D)))
     _check(lib().dgq_prompt_attn(_ptr(q), _ptr(k), _ptr(v), Tq, T, _ptr(cu_q), _ptr(cu_kv),
                                  B, Hq, Hkv, D, _ptr(out), _ptr(workspace),
                                  _nbytes(workspace), _stream(stream)), "dgq_prompt_attn")
@@ -472,14 +473,15 @@ def dgq_prompt_attn_paged(q, cu_q, k_src, v_src, src_block_tables, seq_lens, out
     """dgq_prompt_attn over a bf16 paged cache: k_src, v_src bf16 [num_src_blocks, Hkv, bs, 128],
     src_block_tables int32 [B, max_src_blocks], seq_lens int32 [B] (keys of each request, the chunk's
     own among them); the rest as dgq_prompt_attn."""
+    from torch import bfloat16, int32
     Tq, Hq, D = q.shape
     blocks, Hkv, bs, _ = k_src.shape
-    B = seq_lens.shape[0]
-    _operands("dgq_prompt_attn_paged", (q, "bfloat16", (Tq, Hq, D)), (k_src, "bfloat16", (blocks, Hkv, bs, D)),
-              (v_src, "bfloat16", (blocks, Hkv, bs, D)), (cu_q, "int32", (B + 1,)), (seq_lens, "int32", (B,)),
-              (src_block_tables, "int32", (B, None)), (out, "bfloat16", (Tq, Hq, D)))
+    B, columns = src_block_tables.shape
+    _operands("dgq_prompt_attn_paged", (q, bfloat16, (Tq, Hq, D)), (k_src, bfloat16, (blocks, Hkv, bs, D)),
+              (v_src, bfloat16, (blocks, Hkv, bs, D)), (cu_q, int32, (B + 1,)), (seq_lens, int32, (B,)),
+              (src_block_tables, int32, (B, columns)), (out, bfloat16, (Tq, Hq, D)))
     _check(lib().dgq_prompt_attn_paged(_ptr(q), Tq, _ptr(cu_q), _ptr(k_src), _ptr(v_src), blocks,
-                                       _ptr(src_block_tables), src_block_tables.shape[1], _ptr(seq_lens), B, Hq, Hkv, D, bs, _ptr(out), _ptr(workspace),
+                                       _ptr(src_block_tables), columns, _ptr(seq_lens), B, Hq, Hkv, D, bs, _ptr(out), _ptr(workspace),
                                        _nbytes(workspace), _stream(stream)), "dgq_prompt_attn_paged")
 
 
@@ -492,23 +494,34 @@ def dgq_copy_pages(arrays, pairs, workspace, stream=None) -> None:
     first dimension: pools of any layers, or segment tables [B, Hkv, 128]; all with the same number
     and size of pages).  pairs: int32 CUDA tensor [n, 2] of (source, destination) ids, destinations
     distinct and none of them a source; workspace uint8 (dgq_copy_pages_workspace_size bytes)."""
+    import array
+    from operator import attrgetter
+
+    import torch
     arrays = list(arrays)
-    n = arrays[0].shape[0] if arrays else 1
-    size = _nbytes(arrays[0]) // max(n, 1) if arrays else 16
-    for a in arrays:
-        if a.shape[0] != n or _nbytes(a) != n * size or not a.is_contiguous():
+    count = len(arrays)
+    pages, nbytes, address = 1, 16, 0
+    _operands("dgq_copy_pages", (pairs, torch.int32, (pairs.shape[0], 2)))
+    if count:  # (a list of 64 pools: the checks run as C loops)
+        first = arrays[0]
+        pages, nbytes = first.shape[0], first.nbytes
+        if list(map(len, arrays)).count(pages) != count or \
+                list(map(attrgetter("nbytes"), arrays)).count(nbytes) != count or \
+                not all(map(torch.Tensor.is_contiguous, arrays)) or \
+                list(map(torch.Tensor.get_device, arrays)).count(pairs.get_device()) != count:
             raise DGQError(-1, "dgq_copy_pages")
-    _operands("dgq_copy_pages", (pairs, "int32", (None, 2)))
-    ptrs = (ctypes.c_void_p * max(len(arrays), 1))(*[_ptr(a) for a in arrays])
-    _check(lib().dgq_copy_pages(ptrs, len(arrays), size, n, _ptr(pairs), pairs.shape[0], _ptr(workspace),
-                                _nbytes(workspace), _stream(stream)), "dgq_copy_pages")
+        pointers = array.array("Q", map(torch.Tensor.data_ptr, arrays))
+        address = pointers.buffer_info()[0]
+    _check(lib().dgq_copy_pages(address, count, nbytes // max(pages, 1), pages, _ptr(pairs), pairs.shape[0],
+                                _ptr(workspace), _nbytes(workspace), _stream(stream)), "dgq_copy_pages")
 
 
 def dgq_remap_tables(tables, remap, out, workspace, stream=None) -> None:
     """out[...] = remap[tables[...]]: contiguous int32 CUDA tensors (out may be tables); remap int32
     [num_pages] as BlockPool.compact returns it; workspace as for dgq_copy_pages."""
-    _operands("dgq_remap_tables", (tables, "int32", tuple(tables.shape)), (out, "int32", tuple(tables.shape)),
-              (remap, "int32", (None,)))
+    from torch import int32
+    _operands("dgq_remap_tables", (tables, int32, tables.shape), (out, int32, tables.shape),
+              (remap, int32, (remap.numel(),)))
     _check(lib().dgq_remap_tables(_ptr(tables), tables.numel(), _ptr(remap), remap.numel(), _ptr(out),
                                   _ptr(workspace), _nbytes(workspace), _stream(stream)), "dgq_remap_tables")
 

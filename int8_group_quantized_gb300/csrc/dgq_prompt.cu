@@ -1218,6 +1218,8 @@ cudaError_t launch_prompt(const void *q, const void *k, const void *v, int32_t t
     prompt_kernel<<<(unsigned)nsm, kPmThreads, kPmSmem, stream>>>(a, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    // no request has a unit that may be cut: nothing to merge
+    if ((bt ? (int64_t)max_blocks * bs : (int64_t)total_kv) <= (2 * kPmSnap - 1) * kPmTile) return cudaSuccess;
 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)nsm, kPmMergeParts);
