@@ -491,8 +491,7 @@ def dgq_copy_pages_workspace_size() -> int:
 
 def dgq_copy_pages(arrays, pairs, workspace, stream=None) -> None:
     """Pages copied inside every array of `arrays` (contiguous CUDA tensors with the pages along the
-    first dimension: pools of any layers, or segment tables [B, Hkv, 128]; all with the same number
-    and size of pages).  pairs: int32 CUDA tensor [n, 2] of (source, destination) ids, destinations
+    first dimension: pools of any layers, or segment tables [B, Hkv, 128]; all of one shape and type).  pairs: int32 CUDA tensor [n, 2] of (source, destination) ids, destinations
     distinct and none of them a source; workspace uint8 (dgq_copy_pages_workspace_size bytes)."""
     import array
     from operator import attrgetter
@@ -505,8 +504,8 @@ def dgq_copy_pages(arrays, pairs, workspace, stream=None) -> None:
     if count:  # (a list of 64 pools: the checks run as C loops)
         first = arrays[0]
         pages, nbytes = first.shape[0], first.nbytes
-        if list(map(len, arrays)).count(pages) != count or \
-                list(map(attrgetter("nbytes"), arrays)).count(nbytes) != count or \
+        if list(map(torch.Tensor.size, arrays)).count(first.shape) != count or \
+                list(map(attrgetter("dtype"), arrays)).count(first.dtype) != count or \
                 not all(map(torch.Tensor.is_contiguous, arrays)) or \
                 list(map(torch.Tensor.get_device, arrays)).count(pairs.get_device()) != count:
             raise DGQError(-1, "dgq_copy_pages")
