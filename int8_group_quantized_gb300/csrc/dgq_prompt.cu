@@ -842,7 +842,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         for (PromptItem z; ok && next_item(z);) {
             const int32_t e = t ? z.e1 : z.e0;
             const bool has_row = rtok < z.toks;
-            int32_t left = has_row ? z.see + rtok : 0;  // columns from this key tile on that the row sees
+            // columns from this key tile on that the row sees (a row without a token, whose result nobody
+            // takes, sees all: it must not send the warp through the hiding of columns)
+            int32_t left = has_row ? z.see + rtok : 1 << 30;
             float m = -INFINITY, l = 0.0f;
             for (int32_t j = 0; j < e; ++j, left -= kPmTile) {
                 if (!pm_wait(smem_u32(&sb->s_full[t]), ns & 1u, a.hdr)) { ok = false; break; }
