@@ -1015,10 +1015,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                             make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
                     __syncwarp();
 #pragma unroll 4
-                    for (int k = 0; k < 8; ++k) {  // (rows without a token go along: nobody reads them)
+                    for (int k = 0; k < 8; ++k) {
                         const int r = 4 * k + (lane >> 3);
-                        __stcg(reinterpret_cast<uint4 *>(part + 4 * k * kD + c),
-                               *reinterpret_cast<const uint4 *>(turn + r * 128 + ((u ^ (r & 7)) << 4)));
+                        st_if(part + 4 * k * kD + c, *reinterpret_cast<const uint4 *>(turn + r * 128 + ((u ^ (r & 7)) << 4)),
+                              t * (U / 2) + (((warp & 3) * 32 + r) >> lg) < z.toks);
                     }
                 }
             }
