@@ -468,6 +468,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
 
     pdl_launch_dependents();  // the merge may be scheduled while this kernel runs
 
+    if (tid < 3) prefetch_tensormap(tid == 0 ? &maps.q : (tid == 1 ? &maps.k : &maps.v));
     // ---- this CTA's slice of the flat list
     {
         int64_t *pre = reinterpret_cast<int64_t *>(smem + 2 * kPmTileBytes);  // the ring is not in use yet
