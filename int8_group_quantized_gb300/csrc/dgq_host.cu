@@ -636,10 +636,8 @@ dgq_status dgq_copy_pages(void *const *arrays, int32_t num_arrays, int64_t page_
     if (!workspace || !aligned16(workspace) || workspace_bytes < dgq_copy_pages_workspace_size())
         return DGQ_ERR_WORKSPACE;
     if (num_arrays == 0 || num_pairs == 0) return DGQ_OK;
-    int nsm = 0;
-    if (device_sm_count(&nsm) != 0) return DGQ_ERR_CUDA;
     const cudaError_t e = dgq::launch_copy_pages(arrays, num_arrays, page_bytes, num_pages, pairs_dev, num_pairs,
-                                                 workspace, nsm, static_cast<cudaStream_t>(cuda_stream));
+                                                 workspace, static_cast<cudaStream_t>(cuda_stream));
     return e == cudaSuccess ? DGQ_OK : DGQ_ERR_CUDA;
 }
 

@@ -100,7 +100,7 @@ cudaError_t launch_prompt(const void *q, const void *k, const void *v, int32_t t
 
 // Pages copied by a list of (source, destination) ids in every array; table entries renamed.
 cudaError_t launch_copy_pages(void *const *arrays, int32_t num_arrays, int64_t page_bytes, int32_t num_pages,
-                              const int32_t *pairs, int32_t num_pairs, void *ws, int nsm, cudaStream_t stream);
+                              const int32_t *pairs, int32_t num_pairs, void *ws, cudaStream_t stream);
 cudaError_t launch_remap_tables(const int32_t *in, int64_t n, const int32_t *remap, int32_t num_pages, int32_t *out,
                                 void *ws, int nsm, cudaStream_t stream);
 
