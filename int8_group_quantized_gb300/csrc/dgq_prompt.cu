@@ -52,7 +52,7 @@ constexpr int kPmLoadWarp = 8, kPmMmaWarp = 9;
 constexpr int kPmUnitCost = 2 * kPmTile;          // a unit's fixed cost, in keys
 constexpr int kPmSnap = 4;                        // key tiles: no part of a cut unit is smaller
 constexpr int kPmRows = 2 * kPmTile;              // packed rows of a unit
-constexpr uint32_t kPmWaitPolls = 1u << 23;       // polls before a wait gives up: a second or more
+constexpr uint32_t kPmWaitPolls = 1u << 18;       // a poll suspends for up to 4 us: about a second
 
 // Tensor-memory columns of the 512 a CTA takes: S (and P) of tile 0 and 1, O of tile 0 and 1.
 constexpr uint32_t kPmColS = 0, kPmColO = 256;
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         if (!ok && lane == 0) {  // a wait ran out: no copy may still be in flight when the CTA ends
             auto drain = [](uint64_t *bar, uint32_t parity) {
 #pragma unroll 1
-                for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(bar, parity); ++i) {}
+                for (uint32_t i = 0; i < kPmWaitPolls && !mbar_try_wait(bar, parity); ++i) {}
             };
             for (uint32_t k = it > kPmStages ? it - kPmStages : 0; k < it; ++k)
                 drain(&sb->full[k % kPmStages], (k / kPmStages) & 1u);
@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         if (elect_one()) tc_commit(smem_u32(&sb->drain));
         __syncwarp();
 #pragma unroll 1
-        for (uint32_t i = 0; i < (1u << 24) && !mbar_try_wait(&sb->drain, 0); ++i) {}
+        for (uint32_t i = 0; i < kPmWaitPolls && !mbar_try_wait(&sb->drain, 0); ++i) {}
         __syncwarp();
     } else {
         // ======================================== softmax: tile t, this thread's row

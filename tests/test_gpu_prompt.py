@@ -192,6 +192,18 @@ def test_many_requests():
     verify(shape, 2, 1, seed=41, block=16)
 
 
+@pytest.mark.parametrize("n", [40, 64, 128, 200])
+def test_many_short_units_to_a_block(n):
+    # every thread block goes through a dozen units of one to four key tiles, one after the other
+    p = Prompt([(n, n)] * (12000 // n), 32, 8, seed=44).device()
+    out = p.run()
+    per = max(1, len(p.n) // 12)
+    for b in list(range(0, len(p.n), per)) + [len(p.n) - 1]:     # a dozen requests are looked at
+        ref, bound = prompt(p.q[b * n:(b + 1) * n], p.ks[b:b + 1], p.vs[b:b + 1], [n], 32, 8)
+        check(out[b * n:(b + 1) * n], ref, bound)
+    assert torch.equal(out, p.run())
+
+
 def test_chunks_of_a_prompt_equal_the_whole_within_the_bound():
     # the same prompt in three chunks against the pages written so far
     import int8_group_quantized_gb300 as dgq
