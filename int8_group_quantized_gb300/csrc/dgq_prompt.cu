@@ -522,10 +522,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         }
         __syncthreads();
         if (lane == 0 && warp < 2) {
-            const int64_t c = blockIdx.x + warp;
-            sb->cut[warp] = c == 0 ? cut_at(a, U, 0, pre)
-                                   : (c == gridDim.x ? PromptPos{a.B, 0, 0, 0}
-                                                     : cut_at(a, U, (int64_t)((carry / gridDim.x) * c + (carry % gridDim.x) * c / gridDim.x), pre));
+            const int64_t c = blockIdx.x + warp, n = gridDim.x, each = carry / n;  // (no overflow, exact at c = n)
+            sb->cut[warp] = cut_at(a, U, each * c + (carry - each * n) * c / n, pre);
         }
         __syncthreads();
     }
