@@ -36,11 +36,11 @@
  *     state, so calls from several threads at once are safe (each on its own stream and
  *     workspace, as above), on any number of devices.
  *   - CUDA graphs: every compute call (compress, decode, append, the prefill calls, the
- *     comparison formats) enqueues only kernel launches and workspace memsets on its stream,
- *     with no host synchronisation, so it may be captured into a graph on a capturing stream;
+ *     comparison formats, prompt attention, the page calls) enqueues only kernel launches and
+ *     workspace memsets on its stream, with no host synchronisation, so it may be captured into a graph on a capturing stream;
  *     a replay does what the call does.  Make one call on the device and host thread first
- *     (outside the capture) so that the launcher's per-device setup is done; the decode merge's
- *     programmatic dependent launch becomes a programmatic edge of the graph.
+ *     (outside the capture) so that the launcher's per-device setup is done; the programmatic
+ *     dependent launch of the decode and prompt merges becomes a programmatic edge of the graph.
  *     dgq_workspace_error reads the workspace back and synchronises: not inside a capture.
  */
 #ifndef DGQ_H
@@ -346,8 +346,11 @@ dgq_status dgq_paged_decode_attn_bf16(const void *q_bf16, const void *k_new_bf16
  * k_bf16, v_bf16    [total_kv, Hkv, 128] bf16, device, packed rows as dgq_compress reads them.
  * cu_q_dev, cu_kv_dev  [batch+1] int32, device, non-decreasing, at most total_q / total_kv (a
  *                   request that is not is flagged in the workspace and cut to the buffers).
- * Supported: Hq % Hkv == 0 with G = Hq / Hkv in {1, 2, 4, 8}.  A request's own rows must be finite;
- * rows of other requests, and behind the last one, cannot reach its output.
+ * Supported: Hq % Hkv == 0 with G = Hq / Hkv in {1, 2, 4, 8}; at most 2^30 keys or rows.  A request's
+ * own rows must be finite (a key that a row does not see has weight 0, and 0 times an infinite value
+ * is not a number); rows of other requests, and behind the last one, cannot reach its output.
+ * One launch of one block per SM (tensor memory and most of the shared memory of each), and one that
+ * merges the rows whose keys several blocks share, in a fixed order: bitwise repeatable on a given GPU.
  * workspace         >= dgq_prompt_attn_workspace_size(batch, Hq, Hkv) bytes, zero-filled before first use.
  */
 dgq_status dgq_prompt_attn(const void *q_bf16, const void *k_bf16, const void *v_bf16, int32_t total_q,

@@ -567,14 +567,14 @@ dgq_status prompt_impl(const void *q, const void *k, const void *v, int32_t tota
         return DGQ_ERR_INVALID_ARG;
     const int32_t G = num_q_heads / num_kv_heads;
     if (G != 1 && G != 2 && G != 4 && G != 8) return DGQ_ERR_UNSUPPORTED;
-    // grid: one row per KV head; keys, query rows and their heads are counted in 32 bits
-    if (num_kv_heads > 65535 || (int64_t)total_q * num_q_heads >= INT32_MAX ||
-        (int64_t)total_kv * num_kv_heads >= INT32_MAX)
+    // rows of all heads are counted in 32 bits, and a request's keys stay below 2^30
+    if ((int64_t)total_q * num_q_heads >= INT32_MAX || (int64_t)total_kv * num_kv_heads >= INT32_MAX ||
+        total_q > (1 << 30) || total_kv > (1 << 30))
         return DGQ_ERR_UNSUPPORTED;
     if (paged) {
         if (num_blocks <= 0 || max_blocks <= 0 || !bt || !aligned16(bt)) return DGQ_ERR_INVALID_ARG;
         if ((int64_t)num_blocks * num_kv_heads * block_size >= INT32_MAX ||
-            (int64_t)max_blocks * block_size >= INT32_MAX)
+            (int64_t)max_blocks * block_size > (1 << 30))
             return DGQ_ERR_UNSUPPORTED;
     }
     // an empty buffer has no address
@@ -627,8 +627,10 @@ dgq_status dgq_copy_pages(void *const *arrays, int32_t num_arrays, int64_t page_
 {
     if (num_arrays < 0 || num_pairs < 0 || page_bytes <= 0 || (page_bytes & 15) || num_pages <= 0)
         return DGQ_ERR_INVALID_ARG;
-    // units of 4 KB in a page are counted in 32 bits, bytes of an array in 64
-    if (page_bytes > ((int64_t)1 << 40) || page_bytes > INT64_MAX / num_pages) return DGQ_ERR_UNSUPPORTED;
+    // units of 4 KB in a page are counted in 32 bits, bytes of an array and units of a call in 64
+    if (page_bytes > ((int64_t)1 << 40) || page_bytes > INT64_MAX / num_pages ||
+        (int64_t)num_pairs > ((int64_t)1 << 50) / (page_bytes / 4096 + 1))
+        return DGQ_ERR_UNSUPPORTED;
     if ((num_arrays > 0 && !arrays) || (num_pairs > 0 && !pairs_dev) || !aligned16(pairs_dev))
         return DGQ_ERR_INVALID_ARG;
     for (int32_t i = 0; i < num_arrays; ++i)
@@ -679,7 +681,7 @@ dgq_pool *dgq_pool_create(int32_t num_blocks)
         p->free_list.resize(num_blocks);
         p->refs.assign(num_blocks, 0);
         p->mark.assign(num_blocks, 0);
-    } catch (const std::bad_alloc &) {
+    } catch (...) {  // (no exception leaves a C entry)
         delete p;
         return nullptr;
     }
