@@ -5,18 +5,31 @@
 // m - n + i and sees the keys t <= m - n + i:
 //   out[i] = sum_t softmax_t(q_i . k_t / sqrt(128)) v_t, zeros where the row sees no key (m < n).
 //
+// What bounds it.  4 * 128 flop per (row, key) pair against 512 bytes per key and KV head: the tensor
+// cores for prompts (one prompt of 16384 tokens, 32 query and 8 KV heads: 2.2 Tflop for 336 MB), HBM
+// for a few rows behind a long history.  Measured on a GB300: 1.25 ms for that prompt, 1750 TFLOP/s,
+// 94% of a cuBLAS product's burst rate (1.35 ms, 96% of the sustained rate, in a long run under the
+// power cap); 213 us for eight prompts of 2048; 95 us for sixteen short turns over 438 MB of cache.
+//
 // GPU design.
 //  * Rows: the G query heads of a KV head are packed into the rows of one product (row r of a tile is
 //    token r / G, head r % G), so a K and V tile is read once for the whole group.  A unit is two
 //    tiles of 128 rows (256 / G tokens of one KV head).
 //  * Products: S = Q K^T and O += P V on the fifth-generation tensor cores (tcgen05.mma, 128 x 128 x 16
 //    per instruction, fp32 accumulators in tensor memory).  Tensor memory holds S and O of both tiles
-//    (4 x 128 columns); P, rounded to bf16, overwrites the S it came from and is the A operand of the
-//    second product, so no weight passes through shared memory.  V is read as it lies (keys by
-//    values), a transposed B operand.
-//  * Roles: warp 8 loads (TMA, a ring of five 32 KB K or V tiles, 128-byte swizzle), one thread of warp
-//    9 issues every product, warps 0-3 and 4-7 are the softmax of tile 0 and of tile 1, one row per
-//    thread.  While one tile's softmax runs, the tensor cores work on the other's products.
+//    (4 x 128 columns, all of it); P, rounded to bf16, overwrites the S it came from and is the A
+//    operand of the second product, so no weight passes through shared memory.  V is read as it lies
+//    (keys by values), a transposed B operand.
+//  * Roles: warps 0-3 and 4-7 are the softmax of tile 0 and of tile 1, one row per thread; warp 8 loads
+//    (TMA, a ring of four 32 KB K or V tiles under the 128-byte swizzle; five measured the same) and
+//    hands the pieces of work to the others; one thread of warp 9 issues every product.  While one
+//    tile's softmax runs, the tensor cores work on the other's products.  (A product warp for each
+//    tile was slower, 1.78 against 1.52 ms: their products interleave, both tiles finish together and
+//    the tensor cores wait for both.  So was a warpgroup of its own for writing results.)
+//  * The code of all roles has to stay in the instruction cache, and there is next to no L1 left for
+//    spilled registers: unrolling the wait loops (200 KB of code) cost 25% on ragged batches, 200
+//    bytes of spills 30%.  The warp index goes through a shuffle so that the compiler knows the roles'
+//    branches are uniform: the products' operands then stay in uniform registers (1.40 -> 1.30 ms).
 //  * Softmax: online, log2 domain, the reference maximum moving only when a tile exceeds it by 8 (lazy
 //    rescaling: O in tensor memory is then multiplied in place; the softmax threads may do that
 //    between products because S of the next key tile is complete only after O's product is).
@@ -24,12 +37,12 @@
 //    each CTA (one per SM) takes an equal slice; a slice may begin and end inside a unit, at a key
 //    tile.  A unit cut that way leaves its parts' maxima, sums and unnormalised O in the workspace, and
 //    a merge kernel chained with programmatic dependent launch folds them in order (bitwise
-//    repeatable on a given GPU).  Cuts within kSnap key tiles of a unit's end move there.
+//    repeatable on a given GPU).  Cuts within kPmSnap key tiles of a unit's end move there.
 //  * What cannot be seen: columns past a row's limit get weight 0; V rows behind a request's end are
 //    zeroed in shared memory, so that values of other requests or of unused slots (NaN too) never
 //    meet a weight.
-//  * Every wait is bounded (two seconds): a wait that runs out records an error and raises a flag at which
-//    all roles leave.
+//  * Every wait is bounded: one that runs out records an error and its role leaves, after which the others'
+//    waits run out too.
 #include "dgq_device.cuh"
 #include "dgq.h"
 #include "dgq_launch.h"
@@ -49,7 +62,10 @@ constexpr int kPmTileBytes = kPmTile * kD * 2;    // 32 KB: two halves of 64 col
 constexpr int kPmHalf = kPmTileBytes / 2;
 constexpr int kPmThreads = 320;  // two softmax warpgroups, a load warp, a product warp
 constexpr int kPmLoadWarp = 8, kPmMmaWarp = 9;
-constexpr int kPmUnitCost = 2 * kPmTile;          // a unit's fixed cost, in keys
+// A unit's fixed cost, in keys.  Eight prompts of 2048 / ragged batch, us: 64 -> 216 / 167, 128 -> 213 / 162,
+// 256 -> 213 / 164, 384 -> 221 / 169, 512 -> 227 / 176; short turns over long histories, whose work is
+// cut most, do not depend on it, and one 16384-token prompt prefers 256 to 128 by 1%.
+constexpr int kPmUnitCost = 2 * kPmTile;
 constexpr int kPmSnap = 4;                        // key tiles: no part of a cut unit is smaller
 constexpr int kPmRows = 2 * kPmTile;              // packed rows of a unit
 constexpr uint32_t kPmWaitPolls = 1u << 18;       // a poll suspends for up to 4 us: about a second
@@ -1031,10 +1047,11 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
     }
 }
 
-// Merge of the units cut between CTAs: block (c, part) folds 16 rows of the unit whose first part is
-// CTA c's last piece, in CTA order; a warp takes two rows, four columns per lane, and has the parts
-// of kPmMergeDepth CTAs in flight.
-constexpr int kPmMergeParts = 16, kPmMergeWarps = 8, kPmMergeDepth = 4;
+// Merge of the units cut between CTAs: block (c, part) folds 32 rows of the unit whose first part is
+// CTA c's last piece, in CTA order; a warp takes four rows, four columns per lane, and has the parts
+// of kPmMergeDepth CTAs in flight.  Bound by the latency of its dependent reads: 7 to 10 us for the
+// parts of any call (eight rows a warp with one part in flight took 20 to 55).
+constexpr int kPmMergeParts = 8, kPmMergeWarps = 8, kPmMergeDepth = 8;
 constexpr int kPmMaxCtas = 1024;
 
 __global__ void __launch_bounds__(kPmMergeWarps * 32) prompt_merge_kernel(const PromptArgs a, int32_t ctas)
