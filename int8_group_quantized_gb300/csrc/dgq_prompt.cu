@@ -179,8 +179,10 @@ __device__ PromptPos cut_at(const PromptArgs &a, int32_t U, int64_t pos, const i
     const int64_t per_head = unit_cost(s, U, nu);
     int64_t r = pos - pre[lo];
     p.b = lo;
-    p.h = (int32_t)(r / per_head);
+    p.h = (int32_t)__fdividef((float)r, (float)per_head);  // off by one at most below a million heads
     r -= p.h * per_head;
+    for (; r < 0; r += per_head) --p.h;
+    for (; r >= per_head; r -= per_head) ++p.h;
     lo = 0;
     hi = nu - 1;
     while (lo < hi) {
@@ -361,6 +363,13 @@ __device__ __forceinline__ float pm_ex2(float x)
     return y;
 }
 
+__device__ __forceinline__ float pm_rcp(float x)  // to one unit in the last place
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float y;
@@ -538,8 +547,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         }
         __syncthreads();
         if (lane == 0 && warp < 2) {
-            const int64_t c = blockIdx.x + warp, n = gridDim.x, each = carry / n;  // (no overflow, exact at c = n)
-            sb->cut[warp] = cut_at(a, U, each * c + (carry - each * n) * c / n, pre);
+            // carry * c / n in steps of 2^-20 (monotone, exact at c = n, no 64-bit division: one took 400 cycles)
+            const int64_t f = (uint32_t)((blockIdx.x + warp) << 20) / gridDim.x;
+            sb->cut[warp] = cut_at(a, U, (carry >> 20) * f + (((carry & 0xfffff) * f) >> 20), pre);
         }
         __syncthreads();
     }
@@ -973,7 +983,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             }
             const int64_t prow = (int64_t)z.slot * kPmRows + t * kPmTile + (warp & 3) * 32;
             if (partial && has_row) __stcg(a.ml + prow + lane, make_float2(m, l));
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;  // (a row that sees no key: 0)
+            const float inv = l > 0.0f ? pm_rcp(l) : 0.0f;  // (a row that sees no key: its O is 0 too)
             uint8_t *mine = turn + lane * 128;  // 16-byte unit u of row r lies at unit u ^ r % 8
             const int u = lane & 7;
             if (!partial) {
@@ -988,17 +998,21 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                     __syncwarp();
 #pragma unroll
                     for (int v = 0; v < 8; ++v) {
-                        if (e > 0 && (v & 3) == 0) {
-                            tc_ld32(to + c + 8 * v, o);
-                            tc_wait_ld();
+                        if ((v & 3) == 0) {
+                            if (e > 0) {
+                                tc_ld32(to + c + 8 * v, o);
+                                tc_wait_ld();
+                            } else {  // no key tile
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] = 0u;
+                            }
                         }
-                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                        if (l > 0.0f) {
-                            w.x = pm_pack_bf16(__uint_as_float(o[8 * (v & 3)]) * inv, __uint_as_float(o[8 * (v & 3) + 1]) * inv);
-                            w.y = pm_pack_bf16(__uint_as_float(o[8 * (v & 3) + 2]) * inv, __uint_as_float(o[8 * (v & 3) + 3]) * inv);
-                            w.z = pm_pack_bf16(__uint_as_float(o[8 * (v & 3) + 4]) * inv, __uint_as_float(o[8 * (v & 3) + 5]) * inv);
-                            w.w = pm_pack_bf16(__uint_as_float(o[8 * (v & 3) + 6]) * inv, __uint_as_float(o[8 * (v & 3) + 7]) * inv);
-                        }
+                        const int k = 8 * (v & 3);
+                        uint4 w;
+                        w.x = pm_pack_bf16(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv);
+                        w.y = pm_pack_bf16(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv);
+                        w.z = pm_pack_bf16(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv);
+                        w.w = pm_pack_bf16(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv);
                         *reinterpret_cast<uint4 *>(mine + ((v ^ (lane & 7)) << 4)) = w;
                     }
                     __syncwarp();
@@ -1006,7 +1020,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         w[k] = *reinterpret_cast<const uint4 *>(from + k * 512 + ((u ^ ((4 * k + (lane >> 3)) & 7)) << 4));
-                    uint16_t *out = a.out + ((int64_t)(z.row + tok0) * a.Hq + z.h * G + (r0 & (G - 1))) * kD + u * 8 + c;
+                    uint16_t *out = a.out + (int64_t)((z.row + tok0) * a.Hq + z.h * G + (r0 & (G - 1))) * kD + u * 8 + c;
                     int32_t tok = tok0;
 #pragma unroll
                     for (int k = 0; k < 8; k += 2) {
@@ -1052,7 +1066,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
 // of kPmMergeDepth CTAs in flight.  Bound by the latency of its dependent reads: 7 to 10 us for the
 // parts of any call (eight rows a warp with one part in flight took 20 to 55).
 constexpr int kPmMergeParts = 8, kPmMergeWarps = 8, kPmMergeDepth = 8;
-constexpr int kPmMaxCtas = 1024;
+constexpr int kPmMaxCtas = 1024;  // (c << 20 fits 32 bits in the slice search)
 
 __global__ void __launch_bounds__(kPmMergeWarps * 32) prompt_merge_kernel(const PromptArgs a, int32_t ctas)
 {
