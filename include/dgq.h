@@ -37,7 +37,8 @@
  *     workspace, as above), on any number of devices.
  *   - CUDA graphs: every compute call (compress, decode, append, the prefill calls, the
  *     comparison formats, prompt attention, the page calls) enqueues only kernel launches and
- *     workspace memsets on its stream, with no host synchronisation, so it may be captured into a graph on a capturing stream;
+ *     workspace memsets on its stream, with no host synchronisation, so it may be captured into
+ *     a graph on a capturing stream;
  *     a replay does what the call does.  Make one call on the device and host thread first
  *     (outside the capture) so that the launcher's per-device setup is done; the programmatic
  *     dependent launch of the decode and prompt merges becomes a programmatic edge of the graph.

@@ -181,11 +181,13 @@ def _check(status: int, what: str) -> None:
         raise DGQError(status, what)
 
 
-def _operands(what: str, *specs) -> None:
-    """Refuses operands the raw pointers would misread: each spec is (tensor, dtype, shape); tensors must
-    be contiguous and on the current CUDA device."""
+def _operands(what: str, workspace, *specs) -> None:
+    """Refuses operands the raw pointers would misread: each spec is (tensor, dtype, shape); tensors, and
+    the workspace, must be contiguous and on the current CUDA device."""
     import torch
     device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    if not workspace.is_contiguous() or workspace.get_device() != device:
+        raise DGQError(-1, what)
     for x, dtype, shape in specs:
         if x.dtype is not dtype or x.shape != shape or not x.is_contiguous() or x.get_device() != device:
             raise DGQError(-1, what)
@@ -391,7 +393,7 @@ def dgq_paged_decode_attn_bf16(q, k_new, v_new, k_src, v_src, src_block_tables, 
     B, Hq, D = q.shape
     blocks, Hkv, bs, _ = k_src.shape
     columns = src_block_tables.shape[1]
-    _operands("dgq_paged_decode_attn_bf16", (q, bfloat16, (B, Hq, D)), (k_new, bfloat16, (B, Hkv, D)),
+    _operands("dgq_paged_decode_attn_bf16", workspace, (q, bfloat16, (B, Hq, D)), (k_new, bfloat16, (B, Hkv, D)),
               (v_new, bfloat16, (B, Hkv, D)), (k_src, bfloat16, (blocks, Hkv, bs, D)),
               (v_src, bfloat16, (blocks, Hkv, bs, D)), (src_block_tables, int32, (B, columns)),
               (seq_lens, int32, (B,)), (out, bfloat16, (B, Hq, D)))
@@ -462,8 +464,8 @@ def dgq_prompt_attn(q, k, v, cu_q, cu_kv, out, workspace, stream=None) -> None:
     Tq, Hq, D = q.shape
     T, Hkv, _ = k.shape
     B = cu_q.shape[0] - 1
-    _operands("dgq_prompt_attn", (q, bfloat16, (Tq, Hq, D)), (k, bfloat16, (T, Hkv, D)), (v, bfloat16, (T, Hkv, D)),
-              (cu_q, int32, (B + 1,)), (cu_kv, int32, (B + 1,)), (out, bfloat16, (Tq, Hq, D)))
+    _operands("dgq_prompt_attn", workspace, (q, bfloat16, (Tq, Hq, D)), (k, bfloat16, (T, Hkv, D)),
+              (v, bfloat16, (T, Hkv, D)), (cu_q, int32, (B + 1,)), (cu_kv, int32, (B + 1,)), (out, bfloat16, (Tq, Hq, D)))
     _check(lib().dgq_prompt_attn(_ptr(q), _ptr(k), _ptr(v), Tq, T, _ptr(cu_q), _ptr(cu_kv),
                                  B, Hq, Hkv, D, _ptr(out), _ptr(workspace),
                                  _nbytes(workspace), _stream(stream)), "dgq_prompt_attn")
@@ -477,12 +479,12 @@ def dgq_prompt_attn_paged(q, cu_q, k_src, v_src, src_block_tables, seq_lens, out
     Tq, Hq, D = q.shape
     blocks, Hkv, bs, _ = k_src.shape
     B, columns = src_block_tables.shape
-    _operands("dgq_prompt_attn_paged", (q, bfloat16, (Tq, Hq, D)), (k_src, bfloat16, (blocks, Hkv, bs, D)),
+    _operands("dgq_prompt_attn_paged", workspace, (q, bfloat16, (Tq, Hq, D)), (k_src, bfloat16, (blocks, Hkv, bs, D)),
               (v_src, bfloat16, (blocks, Hkv, bs, D)), (cu_q, int32, (B + 1,)), (seq_lens, int32, (B,)),
               (src_block_tables, int32, (B, columns)), (out, bfloat16, (Tq, Hq, D)))
     _check(lib().dgq_prompt_attn_paged(_ptr(q), Tq, _ptr(cu_q), _ptr(k_src), _ptr(v_src), blocks,
-                                       _ptr(src_block_tables), columns, _ptr(seq_lens), B, Hq, Hkv, D, bs, _ptr(out), _ptr(workspace),
-                                       _nbytes(workspace), _stream(stream)), "dgq_prompt_attn_paged")
+                                       _ptr(src_block_tables), columns, _ptr(seq_lens), B, Hq, Hkv, D, bs,
+                                       _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream)), "dgq_prompt_attn_paged")
 
 
 def dgq_copy_pages_workspace_size() -> int:
@@ -491,8 +493,9 @@ def dgq_copy_pages_workspace_size() -> int:
 
 def dgq_copy_pages(arrays, pairs, workspace, stream=None) -> None:
     """Pages copied inside every array of `arrays` (contiguous CUDA tensors with the pages along the
-    first dimension: pools of any layers, or segment tables [B, Hkv, 128]; all of one shape and type).  pairs: int32 CUDA tensor [n, 2] of (source, destination) ids, destinations
-    distinct and none of them a source; workspace uint8 (dgq_copy_pages_workspace_size bytes)."""
+    first dimension: pools of any layers, or segment tables [B, Hkv, 128]; all of one shape and type).
+    pairs: int32 CUDA tensor [n, 2] of (source, destination) ids, destinations distinct and none of them
+    a source; workspace uint8 (dgq_copy_pages_workspace_size bytes)."""
     import array
     from operator import attrgetter
 
@@ -500,7 +503,7 @@ def dgq_copy_pages(arrays, pairs, workspace, stream=None) -> None:
     arrays = list(arrays)
     count = len(arrays)
     pages, nbytes, address = 1, 16, 0
-    _operands("dgq_copy_pages", (pairs, torch.int32, (pairs.shape[0], 2)))
+    _operands("dgq_copy_pages", workspace, (pairs, torch.int32, (pairs.shape[0], 2)))
     if count:  # (a list of 64 pools: the checks run as C loops)
         first = arrays[0]
         pages, nbytes = first.shape[0], first.nbytes
@@ -519,7 +522,7 @@ def dgq_remap_tables(tables, remap, out, workspace, stream=None) -> None:
     """out[...] = remap[tables[...]]: contiguous int32 CUDA tensors (out may be tables); remap int32
     [num_pages] as BlockPool.compact returns it; workspace as for dgq_copy_pages."""
     from torch import int32
-    _operands("dgq_remap_tables", (tables, int32, tables.shape), (out, int32, tables.shape),
+    _operands("dgq_remap_tables", workspace, (tables, int32, tables.shape), (out, int32, tables.shape),
               (remap, int32, (remap.numel(),)))
     _check(lib().dgq_remap_tables(_ptr(tables), tables.numel(), _ptr(remap), remap.numel(), _ptr(out),
                                   _ptr(workspace), _nbytes(workspace), _stream(stream)), "dgq_remap_tables")

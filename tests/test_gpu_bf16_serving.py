@@ -121,3 +121,22 @@ def test_prompt_decode_compress_fork_append_free_compact():
     assert torch.equal(decode(bt.cpu().numpy(), forked, [n + 1 for n in lens]), grown)
     for w in (ws, aws, cws, pws):
         assert dgq.dgq_workspace_error(w) == 0
+
+
+def test_workspace_outside_the_current_device_is_refused():
+    """A workspace in host memory, or one with gaps, is refused by every call before anything is launched."""
+    import int8_group_quantized_gb300 as dgq
+    q, kv = rows(4, HQ, 1).cuda(), rows(4, HKV, 2).cuda()
+    src = Pages([rows(4, HKV, 3)], [rows(4, HKV, 4)], HKV, BS).cuda()
+    cu, one, ids = i32([0, 4]), i32([3]), i32([[0, 0]])
+    out = torch.full_like(q, 7.0)
+    size = max(dgq.dgq_prompt_attn_workspace_size(1, HQ, HKV), dgq.dgq_attn_workspace_size(4, HQ, HKV, 16))
+    for bad in (torch.zeros(size, dtype=torch.uint8), zeros(2 * size)[::2]):
+        for call in (lambda: dgq.dgq_prompt_attn(q, kv, kv, cu, cu, out, bad),
+                     lambda: dgq.dgq_prompt_attn_paged(q, cu, src.k, src.v, src.table, src.lens, out, bad),
+                     lambda: dgq.dgq_paged_decode_attn_bf16(q[:1], kv[:1], kv[:1], src.k, src.v, src.table, one, 16, out[:1], bad),
+                     lambda: dgq.dgq_copy_pages([src.k], ids, bad),
+                     lambda: dgq.dgq_remap_tables(src.table, one, src.table, bad)):
+            with pytest.raises(dgq.DGQError):
+                call()
+    assert torch.all(out == 7.0)
