@@ -34,7 +34,9 @@ struct WsHeader {
     uint32_t error;        // first device-side error code (0 = none)
     uint32_t path;         // which kernel path the last call took (kPath*), for tests
     uint32_t done_ctas;    // CTAs finished in the current call (compress)
-    uint32_t pad[61];
+    uint32_t tickets;      // units handed out in the current call behind each CTA's first (prompt)
+    uint32_t ended_ctas;   // CTAs finished in the current call (prompt)
+    uint32_t pad[59];
 };
 static_assert(sizeof(WsHeader) == 256, "workspace header must be 256 bytes");
 

@@ -9,7 +9,7 @@
 // cores for prompts (one prompt of 16384 tokens, 32 query and 8 KV heads: 2.2 Tflop for 336 MB), HBM
 // for a few rows behind a long history.  Measured on a GB300: 1.25 ms for that prompt, 1750 TFLOP/s,
 // 94% of a cuBLAS product's burst rate (1.35 ms, 96% of the sustained rate, in a long run under the
-// power cap); 213 us for eight prompts of 2048; 95 us for sixteen short turns over 438 MB of cache.
+// power cap); 202 us for eight prompts of 2048; 88 us for sixteen short turns over 438 MB of cache.
 //
 // GPU design.
 //  * Rows: the G query heads of a KV head are packed into the rows of one product (row r of a tile is
@@ -33,11 +33,17 @@
 //  * Softmax: online, log2 domain, the reference maximum moving only when a tile exceeds it by 8 (lazy
 //    rescaling: O in tensor memory is then multiplied in place; the softmax threads may do that
 //    between products because S of the next key tile is complete only after O's product is).
-//  * Work: all units lie in one flat list by cost, a unit costing the keys it sees plus a constant, and
-//    each CTA (one per SM) takes an equal slice; a slice may begin and end inside a unit, at a key
-//    tile.  A unit cut that way leaves its parts' maxima, sums and unnormalised O in the workspace, and
-//    a merge kernel chained with programmatic dependent launch folds them in order (bitwise
-//    repeatable on a given GPU).  Cuts within kPmSnap key tiles of a unit's end move there.
+//  * Work where a CTA's share (one per SM) is at least kPmQueued times the longest unit: the load warps
+//    draw whole units from a counter, a request's longest first, the next number while a unit is loaded.
+//    All CTAs then work in few requests at a time, whose K and V stay in L2, and the short units at the
+//    end level them out; which CTA has a unit changes no result.  Against slices (below), us with launch:
+//    213 -> 202 for eight prompts of 2048, 164 -> 152 for the ragged batch, 213 -> 195 for eight chunks of
+//    512 behind 3584.
+//  * Else the units lie in one flat list by cost, a unit costing the keys it sees plus a constant, and
+//    each CTA takes an equal slice, which may begin and end inside a unit, at a key tile.  A unit cut
+//    that way leaves its parts' maxima, sums and unnormalised O in the workspace, and a merge kernel
+//    chained with programmatic dependent launch folds them in order (bitwise repeatable on a given
+//    GPU).  Cuts within kPmSnap key tiles of a unit's end move there.
 //  * What cannot be seen: columns past a row's limit get weight 0; V rows behind a request's end are
 //    zeroed in shared memory, so that values of other requests or of unused slots (NaN too) never
 //    meet a weight.
@@ -62,11 +68,15 @@ constexpr int kPmTileBytes = kPmTile * kD * 2;    // 32 KB: two halves of 64 col
 constexpr int kPmHalf = kPmTileBytes / 2;
 constexpr int kPmThreads = 320;  // two softmax warpgroups, a load warp, a product warp
 constexpr int kPmLoadWarp = 8, kPmMmaWarp = 9;
-// A unit's fixed cost, in keys.  Eight prompts of 2048 / ragged batch, us: 64 -> 216 / 167, 128 -> 213 / 162,
-// 256 -> 213 / 164, 384 -> 221 / 169, 512 -> 227 / 176; short turns over long histories, whose work is
-// cut most, do not depend on it, and one 16384-token prompt prefers 256 to 128 by 1%.
-constexpr int kPmUnitCost = 2 * kPmTile;
-constexpr int kPmSnap = 4;                        // key tiles: no part of a cut unit is smaller
+// A unit's fixed cost, in keys, and what a key tile costs where only tile 0 has rows (it takes 0.76 to 0.85
+// of the time of both).  Sixteen short turns behind up to 32768, us with launch: 128 -> 106, 160 -> 100,
+// 192 -> 102; all key tiles alike 108.
+constexpr int kPmUnitCost = 160, kPmLoneTile = 104;
+// Key tiles: no part of a cut unit is smaller.  The same turns: 1 -> 101, 2 -> 100, 4 -> 102.
+constexpr int kPmSnap = 2;
+// Shares from which on units are drawn from a counter.  464 units of one length (58 requests, 3.05 to a
+// CTA) take as long as in slices, 124 us with launch; at two, 2 prompts of 2048 do, 77 us.
+constexpr int kPmQueued = 3;
 constexpr int kPmRows = 2 * kPmTile;              // packed rows of a unit
 constexpr uint32_t kPmWaitPolls = 1u << 18;       // a poll suspends for up to 4 us: about a second
 
@@ -140,14 +150,25 @@ __device__ __forceinline__ int32_t keys_before(const PromptSeq &s, int32_t tok)
 
 __device__ __forceinline__ int32_t key_tiles(int32_t keys) { return (keys + kPmTile - 1) / kPmTile; }
 
-// Cost of a head's first i units: kPmUnitCost each and max(0, off + x U) for x = 1 .. i (the last unit
-// counted as if it were full).
+// Cost of a head's first i units (the last one not among them): kPmUnitCost each and the keys of its
+// last token, max(0, off + x U) for unit x = 1 .. i.
 __device__ __forceinline__ int64_t unit_cost(const PromptSeq &s, int32_t U, int32_t i)
 {
     const int32_t off = s.m - s.n;
     const int64_t x0 = off >= 0 ? 0 : min(i, -off / U);  // units that see no key
     const int64_t c = (int64_t)i - x0;
     return (int64_t)i * kPmUnitCost + c * off + U * (((int64_t)i * (i + 1) - x0 * (x0 + 1)) / 2);
+}
+
+// A head's last unit sees all keys; where it has rows in tile 0 only, a key tile costs kPmLoneTile.
+__device__ __forceinline__ bool lone_tile(const PromptSeq &s, int32_t U, int32_t nu) { return s.n - (nu - 1) * U <= U / 2; }
+
+// Cost of a head with nu units.
+__device__ __forceinline__ int64_t head_cost(const PromptSeq &s, int32_t U, int32_t nu)
+{
+    if (nu == 0) return 0;
+    const int64_t last = lone_tile(s, U, nu) ? (int64_t)s.m * kPmLoneTile / kPmTile : s.m;
+    return unit_cost(s, U, nu - 1) + kPmUnitCost + last;
 }
 
 __device__ __forceinline__ void next_unit(const PromptArgs &a, int32_t U, PromptPos &p, PromptSeq &s)
@@ -160,6 +181,52 @@ __device__ __forceinline__ void next_unit(const PromptArgs &a, int32_t U, Prompt
     while (++p.b < a.B) {
         s = prompt_seq(a, p.b, false);
         if (s.n > 0) return;
+    }
+}
+
+// The units drawn one by one, a request's longest first: the requests in a window of 32, one per lane.
+struct PromptQueue {
+    PromptSeq s;    // this lane's request
+    int64_t upto;   // units of the window's requests up to it
+    int64_t base;   // units before the window
+    int32_t first;  // the window's first request
+};
+
+__device__ __forceinline__ void queue_window(const PromptArgs &a, int32_t U, int lane, PromptQueue &w)
+{
+    w.s = PromptSeq{0, 0, 0, 0};
+    if (w.first + lane < a.B) w.s = prompt_seq(a, w.first + lane, false);
+    w.upto = (int64_t)prompt_units(w.s, U) * a.Hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, w.upto, o);
+        if (lane >= o) w.upto += y;
+    }
+}
+
+// Unit number `ticket` and its request, or false: there are not so many (the whole warp; tickets only rise).
+__device__ __forceinline__ bool queue_unit(const PromptArgs &a, int32_t U, int lane, PromptQueue &w, int64_t ticket,
+                                           PromptPos &p, PromptSeq &s)
+{
+    for (;;) {
+        const uint32_t hit = __ballot_sync(0xffffffffu, w.base + w.upto > ticket);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            s.q0 = __shfl_sync(0xffffffffu, w.s.q0, l);
+            s.n = __shfl_sync(0xffffffffu, w.s.n, l);
+            s.kv0 = __shfl_sync(0xffffffffu, w.s.kv0, l);
+            s.m = __shfl_sync(0xffffffffu, w.s.m, l);
+            const int32_t back = (int32_t)(w.base + __shfl_sync(0xffffffffu, w.upto, l) - ticket) - 1;  // from the request's end
+            p.b = w.first + l;
+            p.i = back / a.Hkv;
+            p.h = back - p.i * a.Hkv;
+            p.j = 0;
+            return true;
+        }
+        w.base += __shfl_sync(0xffffffffu, w.upto, 31);
+        w.first += 32;
+        if (w.first >= a.B) return false;
+        queue_window(a, U, lane, w);
     }
 }
 
@@ -176,7 +243,7 @@ __device__ PromptPos cut_at(const PromptArgs &a, int32_t U, int64_t pos, const i
     }
     PromptSeq s = prompt_seq(a, lo, false);  // has units: the next prefix is larger
     const int32_t nu = prompt_units(s, U);
-    const int64_t per_head = unit_cost(s, U, nu);
+    const int64_t per_head = head_cost(s, U, nu);
     int64_t r = pos - pre[lo];
     p.b = lo;
     p.h = (int32_t)__fdividef((float)r, (float)per_head);  // off by one at most below a million heads
@@ -193,7 +260,7 @@ __device__ PromptPos cut_at(const PromptArgs &a, int32_t U, int64_t pos, const i
     p.i = lo;
     r -= unit_cost(s, U, lo) + kPmUnitCost;
     const int32_t tiles = key_tiles(keys_before(s, (lo + 1) * U));
-    int32_t j = r > 0 ? (int32_t)(r / kPmTile) : 0;
+    int32_t j = r > 0 ? (int32_t)r / (lo == nu - 1 && lone_tile(s, U, nu) ? kPmLoneTile : kPmTile) : 0;  // (r <= m < 2^31)
     if (j > tiles - kPmSnap) {
         if (j >= kPmSnap || r > 0) next_unit(a, U, p, s);
         return p;
@@ -436,6 +503,7 @@ struct PromptBars {
     uint32_t tmem;
     PromptPos cut[2];
     int64_t wsum[kPmThreads / 32];
+    int32_t wmax[kPmThreads / 32];
 };
 
 constexpr int kPmTurn = 32 * 128;  // a softmax warp's buffer for turning rows
@@ -494,16 +562,19 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
     pdl_launch_dependents();  // the merge may be scheduled while this kernel runs
 
     if (tid < 3) prefetch_tensormap(tid == 0 ? &maps.q : (tid == 1 ? &maps.k : &maps.v));
-    // ---- this CTA's slice of the flat list
+    // ---- this CTA's slice of the flat list, or whether units are handed out one by one
+    bool queued;
     {
         int64_t *pre = reinterpret_cast<int64_t *>(smem + 2 * kPmTileBytes);  // the ring is not in use yet
         int64_t carry = 0;
+        int32_t longest = 0;
         for (int32_t base = 0; base < a.B; base += kPmThreads) {
             const int32_t b = base + tid;
             int64_t c = 0;
             if (b < a.B) {
                 const PromptSeq s = prompt_seq(a, b, blockIdx.x == 0);
-                c = a.Hkv * unit_cost(s, U, prompt_units(s, U));
+                c = a.Hkv * head_cost(s, U, prompt_units(s, U));
+                if (s.n > 0) longest = max(longest, s.m);
             }
             int64_t x = c;
 #pragma unroll
@@ -523,6 +594,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             carry += all;
             __syncthreads();
         }
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 0) sb->wmax[warp] = longest;
         if (tid == 0) {
             pre[a.B] = carry;
             for (int i = 0; i < kPmStages; ++i) {
@@ -546,7 +619,12 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             fence_barrier_init();
         }
         __syncthreads();
-        if (lane == 0 && warp < 2) {
+#pragma unroll
+        for (int w = 0; w < kPmThreads / 32; ++w) longest = max(longest, sb->wmax[w]);
+        queued = ((int64_t)longest + kPmUnitCost) * (kPmQueued * gridDim.x) <= carry;
+        if (queued) {
+            if (lane == 0 && warp < 2) sb->cut[warp] = PromptPos{warp ? a.B : 0, 0, 0, 0};
+        } else if (lane == 0 && warp < 2) {
             // carry * c / n in steps of 2^-20 (monotone, exact at c = n, no 64-bit division: one took 400 cycles)
             const int64_t f = (uint32_t)((blockIdx.x + warp) << 20) / gridDim.x;
             sb->cut[warp] = cut_at(a, U, (carry >> 20) * f + (((carry & 0xfffff) * f) >> 20), pre);
@@ -554,7 +632,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         __syncthreads();
     }
     const PromptPos begin = sb->cut[0], end = sb->cut[1];
-    const bool work = before(begin, end);
+    const bool work = before(begin, end);  // (queued: any)
     if (tid == 0) {  // read by the merge
         const bool one = same_unit(begin, end);
         int4 head = make_int4(0, 0, 0, 0);
@@ -594,7 +672,26 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
     if (warp == kPmLoadWarp) {
         // ======================================== pieces and their loads
         PromptPos pos = begin;
-        PromptSeq s = prompt_seq(a, pos.b, false);
+        PromptSeq s;
+        PromptQueue queue;
+        uint32_t ticket = 0;  // (lane 0)
+        bool more = true;
+        if (queued) {
+            queue.base = 0;
+            queue.first = 0;
+            queue_window(a, U, lane, queue);
+            more = queue_unit(a, U, lane, queue, blockIdx.x, pos, s);
+        } else {
+            s = prompt_seq(a, pos.b, false);
+        }
+        auto advance = [&]() {
+            if (queued) {
+                more = queue_unit(a, U, lane, queue, (int64_t)gridDim.x + __shfl_sync(0xffffffffu, ticket, 0), pos, s);
+            } else {
+                next_unit(a, U, pos, s);
+                more = before(pos, end);
+            }
+        };
         auto hand_out = [&](const PromptItem &z) -> bool {
             const uint32_t i = ni % kPmItems;
             if (ni >= kPmItems && !pm_wait(smem_u32(&sb->item_empty[i]), (ni / kPmItems - 1) & 1u, a.hdr))
@@ -631,7 +728,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             }
             return true;
         };
-        for (bool first = true; ok && before(pos, end); next_unit(a, U, pos, s), first = false) {
+        for (bool first = true; ok && more; advance(), first = false) {
+            if (queued && lane == 0) ticket = atomicAdd(&a.hdr->tickets, 1u);  // of the next unit
             const PromptPiece z = piece_of(s, pos, end, U);
             const int32_t toks = s.n - pos.i * U, row0 = s.q0 + pos.i * U;
             if (z.steps == 0) {  // rows that see no key
@@ -1055,6 +1153,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         }
     }
     __syncthreads();
+    if (queued && tid == 0 && atomicAdd(&a.hdr->ended_ctas, 1u) + 1u == gridDim.x) {  // the last one: for the next call
+        a.hdr->tickets = 0u;
+        a.hdr->ended_ctas = 0u;
+    }
     if (warp == kPmMmaWarp) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));

@@ -4,6 +4,7 @@ histories, every group size, rows that see no key, values outside the requests, 
 graphs, streams and threads."""
 import threading
 
+import numpy as np
 import pytest
 import torch
 
@@ -202,6 +203,46 @@ def test_many_short_units_to_a_block(n):
         ref, bound = prompt(p.q[b * n:(b + 1) * n], p.ks[b:b + 1], p.vs[b:b + 1], [n], 32, 8)
         check(out[b * n:(b + 1) * n], ref, bound)
     assert torch.equal(out, p.run())
+
+
+def drawn(block, seed=0):
+    """A batch whose units are drawn from the counter: 80 requests, some of them empty, the last ones too."""
+    g = np.random.default_rng(seed)
+    n = [0 if b % 7 == 3 or b >= 76 else int(g.integers(1, 201)) for b in range(80)]
+    m = [x + int(g.integers(0, 3)) * 50 - (30 if b % 11 == 0 and x > 40 else 0) for b, x in enumerate(n)]
+    return Prompt(list(zip(n, m)), 64, 8, seed=46, block=block)
+
+
+@pytest.mark.parametrize("block", [None, 16])
+def test_units_drawn_from_a_counter(block):
+    p = drawn(block).device()
+    out = p.run()
+    start = np.concatenate([[0], np.cumsum(p.n)])
+    for b in list(range(0, 80, 9)) + [33, 75]:
+        if p.n[b]:
+            lo, hi = int(start[b]), int(start[b + 1])
+            ref, bound = prompt(p.q[lo:hi], p.ks[b:b + 1], p.vs[b:b + 1], [p.n[b]], 64, 8)
+            check(out[lo:hi], ref, bound)
+    for _ in range(3):      # whichever block draws a unit, and however often the counter was used
+        assert torch.equal(out, p.run())
+
+
+def test_drawn_and_sliced_calls_share_a_workspace_and_a_graph():
+    a, b = drawn(None).device(), Prompt([(3, 9000), (40, 40)], 64, 8, seed=47).device()
+    ra, rb = a.run(), b.run()
+    b.check(rb)
+    oa, ob = torch.zeros_like(a.dq), torch.zeros_like(b.dq)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for p, o in ((a, oa), (b, ob), (a, oa)):
+            p.call(o, a.ws)
+    for _ in range(3):
+        oa.fill_(7.0)
+        ob.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(oa, ra) and torch.equal(ob, rb)
+    assert torch.equal(a.run(), ra)
 
 
 def test_chunks_of_a_prompt_equal_the_whole_within_the_bound():
