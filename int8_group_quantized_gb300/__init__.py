@@ -8,8 +8,10 @@ is missing the import of any entry point fails loudly.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
+from operator import attrgetter
 
 from . import _build
 
@@ -162,15 +164,29 @@ def _ptr(x) -> int:
     return x.data_ptr()
 
 
+_torch_module = None
+
+
+def _torch():
+    """torch, imported when a call first needs it (an import statement in every call takes a microsecond)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _nbytes(x) -> int:
     return x.numel() * x.element_size()
 
 
 def _stream(stream) -> int:
     if stream is None:
-        import torch
+        torch = _torch()
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 3 us less than building a Stream object
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        if raw and torch.cuda.is_initialized():
+            return raw(torch._C._cuda_getDevice())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -181,16 +197,25 @@ def _check(status: int, what: str) -> None:
         raise DGQError(status, what)
 
 
-def _operands(what: str, workspace, *specs) -> None:
-    """Refuses operands the raw pointers would misread: each spec is (tensor, dtype, shape); tensors, and
-    the workspace, must be contiguous and on the current CUDA device."""
-    import torch
-    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
-    if not workspace.is_contiguous() or workspace.get_device() != device:
-        raise DGQError(-1, what)
+def _operands(what: str, workspace, *specs) -> list:
+    """Addresses of the operands and the workspace.  Refuses what the raw pointers would misread: each spec is
+    (tensor, dtype, shape); tensors, and the workspace, must be contiguous and on the current CUDA device."""
+    device = _device()
+    at = []
     for x, dtype, shape in specs:
         if x.dtype is not dtype or x.shape != shape or not x.is_contiguous() or x.get_device() != device:
             raise DGQError(-1, what)
+        at.append(x.data_ptr())
+    if not workspace.is_contiguous() or workspace.get_device() != device:
+        raise DGQError(-1, what)
+    at.append(workspace.data_ptr())
+    return at
+
+
+def _device() -> int:
+    """The current CUDA device, -2 where CUDA is not in use (no tensor is there)."""
+    torch = _torch()
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
 
 
 def seg_record_dtype():
@@ -389,18 +414,18 @@ def dgq_paged_decode_attn_bf16(q, k_new, v_new, k_src, v_src, src_block_tables, 
     """dgq_paged_decode_attn over an unquantised cache: k_src, v_src bf16 paged cache
     [num_src_blocks, Hkv, bs, 128] with src_block_tables int32 [B, max_src_blocks]; the other
     arguments and the workspace (dgq_attn_workspace_size) as there."""
-    from torch import bfloat16, int32
+    torch = _torch()
+    bf16, i32 = torch.bfloat16, torch.int32
     B, Hq, D = q.shape
     blocks, Hkv, bs, _ = k_src.shape
     columns = src_block_tables.shape[1]
-    _operands("dgq_paged_decode_attn_bf16", workspace, (q, bfloat16, (B, Hq, D)), (k_new, bfloat16, (B, Hkv, D)),
-              (v_new, bfloat16, (B, Hkv, D)), (k_src, bfloat16, (blocks, Hkv, bs, D)),
-              (v_src, bfloat16, (blocks, Hkv, bs, D)), (src_block_tables, int32, (B, columns)),
-              (seq_lens, int32, (B,)), (out, bfloat16, (B, Hq, D)))
-    _check(lib().dgq_paged_decode_attn_bf16(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_src), _ptr(v_src), blocks,
-                                            _ptr(src_block_tables), columns, _ptr(seq_lens),
-                                            int(max_seqlen), B, Hq, Hkv, D, bs, _ptr(out),
-                                            _ptr(workspace), _nbytes(workspace), _stream(stream)),
+    new, cache = (B, Hkv, D), (blocks, Hkv, bs, D)
+    q_, kn, vn, k, v, bt, lens, o, ws = _operands(
+        "dgq_paged_decode_attn_bf16", workspace, (q, bf16, (B, Hq, D)), (k_new, bf16, new), (v_new, bf16, new),
+        (k_src, bf16, cache), (v_src, bf16, cache), (src_block_tables, i32, (B, columns)), (seq_lens, i32, (B,)),
+        (out, bf16, (B, Hq, D)))
+    _check(lib().dgq_paged_decode_attn_bf16(q_, kn, vn, k, v, blocks, bt, columns, lens, int(max_seqlen), B, Hq, Hkv, D,
+                                            bs, o, ws, _nbytes(workspace), _stream(stream)),
            "dgq_paged_decode_attn_bf16")
 
 
@@ -460,31 +485,34 @@ def dgq_prompt_attn(q, k, v, cu_q, cu_kv, out, workspace, stream=None) -> None:
     """Causal attention of packed prompts: q, out bf16 [Tq, Hq, 128]; k, v bf16 [Tkv, Hkv, 128]; cu_q,
     cu_kv int32 [B+1] (queries and keys of a request end at the same token); workspace uint8
     (dgq_prompt_attn_workspace_size bytes).  All CUDA tensors."""
-    from torch import bfloat16, int32
+    torch = _torch()
+    bf16, i32 = torch.bfloat16, torch.int32
     Tq, Hq, D = q.shape
     T, Hkv, _ = k.shape
     B = cu_q.shape[0] - 1
-    _operands("dgq_prompt_attn", workspace, (q, bfloat16, (Tq, Hq, D)), (k, bfloat16, (T, Hkv, D)),
-              (v, bfloat16, (T, Hkv, D)), (cu_q, int32, (B + 1,)), (cu_kv, int32, (B + 1,)), (out, bfloat16, (Tq, Hq, D)))
-    _check(lib().dgq_prompt_attn(_ptr(q), _ptr(k), _ptr(v), Tq, T, _ptr(cu_q), _ptr(cu_kv),
-                                 B, Hq, Hkv, D, _ptr(out), _ptr(workspace),
-                                 _nbytes(workspace), _stream(stream)), "dgq_prompt_attn")
+    q_, k_, v_, cq, ck, o, ws = _operands(
+        "dgq_prompt_attn", workspace, (q, bf16, (Tq, Hq, D)), (k, bf16, (T, Hkv, D)), (v, bf16, (T, Hkv, D)),
+        (cu_q, i32, (B + 1,)), (cu_kv, i32, (B + 1,)), (out, bf16, (Tq, Hq, D)))
+    _check(lib().dgq_prompt_attn(q_, k_, v_, Tq, T, cq, ck, B, Hq, Hkv, D, o, ws, _nbytes(workspace),
+                                 _stream(stream)), "dgq_prompt_attn")
 
 
 def dgq_prompt_attn_paged(q, cu_q, k_src, v_src, src_block_tables, seq_lens, out, workspace, stream=None) -> None:
     """dgq_prompt_attn over a bf16 paged cache: k_src, v_src bf16 [num_src_blocks, Hkv, bs, 128],
     src_block_tables int32 [B, max_src_blocks], seq_lens int32 [B] (keys of each request, the chunk's
     own among them); the rest as dgq_prompt_attn."""
-    from torch import bfloat16, int32
+    torch = _torch()
+    bf16, i32 = torch.bfloat16, torch.int32
     Tq, Hq, D = q.shape
     blocks, Hkv, bs, _ = k_src.shape
     B, columns = src_block_tables.shape
-    _operands("dgq_prompt_attn_paged", workspace, (q, bfloat16, (Tq, Hq, D)), (k_src, bfloat16, (blocks, Hkv, bs, D)),
-              (v_src, bfloat16, (blocks, Hkv, bs, D)), (cu_q, int32, (B + 1,)), (seq_lens, int32, (B,)),
-              (src_block_tables, int32, (B, columns)), (out, bfloat16, (Tq, Hq, D)))
-    _check(lib().dgq_prompt_attn_paged(_ptr(q), Tq, _ptr(cu_q), _ptr(k_src), _ptr(v_src), blocks,
-                                       _ptr(src_block_tables), columns, _ptr(seq_lens), B, Hq, Hkv, D, bs,
-                                       _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream)), "dgq_prompt_attn_paged")
+    cache = (blocks, Hkv, bs, D)
+    q_, k, v, cq, lens, bt, o, ws = _operands(
+        "dgq_prompt_attn_paged", workspace, (q, bf16, (Tq, Hq, D)), (k_src, bf16, cache), (v_src, bf16, cache),
+        (cu_q, i32, (B + 1,)), (seq_lens, i32, (B,)), (src_block_tables, i32, (B, columns)),
+        (out, bf16, (Tq, Hq, D)))
+    _check(lib().dgq_prompt_attn_paged(q_, Tq, cq, k, v, blocks, bt, columns, lens, B, Hq, Hkv, D, bs, o, ws,
+                                       _nbytes(workspace), _stream(stream)), "dgq_prompt_attn_paged")
 
 
 def dgq_copy_pages_workspace_size() -> int:
@@ -496,14 +524,11 @@ def dgq_copy_pages(arrays, pairs, workspace, stream=None) -> None:
     first dimension: pools of any layers, or segment tables [B, Hkv, 128]; all of one shape and type).
     pairs: int32 CUDA tensor [n, 2] of (source, destination) ids, destinations distinct and none of them
     a source; workspace uint8 (dgq_copy_pages_workspace_size bytes)."""
-    import array
-    from operator import attrgetter
-
-    import torch
+    torch = _torch()
     arrays = list(arrays)
     count = len(arrays)
     pages, nbytes, address = 1, 16, 0
-    _operands("dgq_copy_pages", workspace, (pairs, torch.int32, (pairs.shape[0], 2)))
+    pairs_, ws = _operands("dgq_copy_pages", workspace, (pairs, torch.int32, (pairs.shape[0], 2)))
     if count:  # (a list of 64 pools: the checks run as C loops)
         first = arrays[0]
         pages, nbytes = first.shape[0], first.nbytes
@@ -514,18 +539,18 @@ def dgq_copy_pages(arrays, pairs, workspace, stream=None) -> None:
             raise DGQError(-1, "dgq_copy_pages")
         pointers = array.array("Q", map(torch.Tensor.data_ptr, arrays))
         address = pointers.buffer_info()[0]
-    _check(lib().dgq_copy_pages(address, count, nbytes // max(pages, 1), pages, _ptr(pairs), pairs.shape[0],
-                                _ptr(workspace), _nbytes(workspace), _stream(stream)), "dgq_copy_pages")
+    _check(lib().dgq_copy_pages(address, count, nbytes // max(pages, 1), pages, pairs_, pairs.shape[0], ws,
+                                _nbytes(workspace), _stream(stream)), "dgq_copy_pages")
 
 
 def dgq_remap_tables(tables, remap, out, workspace, stream=None) -> None:
     """out[...] = remap[tables[...]]: contiguous int32 CUDA tensors (out may be tables); remap int32
     [num_pages] as BlockPool.compact returns it; workspace as for dgq_copy_pages."""
-    from torch import int32
-    _operands("dgq_remap_tables", workspace, (tables, int32, tables.shape), (out, int32, tables.shape),
-              (remap, int32, (remap.numel(),)))
-    _check(lib().dgq_remap_tables(_ptr(tables), tables.numel(), _ptr(remap), remap.numel(), _ptr(out),
-                                  _ptr(workspace), _nbytes(workspace), _stream(stream)), "dgq_remap_tables")
+    i32 = _torch().int32
+    tables_, out_, remap_, ws = _operands("dgq_remap_tables", workspace, (tables, i32, tables.shape),
+                                          (out, i32, tables.shape), (remap, i32, (remap.numel(),)))
+    _check(lib().dgq_remap_tables(tables_, tables.numel(), remap_, remap.numel(), out_, ws, _nbytes(workspace),
+                                  _stream(stream)), "dgq_remap_tables")
 
 
 def _host_table(table, *rows):
