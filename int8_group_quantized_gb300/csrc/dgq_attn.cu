@@ -412,10 +412,13 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
     const int32_t T = s_tpre[B];
     const int64_t C = (int64_t)T + (int64_t)kPieceCost * B * Hkv;  // total cost
     const int32_t ncta = gridDim.x, cta = blockIdx.x;
-    const int32_t c0 = tile_at(C * cta / ncta, s_tpre, s_len, B, Hkv);
-    const int32_t c1 = tile_at(C * (cta + 1) / ncta, s_tpre, s_len, B, Hkv);
+    // C cta / ncta and C (cta + 1) / ncta from one quotient (a 64-bit division takes 400 cycles)
+    const int64_t share = C >> 32 ? C / ncta : (int64_t)((uint32_t)C / (uint32_t)ncta);
+    const int32_t rest = (int32_t)(C - share * ncta);  // < ncta
+    const int32_t c0 = tile_at(share * cta + rest * cta / ncta, s_tpre, s_len, B, Hkv);
+    const int32_t c1 = tile_at(share * (cta + 1) + rest * (cta + 1) / ncta, s_tpre, s_len, B, Hkv);
     if (tid == 0) a.held[cta] = c0 < c1 ? 1 : 0;  // read by the merge kernels
-    if (cta == 0 && tid == 0) a.hdr->pad[kHdrAllHeld] = C / ncta > kPieceCost ? 1u : 0u;
+    if (cta == 0 && tid == 0) a.hdr->pad[kHdrAllHeld] = share > kPieceCost ? 1u : 0u;
     if (c0 >= c1) return;  // the whole CTA: no barrier follows for it
 
     const int r = lane >> 2, cq = lane & 3;
@@ -464,15 +467,17 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
         if (k < nmine) {
             const TileLoc c = locate_tile(xw0 + kWarpsPerCta * k, s_tpre, s_len, B);
             if (c.L > 0) blk = __ldg(a.bt + (int64_t)c.b * a.max_blocks + pow2_div(c.j, per_blk));
-            if ((uint32_t)blk >= (uint32_t)a.num_blocks) {  // not a block of the pools: flagged,
-                record_error(a.hdr, kErrBadBlock);          // and block 0 read instead
-                blk = 0;
-            }
         }
         return blk;
     };
+    auto checked = [&](int32_t blk) -> int32_t {
+        if ((uint32_t)blk < (uint32_t)a.num_blocks) return blk;
+        record_error(a.hdr, kErrBadBlock);  // not a block of the pools: flagged, and block 0 read instead
+        return 0;
+    };
     int32_t kb = 0;
-    int32_t bq_cur = fetch_batch(0), bq_next = fetch_batch(32);
+    int32_t bq_cur = fetch_batch(0), bq_next = fetch_batch(32);  // bq_next is checked when its turn comes
+    bq_cur = checked(bq_cur);
 
     // ---- copies of one tile into ring stage `st`; the issue point runs kDeep tiles ahead of the
     // compute point and always lies in the two fetched batches
@@ -482,7 +487,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
     auto issue = [&](int st) {
         if (kn - kb >= 32) {
             kb += 32;
-            bq_cur = bq_next;
+            bq_cur = checked(bq_next);
             bq_next = fetch_batch(kb + 32);
         }
         const int32_t blk = __shfl_sync(0xffffffffu, bq_cur, (kn - kb) & 31);
