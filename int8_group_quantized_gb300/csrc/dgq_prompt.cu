@@ -155,7 +155,7 @@ __device__ __forceinline__ int32_t key_tiles(int32_t keys) { return (keys + kPmT
 __device__ __forceinline__ int64_t unit_cost(const PromptSeq &s, int32_t U, int32_t i)
 {
     const int32_t off = s.m - s.n;
-    const int64_t x0 = off >= 0 ? 0 : min(i, -off / U);  // units that see no key
+    const int64_t x0 = off >= 0 ? 0 : min(i, -off >> (__ffs(U) - 1));  // units that see no key
     const int64_t c = (int64_t)i - x0;
     return (int64_t)i * kPmUnitCost + c * off + U * (((int64_t)i * (i + 1) - x0 * (x0 + 1)) / 2);
 }
@@ -167,21 +167,37 @@ __device__ __forceinline__ bool lone_tile(const PromptSeq &s, int32_t U, int32_t
 __device__ __forceinline__ int64_t head_cost(const PromptSeq &s, int32_t U, int32_t nu)
 {
     if (nu == 0) return 0;
-    const int64_t last = lone_tile(s, U, nu) ? (int64_t)s.m * kPmLoneTile / kPmTile : s.m;
+    const int64_t last = lone_tile(s, U, nu) ? (uint64_t)s.m * kPmLoneTile / kPmTile : s.m;
     return unit_cost(s, U, nu - 1) + kPmUnitCost + last;
 }
 
-__device__ __forceinline__ void next_unit(const PromptArgs &a, int32_t U, PromptPos &p, PromptSeq &s)
+__device__ __forceinline__ PromptSeq seq_of_lane(const PromptSeq &s, int l)
+{
+    return PromptSeq{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.n, l),
+                     __shfl_sync(0xffffffffu, s.kv0, l), __shfl_sync(0xffffffffu, s.m, l)};
+}
+
+// The unit behind p (the whole warp: empty requests are passed 32 at a time); R: requests up to the last one
+// with rows.  (One at a time up to the end, the last block of eight requests padded to 256 finished 14 us
+// after the others.)
+__device__ __forceinline__ void next_unit(const PromptArgs &a, int32_t U, int32_t R, int lane, PromptPos &p, PromptSeq &s)
 {
     p.j = 0;
     if (++p.i < prompt_units(s, U)) return;
     p.i = 0;
     if (++p.h < a.Hkv) return;
     p.h = 0;
-    while (++p.b < a.B) {
-        s = prompt_seq(a, p.b, false);
-        if (s.n > 0) return;
+    for (++p.b; p.b < R; p.b += 32) {
+        PromptSeq t = {0, 0, 0, 0};
+        if (p.b + lane < R) t = prompt_seq(a, p.b + lane, false);
+        const uint32_t hit = __ballot_sync(0xffffffffu, t.n > 0);
+        if (hit) {
+            s = seq_of_lane(t, __ffs(hit) - 1);
+            p.b += __ffs(hit) - 1;
+            return;
+        }
     }
+    p.b = a.B;
 }
 
 // The units drawn one by one, a request's longest first: the requests in a window of 32, one per lane.
@@ -192,10 +208,10 @@ struct PromptQueue {
     int32_t first;  // the window's first request
 };
 
-__device__ __forceinline__ void queue_window(const PromptArgs &a, int32_t U, int lane, PromptQueue &w)
+__device__ __forceinline__ void queue_window(const PromptArgs &a, int32_t U, int32_t R, int lane, PromptQueue &w)
 {
     w.s = PromptSeq{0, 0, 0, 0};
-    if (w.first + lane < a.B) w.s = prompt_seq(a, w.first + lane, false);
+    if (w.first + lane < R) w.s = prompt_seq(a, w.first + lane, false);
     w.upto = (int64_t)prompt_units(w.s, U) * a.Hkv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -205,17 +221,14 @@ __device__ __forceinline__ void queue_window(const PromptArgs &a, int32_t U, int
 }
 
 // Unit number `ticket` and its request, or false: there are not so many (the whole warp; tickets only rise).
-__device__ __forceinline__ bool queue_unit(const PromptArgs &a, int32_t U, int lane, PromptQueue &w, int64_t ticket,
-                                           PromptPos &p, PromptSeq &s)
+__device__ __forceinline__ bool queue_unit(const PromptArgs &a, int32_t U, int32_t R, int lane, PromptQueue &w,
+                                           int64_t ticket, PromptPos &p, PromptSeq &s)
 {
     for (;;) {
         const uint32_t hit = __ballot_sync(0xffffffffu, w.base + w.upto > ticket);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            s.q0 = __shfl_sync(0xffffffffu, w.s.q0, l);
-            s.n = __shfl_sync(0xffffffffu, w.s.n, l);
-            s.kv0 = __shfl_sync(0xffffffffu, w.s.kv0, l);
-            s.m = __shfl_sync(0xffffffffu, w.s.m, l);
+            s = seq_of_lane(w.s, l);
             const int32_t back = (int32_t)(w.base + __shfl_sync(0xffffffffu, w.upto, l) - ticket) - 1;  // from the request's end
             p.b = w.first + l;
             p.i = back / a.Hkv;
@@ -225,44 +238,47 @@ __device__ __forceinline__ bool queue_unit(const PromptArgs &a, int32_t U, int l
         }
         w.base += __shfl_sync(0xffffffffu, w.upto, 31);
         w.first += 32;
-        if (w.first >= a.B) return false;
-        queue_window(a, U, lane, w);
+        if (w.first >= R) return false;
+        queue_window(a, U, R, lane, w);
     }
 }
 
-// The unit and key tile at cost position pos (pre: cost prefix over requests, [B + 1]).
-__device__ PromptPos cut_at(const PromptArgs &a, int32_t U, int64_t pos, const int64_t *pre)
+// The last of n positions from 0 on where `yes` holds (it does at 0, and nowhere behind a position where it
+// does not): 32 are looked at together.
+template <typename F>
+__device__ __forceinline__ int32_t last_where(int32_t n, int lane, F yes)
+{
+    int32_t lo = 0;
+    while (n > 1) {
+        const int32_t step = (n - 1) / 32 + 1, x = lane * step;
+        const int32_t c = __popc(__ballot_sync(0xffffffffu, x < n && yes(lo + x))) - 1;
+        lo += c * step;
+        n = min(step, n - c * step);
+    }
+    return lo;
+}
+
+// The unit and key tile at cost position pos (pre: cost prefix over requests, [B + 1]); the whole warp.
+__device__ PromptPos cut_at(const PromptArgs &a, int32_t U, int32_t R, int64_t pos, const int64_t *pre, int lane)
 {
     PromptPos p = {a.B, 0, 0, 0};
     if (pos >= pre[a.B]) return p;
-    int32_t lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) >> 1;
-        if (pre[mid] <= pos) lo = mid;
-        else hi = mid - 1;
-    }
-    PromptSeq s = prompt_seq(a, lo, false);  // has units: the next prefix is larger
+    p.b = last_where(R, lane, [&](int32_t b) { return pre[b] <= pos; });
+    PromptSeq s = prompt_seq(a, p.b, false);  // has units: the next prefix is larger
     const int32_t nu = prompt_units(s, U);
     const int64_t per_head = head_cost(s, U, nu);
-    int64_t r = pos - pre[lo];
-    p.b = lo;
+    int64_t r = pos - pre[p.b];
     p.h = (int32_t)__fdividef((float)r, (float)per_head);  // off by one at most below a million heads
     r -= p.h * per_head;
     for (; r < 0; r += per_head) --p.h;
     for (; r >= per_head; r -= per_head) ++p.h;
-    lo = 0;
-    hi = nu - 1;
-    while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) >> 1;
-        if (unit_cost(s, U, mid) <= r) lo = mid;
-        else hi = mid - 1;
-    }
+    const int32_t lo = last_where(nu, lane, [&](int32_t i) { return unit_cost(s, U, i) <= r; });
     p.i = lo;
     r -= unit_cost(s, U, lo) + kPmUnitCost;
     const int32_t tiles = key_tiles(keys_before(s, (lo + 1) * U));
     int32_t j = r > 0 ? (int32_t)r / (lo == nu - 1 && lone_tile(s, U, nu) ? kPmLoneTile : kPmTile) : 0;  // (r <= m < 2^31)
     if (j > tiles - kPmSnap) {
-        if (j >= kPmSnap || r > 0) next_unit(a, U, p, s);
+        if (j >= kPmSnap || r > 0) next_unit(a, U, R, lane, p, s);
         return p;
     }
     p.j = j < kPmSnap ? 0 : j;
@@ -503,7 +519,7 @@ struct PromptBars {
     uint32_t tmem;
     PromptPos cut[2];
     int64_t wsum[kPmThreads / 32];
-    int32_t wmax[kPmThreads / 32];
+    int32_t wmax[kPmThreads / 32], wlast[kPmThreads / 32];
 };
 
 constexpr int kPmTurn = 32 * 128;  // a softmax warp's buffer for turning rows
@@ -564,17 +580,22 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
     if (tid < 3) prefetch_tensormap(tid == 0 ? &maps.q : (tid == 1 ? &maps.k : &maps.v));
     // ---- this CTA's slice of the flat list, or whether units are handed out one by one
     bool queued;
+    int32_t requests;  // up to the last one with rows
     {
         int64_t *pre = reinterpret_cast<int64_t *>(smem + 2 * kPmTileBytes);  // the ring is not in use yet
         int64_t carry = 0;
         int32_t longest = 0;
+        requests = 0;
         for (int32_t base = 0; base < a.B; base += kPmThreads) {
             const int32_t b = base + tid;
             int64_t c = 0;
             if (b < a.B) {
                 const PromptSeq s = prompt_seq(a, b, blockIdx.x == 0);
                 c = a.Hkv * head_cost(s, U, prompt_units(s, U));
-                if (s.n > 0) longest = max(longest, s.m);
+                if (s.n > 0) {
+                    longest = max(longest, s.m);
+                    requests = b + 1;
+                }
             }
             int64_t x = c;
 #pragma unroll
@@ -595,7 +616,11 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             __syncthreads();
         }
         longest = __reduce_max_sync(0xffffffffu, longest);
-        if (lane == 0) sb->wmax[warp] = longest;
+        requests = __reduce_max_sync(0xffffffffu, requests);
+        if (lane == 0) {
+            sb->wmax[warp] = longest;
+            sb->wlast[warp] = requests;
+        }
         if (tid == 0) {
             pre[a.B] = carry;
             for (int i = 0; i < kPmStages; ++i) {
@@ -620,14 +645,18 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         }
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kPmThreads / 32; ++w) longest = max(longest, sb->wmax[w]);
+        for (int w = 0; w < kPmThreads / 32; ++w) {
+            longest = max(longest, sb->wmax[w]);
+            requests = max(requests, sb->wlast[w]);
+        }
         queued = ((int64_t)longest + kPmUnitCost) * (kPmQueued * gridDim.x) <= carry;
         if (queued) {
             if (lane == 0 && warp < 2) sb->cut[warp] = PromptPos{warp ? a.B : 0, 0, 0, 0};
-        } else if (lane == 0 && warp < 2) {
+        } else if (warp < 2) {
             // carry * c / n in steps of 2^-20 (monotone, exact at c = n, no 64-bit division: one took 400 cycles)
             const int64_t f = (uint32_t)((blockIdx.x + warp) << 20) / gridDim.x;
-            sb->cut[warp] = cut_at(a, U, (carry >> 20) * f + (((carry & 0xfffff) * f) >> 20), pre);
+            const PromptPos c = cut_at(a, U, requests, (carry >> 20) * f + (((carry & 0xfffff) * f) >> 20), pre, lane);
+            if (lane == 0) sb->cut[warp] = c;
         }
         __syncthreads();
     }
@@ -679,16 +708,16 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         if (queued) {
             queue.base = 0;
             queue.first = 0;
-            queue_window(a, U, lane, queue);
-            more = queue_unit(a, U, lane, queue, blockIdx.x, pos, s);
+            queue_window(a, U, requests, lane, queue);
+            more = queue_unit(a, U, requests, lane, queue, blockIdx.x, pos, s);
         } else {
             s = prompt_seq(a, pos.b, false);
         }
         auto advance = [&]() {
             if (queued) {
-                more = queue_unit(a, U, lane, queue, (int64_t)gridDim.x + __shfl_sync(0xffffffffu, ticket, 0), pos, s);
+                more = queue_unit(a, U, requests, lane, queue, (int64_t)gridDim.x + __shfl_sync(0xffffffffu, ticket, 0), pos, s);
             } else {
-                next_unit(a, U, pos, s);
+                next_unit(a, U, requests, lane, pos, s);
                 more = before(pos, end);
             }
         };

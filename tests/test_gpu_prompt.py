@@ -245,6 +245,30 @@ def test_drawn_and_sliced_calls_share_a_workspace_and_a_graph():
     assert torch.equal(a.run(), ra)
 
 
+@pytest.mark.parametrize("block", [None, 16])
+@pytest.mark.parametrize("shape", [
+    [(0, 0)] * 40 + [(5, 300)] + [(0, 7)] * 70 + [(130, 130)] + [(0, 0)] * 500,
+    [(0, 0)] * 33 + [(3, 6000)] + [(0, 0)] * 31 + [(2, 5000)] + [(0, 0)] * 32 + [(1, 4000)],
+    [(1, 200)] + [(0, 0)] * 63 + [(1, 100)],
+], ids=["few", "cut", "ends"])
+def test_padded_batches(shape, block):
+    # empty requests before, between and behind the others, in runs of more than a warp's lanes
+    verify(shape, 8, 2, seed=48, block=block)
+
+
+def test_drawn_units_of_a_padded_batch():
+    shape = [(0, 0)] * 50 + [(n, n) for n in range(150, 200)] + [(0, 0)] * 70 + [(n, n + 9) for n in range(100, 130)] + \
+        [(0, 0)] * 900
+    p = Prompt(shape, 64, 8, seed=49).device()
+    out = p.run()
+    start = np.concatenate([[0], np.cumsum(p.n)])
+    for b in (50, 75, 99, 170, 199):
+        lo, hi = int(start[b]), int(start[b + 1])
+        ref, bound = prompt(p.q[lo:hi], p.ks[b:b + 1], p.vs[b:b + 1], [p.n[b]], 64, 8)
+        check(out[lo:hi], ref, bound)
+    assert not torch.any(torch.all(out == 7.0, dim=-1))  # every row is written
+
+
 def test_chunks_of_a_prompt_equal_the_whole_within_the_bound():
     # the same prompt in three chunks against the pages written so far
     import int8_group_quantized_gb300 as dgq
