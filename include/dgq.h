@@ -36,7 +36,7 @@
  *     state, so calls from several threads at once are safe (each on its own stream and
  *     workspace, as above), on any number of devices.
  *   - CUDA graphs: every compute call (compress, decode, append, the prefill calls, the
- *     comparison formats, prompt attention, the page calls) enqueues only kernel launches and
+ *     comparison formats, prompt attention, the page and fork calls) enqueues only kernel launches and
  *     workspace memsets on its stream, with no host synchronisation, so it may be captured into
  *     a graph on a capturing stream;
  *     a replay does what the call does.  Make one call on the device and host thread first
@@ -488,6 +488,33 @@ dgq_status dgq_append_split(const void *k_new_bf16, const void *v_new_bf16, int3
                             size_t workspace_bytes, void *cuda_stream);
 
 /* ---------------------------------------------------------------------------------------
+ * dgq_fork_records -- the records of forked requests: every record of row dst becomes row src's cut to
+ * the first len tokens, so that dgq_append continues the fork at token len with the parameters of the
+ * segment that token len - 1 lies in.  (A record copied as it is keeps the source's seq_len: the next
+ * append of a shorter fork would go to that position, in a column that the fork's row does not have.)
+ *
+ * The cut record holds the segments that start before len, seq_len = len and start = len behind the last
+ * of them; len == 0 gives an empty record.  Where the last segment is the source's last one,
+ * k_inv_last / v_inv_last are the source's; for an earlier segment the source holds no factor any more
+ * and they are 1 / scale (0 if flat), within 2^-23 of the encoder's 255 / (max - min): a value less than
+ * 2^-15 of a step from the middle of two codes may be appended with the other one.
+ *
+ * seg_table         [num_rows, Hkv] dgq_seg_record, device, read and updated in place.  A cache with
+ *                   independent V segmentation: one call for each of its two tables.
+ * forks_dev         [num_forks, 3] int32, device: (src row, dst row, len).  Destinations are distinct and
+ *                   none is the source of another fork; src == dst cuts a row in place (tokens taken
+ *                   back: blocks from len / bs on that other rows share need dgq_pool_own_row before
+ *                   the next append).  A fork whose rows are not in [0, num_rows), or whose len is not in
+ *                   [0, seq_len of the source record], is flagged in the workspace, its row untouched.
+ * workspace         >= dgq_append_workspace_size() bytes, zero-filled before first use.
+ * No forks: nothing is launched.  The pages of the fork are dgq_pool_fork_row's and dgq_copy_pages' part;
+ * its window_stats, where the caller keeps them, are copied like a page.
+ */
+dgq_status dgq_fork_records(dgq_seg_record *seg_table, int32_t num_rows, int32_t num_kv_heads,
+                            const int32_t *forks_dev, int32_t num_forks, void *workspace, size_t workspace_bytes,
+                            void *cuda_stream);
+
+/* ---------------------------------------------------------------------------------------
  * Comparison encodings: the same paged cache layout and the same decode kernel, with the
  * K/V codes produced by one of the quantisers DGQ is measured against, so that accuracy and
  * decode speed can be set side by side on one workload.  Sources:
@@ -582,7 +609,8 @@ dgq_status dgq_workspace_error(const void *workspace, void *cuda_stream, int32_t
  * arrays           HOST array of num_arrays device pointers: every array is [num_pages] pages of
  *                  page_bytes bytes (K and V pools of any number of layers, INT8 or bf16; the
  *                  parameter arrays of fixed groups; or segment tables, a page being one
- *                  request's Hkv records of 128 bytes).  Read before the call returns.
+ *                  request's Hkv records of 128 bytes, copied as they are: for a request that moves
+ *                  whole; dgq_fork_records writes those of a fork).  Read before the call returns.
  * page_bytes       a positive multiple of 16.
  * pairs_dev        [num_pairs, 2] int32, device: (source, destination) page ids.  Destinations are
  *                  distinct and none of them is a source (of any pair): pairs run in no order.
@@ -630,8 +658,10 @@ dgq_status dgq_pool_alloc_table_row(dgq_pool *pool, int32_t len, int32_t block_s
 /* Row dst_row becomes a fork of the first `len` tokens of row src_row (two different rows): whole
  * blocks are shared (one more reference), a partly filled last block is replaced by a new one, and
  * (old, new) goes to out_pair[2] with *num_pairs = 1 (0 when len ends on a block): the caller
- * copies that page with dgq_copy_pages, and the request's records.  dst_row's former entries are
- * overwritten, not freed; its unused entries are set to 0.  On error nothing changes. */
+ * copies that page with dgq_copy_pages, and for an INT8 cache writes the fork's records for the same len
+ * with dgq_fork_records (a bf16 cache has none).  dst_row's former entries are overwritten, not freed; its
+ * unused entries are set to 0, so the caller adds a block to the row before token len is written where len
+ * ends on a block (as for dgq_append).  On error nothing changes. */
 dgq_status dgq_pool_fork_row(dgq_pool *pool, int32_t len, int32_t block_size, int32_t *table, int32_t src_row,
                              int32_t dst_row, int32_t max_blocks_per_seq, int32_t *out_pair, int32_t *num_pairs);
 /* Copy on write: each of the row's blocks [first_block, first_block + num_row_blocks) that has other

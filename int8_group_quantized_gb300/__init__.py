@@ -33,7 +33,7 @@ __all__ = [
     "dgq_paged_decode_attn_format", "FORMATS", "dgq_prefill_workspace_size", "dgq_prefill_chunk_stats",
     "dgq_prefill_finish", "dgq_paged_decode_attn_split", "dgq_append_split", "dgq_append_ex",
     "dgq_prompt_attn", "dgq_prompt_attn_paged", "dgq_prompt_attn_workspace_size", "dgq_paged_decode_attn_bf16",
-    "dgq_copy_pages", "dgq_copy_pages_workspace_size", "dgq_remap_tables",
+    "dgq_copy_pages", "dgq_copy_pages_workspace_size", "dgq_remap_tables", "dgq_fork_records",
     "dgq_prefill_finish_ex", "RESEG_WINDOW", "RESEG_NGROUPS",
     "dgq_attn_workspace_size", "dgq_workspace_init", "dgq_workspace_error", "BlockPool",
     "seg_record_dtype",
@@ -127,6 +127,8 @@ def lib() -> ctypes.CDLL:
         L.dgq_copy_pages_workspace_size.restype = sz
         L.dgq_remap_tables.argtypes = [P, ctypes.c_int64, P, i32, P, P, sz, P]
         L.dgq_remap_tables.restype = ctypes.c_int
+        L.dgq_fork_records.argtypes = [P, i32, i32, P, i32, P, sz, P]
+        L.dgq_fork_records.restype = ctypes.c_int
         L.dgq_pool_create.argtypes = [i32]
         L.dgq_pool_create.restype = P
         L.dgq_pool_destroy.argtypes = [P]
@@ -551,6 +553,18 @@ def dgq_remap_tables(tables, remap, out, workspace, stream=None) -> None:
                                           (out, i32, tables.shape), (remap, i32, (remap.numel(),)))
     _check(lib().dgq_remap_tables(tables_, tables.numel(), remap_, remap.numel(), out_, ws, _nbytes(workspace),
                                   _stream(stream)), "dgq_remap_tables")
+
+
+def dgq_fork_records(seg_table, forks, workspace, stream=None) -> None:
+    """Records of forked requests, in place: seg_table uint8 [rows, Hkv, 128]; forks int32 CUDA tensor [n, 3]
+    of (source row, destination row, tokens), destinations distinct and none the source of another fork;
+    workspace uint8 (dgq_append_workspace_size bytes)."""
+    torch = _torch()
+    rows, Hkv, _ = seg_table.shape
+    table, forks_, ws = _operands("dgq_fork_records", workspace, (seg_table, torch.uint8, (rows, Hkv, 128)),
+                                  (forks, torch.int32, (forks.shape[0], 3)))
+    _check(lib().dgq_fork_records(table, rows, Hkv, forks_, forks.shape[0], ws, _nbytes(workspace), _stream(stream)),
+           "dgq_fork_records")
 
 
 def _host_table(table, *rows):

@@ -263,4 +263,56 @@ cudaError_t launch_append(const void *k_new, const void *v_new, int32_t B, int32
     return vtable ? cudaLaunchKernelEx(&cfg, append_split_kernel, a) : cudaLaunchKernelEx(&cfg, append_kernel, a);
 }
 
+// Records of forked requests: row dst's record of head h becomes row src's, cut to its first len tokens.
+// The segments that start before len stay; the first one that does not start there is the end (word for
+// word what a record of len tokens with these segments holds).  The last segment's encoding factor is
+// stored for the source's last segment only: for an earlier one it is 1 / scale, within 2^-23 of the
+// encoder's 255 / (max - min) (scale is the rounded (max - min) / 255, and the division rounds once).
+// One warp per (fork, head), lane i on record word i: 256 bytes moved per pair, bound by the launch.
+__global__ void __launch_bounds__(kAppendPairsPerCta * 32) fork_records_kernel(uint32_t *table, int32_t num_rows,
+                                                                               int32_t Hkv, const int32_t *forks,
+                                                                               int64_t pairs, WsHeader *hdr)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t pair = (int64_t)blockIdx.x * kAppendPairsPerCta + (threadIdx.x >> 5);
+    if (pair >= pairs) return;
+    const int64_t f = pair / Hkv;
+    const int32_t h = (int32_t)(pair - f * Hkv);
+    const int32_t src = __ldg(forks + 3 * f), dst = __ldg(forks + 3 * f + 1), len = __ldg(forks + 3 * f + 2);
+    if ((uint32_t)src >= (uint32_t)num_rows || (uint32_t)dst >= (uint32_t)num_rows) {  // not a row: untouched
+        if (lane == 0) record_error(hdr, kErrBadBlock);
+        return;
+    }
+    const uint32_t w = table[((int64_t)src * Hkv + h) * 32 + lane];
+    const int32_t have = (int32_t)__shfl_sync(0xffffffffu, w, kWLen);
+    if (len < 0 || len > have) {  // tokens that the source does not hold: untouched
+        if (lane == 0) record_error(hdr, kErrBadLength);
+        return;
+    }
+    const int32_t n_src = min(max((int32_t)__shfl_sync(0xffffffffu, w, kWN), 0), kMaxSeg);
+    const int32_t n = __popc(__ballot_sync(0xffffffffu, lane >= kWStart && lane < kWStart + n_src && (int32_t)w < len));
+    uint32_t nw = w;
+    if (lane == kWN) nw = (uint32_t)n;
+    if (lane == kWLen) nw = (uint32_t)len;
+    if (lane >= kWStart + n && lane < kWStart + kMaxSeg) nw = (uint32_t)len;
+    if (lane >= kWKMin && lane < kWKInv && (lane - kWKMin) % kMaxSeg >= n) nw = 0u;  // min and scale of K and V
+    if (n < n_src) {
+        const float ks = __uint_as_float(__shfl_sync(0xffffffffu, w, kWKScale + max(n - 1, 0)));
+        const float vs = __uint_as_float(__shfl_sync(0xffffffffu, w, kWVScale + max(n - 1, 0)));
+        if (lane == kWKInv) nw = n == 0 || ks == 0.0f ? 0u : __float_as_uint(__fdiv_rn(1.0f, ks));
+        if (lane == kWVInv) nw = n == 0 || vs == 0.0f ? 0u : __float_as_uint(__fdiv_rn(1.0f, vs));
+    }
+    table[((int64_t)dst * Hkv + h) * 32 + lane] = nw;
+}
+
+cudaError_t launch_fork_records(dgq_seg_record *table, int32_t num_rows, int32_t Hkv, const int32_t *forks,
+                                int32_t num_forks, void *ws, cudaStream_t stream)
+{
+    const int64_t pairs = (int64_t)num_forks * Hkv;
+    fork_records_kernel<<<(unsigned)((pairs + kAppendPairsPerCta - 1) / kAppendPairsPerCta), kAppendPairsPerCta * 32, 0,
+                          stream>>>(reinterpret_cast<uint32_t *>(table), num_rows, Hkv, forks, pairs,
+                                    static_cast<WsHeader *>(ws));
+    return cudaGetLastError();
+}
+
 }  // namespace dgq

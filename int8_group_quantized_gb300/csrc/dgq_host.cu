@@ -236,6 +236,22 @@ dgq_status append_impl(const void *k_new_bf16, const void *v_new_bf16, int32_t b
 }
 }  // namespace
 
+dgq_status dgq_fork_records(dgq_seg_record *seg_table, int32_t num_rows, int32_t num_kv_heads,
+                            const int32_t *forks_dev, int32_t num_forks, void *workspace, size_t workspace_bytes,
+                            void *cuda_stream)
+{
+    if (num_rows <= 0 || num_kv_heads <= 0 || num_forks < 0) return DGQ_ERR_INVALID_ARG;
+    if ((int64_t)num_forks * num_kv_heads >= INT32_MAX) return DGQ_ERR_UNSUPPORTED;
+    if (!seg_table || !aligned16(seg_table) || (num_forks > 0 && !forks_dev) || !aligned16(forks_dev))
+        return DGQ_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < dgq_append_workspace_size())
+        return DGQ_ERR_WORKSPACE;
+    if (num_forks == 0) return DGQ_OK;
+    const cudaError_t e = dgq::launch_fork_records(seg_table, num_rows, num_kv_heads, forks_dev, num_forks, workspace,
+                                                   static_cast<cudaStream_t>(cuda_stream));
+    return e == cudaSuccess ? DGQ_OK : DGQ_ERR_CUDA;
+}
+
 size_t dgq_attn_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t max_seqlen)
 {
     (void)max_seqlen;

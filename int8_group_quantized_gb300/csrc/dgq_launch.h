@@ -75,6 +75,9 @@ cudaError_t launch_append(const void *k_new, const void *v_new, int32_t B, int32
                           const int32_t *bt, int32_t max_blocks, uint8_t *kpool, uint8_t *vpool, int32_t num_blocks,
                           dgq_seg_record *table, dgq_seg_record *vtable, int32_t *flags, void *ws,
                           cudaStream_t stream);
+// Records of forked requests: forks of (source row, destination row, tokens).
+cudaError_t launch_fork_records(dgq_seg_record *table, int32_t num_rows, int32_t Hkv, const int32_t *forks,
+                                int32_t num_forks, void *ws, cudaStream_t stream);
 
 // Compression in two phases for chunked prefill: window statistics of each request's chunk
 // [begin, end) from a bf16 paged cache, then segmentation and codes for whole requests.
