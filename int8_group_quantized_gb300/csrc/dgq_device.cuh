@@ -53,7 +53,14 @@ enum : uint32_t {
 };
 
 // WsHeader::path values
-enum : uint32_t { kPathGrid = 1, kPathClusterWhole = 2, kPathBlockMerge = 3, kPathWarpMerge = 4 };
+enum : uint32_t {
+    kPathGrid = 1,
+    kPathClusterWhole = 2,
+    kPathBlockMerge = 3,
+    kPathWarpMerge = 4,
+    kPathPromptDrawn = 5,   // prompt: whole units drawn from the counter
+    kPathPromptSliced = 6,  // prompt: equal slices of the unit list, cut units merged
+};
 
 // Upper bound on spin iterations of any wait (each iteration sleeps or polls ~tens of ns;
 // ~2^26 iterations is seconds, far beyond any legitimate wait).

@@ -668,6 +668,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         if (work && end.j > 0 && !(one && begin.j > 0)) head = make_int4(one ? 1 : 2, end.b, end.h, end.i);
         a.head[blockIdx.x] = head;
         a.cont[blockIdx.x] = work && begin.j > 0 ? (one ? 1 : 2) : 0;
+        if (blockIdx.x == 0) a.hdr->path = queued ? kPathPromptDrawn : kPathPromptSliced;  // (tests read it)
     }
     if (!work) return;  // the whole CTA: no barrier follows for it
     if (warp == kPmMmaWarp) {
