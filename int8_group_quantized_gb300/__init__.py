@@ -187,7 +187,7 @@ def _stream(stream) -> int:
         torch = _torch()
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 3 us less than building a Stream object
         if raw and torch.cuda.is_initialized():
-            return raw(torch._C._cuda_getDevice())
+            return raw(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -217,7 +217,10 @@ def _operands(what: str, workspace, *specs) -> list:
 def _device() -> int:
     """The current CUDA device, -2 where CUDA is not in use (no tensor is there)."""
     torch = _torch()
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    if not torch.cuda.is_initialized():
+        return -2
+    # (0.11 us; the public call, which a torch without this one answers, takes 0.24)
+    return getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)()
 
 
 def seg_record_dtype():
