@@ -342,8 +342,9 @@ dgq_status dgq_paged_decode_attn_bf16(const void *q_bf16, const void *k_new_bf16
  * a row that sees no key (n > m) gets zeros.  Softmax statistics and sums in fp32; the weights are
  * rounded to bf16 before they meet V.
  *
- * q_bf16, out_bf16  [total_q, Hq, 128] bf16, device; rows from cu_q[batch] on are neither read nor
- *                   written.
+ * q_bf16, out_bf16  [total_q, Hq, 128] bf16, device; rows from cu_q[batch] on are not written.  A tile
+ *                   of 128 / G rows is loaded whole, so up to 127 rows of q behind a request's last one
+ *                   may be read (never past total_q); no output depends on them.
  * k_bf16, v_bf16    [total_kv, Hkv, 128] bf16, device, packed rows as dgq_compress reads them.
  * cu_q_dev, cu_kv_dev  [batch+1] int32, device, non-decreasing, at most total_q / total_kv (a
  *                   request that is not is flagged in the workspace and cut to the buffers).
@@ -352,7 +353,8 @@ dgq_status dgq_paged_decode_attn_bf16(const void *q_bf16, const void *k_new_bf16
  * is not a number); rows of other requests, and behind the last one, cannot reach its output.
  * One launch of one block per SM (tensor memory and most of the shared memory of each), and one that
  * merges the rows whose keys several blocks share, in a fixed order: bitwise repeatable on a given GPU.
- * workspace         >= dgq_prompt_attn_workspace_size(batch, Hq, Hkv) bytes, zero-filled before first use.
+ * workspace         >= dgq_prompt_attn_workspace_size(batch, Hq, Hkv) bytes, zero-filled before first use
+ *                   (two units' parts per SM of the current device: 40 MB on 152 SMs, whatever the batch).
  */
 dgq_status dgq_prompt_attn(const void *q_bf16, const void *k_bf16, const void *v_bf16, int32_t total_q,
                            int32_t total_kv, const int32_t *cu_q_dev, const int32_t *cu_kv_dev, int32_t batch,
