@@ -33,12 +33,17 @@
 //  * Softmax: online, log2 domain, the reference maximum moving only when a tile exceeds it by 8 (lazy
 //    rescaling: O in tensor memory is then multiplied in place; the softmax threads may do that
 //    between products because S of the next key tile is complete only after O's product is).
+//    (The one-pass softmax is Milakov and Gimelshein's, 2018; two row tiles in turn, P in the place of S and
+//    the lazy maximum are known from published attention kernels of this hardware generation.)
 //  * Work where a CTA's share (one per SM) is at least kPmQueued times the longest unit: the load warps
-//    draw whole units from a counter, a request's longest first, the next number while a unit is loaded.
-//    All CTAs then work in few requests at a time, whose K and V stay in L2, and the short units at the
-//    end level them out; which CTA has a unit changes no result.  Against slices (below), us with launch:
-//    213 -> 202 for eight prompts of 2048, 164 -> 152 for the ragged batch, 213 -> 195 for eight chunks of
-//    512 behind 3584.
+//    draw whole units from a counter, requests in their order and a request's longest unit first, the next
+//    number while a unit is loaded.  All CTAs then work in few requests at a time, whose K and V stay in
+//    L2; which CTA has a unit changes no result.  The last request's units decide how evenly CTAs end: a
+//    prompt's short ones level them out, units of one length leave up to one of them, and a short chunk
+//    behind a long history at the list's end leaves its units to few CTAs alone.  Against slices (below),
+//    us with launch, calls on their own: 199 -> 188 for eight prompts of 2048, 195 -> 180 for eight chunks
+//    of 512 behind 3584; thirty prompts of 2048 and 64 tokens behind 16320 in front of them 748 -> 659, at
+//    their end 746 -> 811; thirteen and 64 tokens behind 8128 330 -> 299 and 330 -> 371.
 //  * Else the units lie in one flat list by cost, a unit costing the keys it sees plus a constant, and
 //    each CTA takes an equal slice, which may begin and end inside a unit, at a key tile.  A unit cut
 //    that way leaves its parts' maxima, sums and unnormalised O in the workspace, and a merge kernel
@@ -78,7 +83,9 @@ constexpr int kPmSnap = 2;
 // CTA) take as long as in slices, 124 us with launch; at two, 2 prompts of 2048 do, 77 us.
 constexpr int kPmQueued = 3;
 constexpr int kPmRows = 2 * kPmTile;              // packed rows of a unit
-constexpr uint32_t kPmWaitPolls = 1u << 18;       // a poll suspends for up to 4 us: about a second
+// A wait ends after this many polls.  One that finds its barrier open took 7776 cycles (4 us), which makes a
+// second of them; how long a poll suspends is up to the hardware, so the time is not a promise.
+constexpr uint32_t kPmWaitPolls = 1u << 18;
 
 // Tensor-memory columns of the 512 a CTA takes: S (and P) of tile 0 and 1, O of tile 0 and 1.
 constexpr uint32_t kPmColS = 0, kPmColO = 256;
@@ -1195,8 +1202,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
 
 // Merge of the units cut between CTAs: block (c, part) folds 32 rows of the unit whose first part is
 // CTA c's last piece, in CTA order; a warp takes four rows, four columns per lane, and has the parts
-// of kPmMergeDepth CTAs in flight.  Bound by the latency of its dependent reads: 7 to 10 us for the
-// parts of any call (eight rows a warp with one part in flight took 20 to 55).
+// of kPmMergeDepth CTAs in flight.  Bound by the latency of its dependent reads, which grows with the
+// parts of a unit (one per CTA at most): sixteen short turns behind up to 32768 tokens 11.1 us on its own,
+// 7 us behind the last block when chained (eight rows a warp with one part in flight took 20 to 55).
 constexpr int kPmMergeParts = 8, kPmMergeWarps = 8, kPmMergeDepth = 8;
 constexpr int kPmMaxCtas = 1024;  // (c << 20 fits 32 bits in the slice search)
 
