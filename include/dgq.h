@@ -349,8 +349,9 @@ dgq_status dgq_paged_decode_attn_bf16(const void *q_bf16, const void *k_new_bf16
  * cu_q_dev, cu_kv_dev  [batch+1] int32, device, non-decreasing, at most total_q / total_kv (a
  *                   request that is not is flagged in the workspace and cut to the buffers).
  * Supported: Hq % Hkv == 0 with G = Hq / Hkv in {1, 2, 4, 8}; at most 2^30 keys or rows.  A request's
- * own rows must be finite (a key that a row does not see has weight 0, and 0 times an infinite value
- * is not a number); rows of other requests, and behind the last one, cannot reach its output.
+ * own rows, and in fp32 the products q . k, must be finite (a key that a row does not see has weight 0,
+ * and 0 times an infinite value is not a number); rows of other requests, and behind the last one,
+ * cannot reach its output.
  * One launch of one block per SM (tensor memory and most of the shared memory of each), and one that
  * merges the rows whose keys several blocks share, in a fixed order: bitwise repeatable on a given GPU.
  * workspace         >= dgq_prompt_attn_workspace_size(batch, Hq, Hkv) bytes, zero-filled before first use

@@ -67,6 +67,11 @@ namespace dgq {
 
 constexpr float kPmScale = 0.12751743074570180f;  // log2(e) / sqrt(128)
 constexpr float kPmLazy = 8.0f / kPmScale;        // the maximum moves when exceeded by 8 in the log2 domain
+// A weight is 2^(x s - fl(m s)), so the largest one is not 1 but 2^e with e the rounding of m s: the same factor
+// in numerator and sum, until from |m| = 2^31 on it leaves the range of fp32 (|e| <= 16 below).  There a power
+// of two stands for s, with which m s is exact; scores that differ do so by 128 or more, so that with either
+// factor any weight but the largest is below 2^-16, and with it below what P's bf16 can add to it.
+constexpr float kPmFar = 2147483648.0f;
 constexpr int kPmTile = 128;                      // rows of a tile, keys of a key tile
 constexpr int kPmStages = 4;
 constexpr int kPmTileBytes = kPmTile * kD * 2;    // 32 KB: two halves of 64 columns, [row][64] each
@@ -1070,8 +1075,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                         tc_st16(to + 16 * c, o);
                     }
                 }
-                const float ref = m == -INFINITY ? 0.0f : -m * kPmScale;
-                const uint64_t sc2 = pack2(kPmScale, kPmScale), ref2 = pack2(ref, ref);
+                const float sc = fabsf(m) < kPmFar ? kPmScale : 0.125f;
+                const float ref = m == -INFINITY ? 0.0f : -m * sc;
+                const uint64_t sc2 = pack2(sc, sc), ref2 = pack2(ref, ref);
                 uint64_t sum[2] = {0ull, 0ull};
                 auto weights = [&](const uint32_t *v, int c) {
                     uint32_t p[16];
