@@ -8,8 +8,9 @@
 // What bounds it.  4 * 128 flop per (row, key) pair against 512 bytes per key and KV head: the tensor
 // cores for prompts (one prompt of 16384 tokens, 32 query and 8 KV heads: 2.2 Tflop for 336 MB), HBM
 // for a few rows behind a long history.  Measured on a GB300: 1.23 ms for that prompt, 1788 TFLOP/s,
-// 96% of a cuBLAS product's burst rate (1.35 ms, 96% of the sustained rate, in a long run under the
-// power cap); 202 us for eight prompts of 2048; 88 us for sixteen short turns over 438 MB of cache.
+// 96% of a cuBLAS product's burst rate (1.34 to 1.36 ms, 95 to 97% of the sustained rate, in a long run
+// under the power cap); 188 us for eight prompts of 2048 (208 there); 86 to 89 us for sixteen short turns
+// over 438 MB of cache.
 //
 // GPU design.
 //  * Rows: the G query heads of a KV head are packed into the rows of one product (row r of a tile is
