@@ -627,7 +627,8 @@ class BlockPool:
 
     def fork_row(self, length: int, block_size: int, table, src_row: int, dst_row: int):
         """Row dst_row of the host table becomes a fork of src_row's first `length` tokens; returns the
-        pages to copy, int32 numpy [0 or 1, 2] (source, destination)."""
+        pages to copy, int32 numpy [0 or 1, 2] (source, destination).  INT8 rows: dgq_fork_records writes
+        the fork's records for the same length."""
         import numpy as np
         pairs, n = np.zeros((1, 2), dtype=np.int32), ctypes.c_int32(0)
         _check(lib().dgq_pool_fork_row(self._h, length, block_size, _host_table(table, src_row, dst_row), src_row,
