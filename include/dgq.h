@@ -36,7 +36,7 @@
  *     state, so calls from several threads at once are safe (each on its own stream and
  *     workspace, as above), on any number of devices.
  *   - CUDA graphs: every compute call (compress, decode, append, the prefill calls, the
- *     comparison formats, prompt attention, the page and fork calls) enqueues only kernel launches and
+ *     comparison formats, prompt attention, the block cache, table, page and fork calls) enqueues only kernel launches and
  *     workspace memsets on its stream, with no host synchronisation, so it may be captured into
  *     a graph on a capturing stream;
  *     a replay does what the call does.  Make one call on the device and host thread first
@@ -332,6 +332,101 @@ dgq_status dgq_paged_decode_attn_bf16(const void *q_bf16, const void *k_new_bf16
                                       void *cuda_stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Decode with a sliding window and sinks: the same step where the new token (position L_b) sees the last
+ * `window` tokens, itself among them, and the first `sinks` ones: the cached tokens t < L_b with
+ * t > L_b - window or t < sinks.  A window that reaches the start of a request changes nothing for it.
+ *
+ * window            >= 1 (1: the new token and the sinks); sinks >= 0.  Else DGQ_ERR_INVALID_ARG.
+ * Only tiles of 16 tokens with a visible one are read, from the first to the last by the block table: the
+ * entries of blocks without a visible token may hold anything, and those blocks' contents too, so a
+ * serving loop may give them back.  The tokens of a block that holds a visible one have to be finite.
+ * Time and reads follow what is seen, not L_b.  Other arguments, limits, the workspace and its size as
+ * dgq_paged_decode_attn (caches of dgq_compress, dgq_append and DGQ_FORMAT_SYM_INT8) and
+ * dgq_paged_decode_attn_bf16.
+ */
+dgq_status dgq_paged_decode_attn_window(const void *q_bf16, const void *k_new_bf16, const void *v_new_bf16,
+                                        const uint8_t *k_pool, const uint8_t *v_pool, const dgq_seg_record *seg_table,
+                                        const int32_t *block_tables_dev, const int32_t *seq_lens_dev,
+                                        int32_t max_seqlen, int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                        int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
+                                        int32_t num_blocks, int32_t window, int32_t sinks, void *out_bf16,
+                                        void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+dgq_status dgq_paged_decode_attn_bf16_window(const void *q_bf16, const void *k_new_bf16, const void *v_new_bf16,
+                                             const void *k_src_bf16, const void *v_src_bf16, int32_t num_src_blocks,
+                                             const int32_t *src_block_tables_dev, int32_t max_src_blocks_per_seq,
+                                             const int32_t *seq_lens_dev, int32_t max_seqlen, int32_t batch,
+                                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                             int32_t block_size, int32_t window, int32_t sinks, void *out_bf16,
+                                             void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/* ---------------------------------------------------------------------------------------
+ * A paged cache in 8 bits with one scale per block and KV head: encoded as tokens arrive, from the first
+ * one on, with no pass over a whole request and no record (dgq_compress needs both), at the price of
+ * scales that know nothing of the variance along the tokens.
+ *
+ * Pools [num_blocks, Hkv, block_size, 128] uint8 and scales [num_blocks, Hkv] fp32, of K and of V.  For
+ * the tokens of a block and head: s = the smallest bfloat16 number not below amax / 127 (INT8) or
+ * amax / 448 (E4M3), amax their largest |x| (s = 0 where it is below 2^-80); x is stored as x / s rounded
+ * to the nearest whole number q, ties to even, as the byte 128 + q, or to the nearest E4M3 number, ties to
+ * even, as its byte; the value of a code is q s or (E4M3 number) s.  (s has 8 significant bits so that no
+ * quotient of a bfloat16 value lies close to a tie: codes do not depend on how it is computed.)
+ *
+ * dgq_store_block8: rows stored by slot (block * block_size + place, as dgq_extend_tables makes them).
+ * Tokens of one block come one behind the other, in the order of their places; the places of a block in front
+ * of a run's first one hold its earlier tokens.  With them, s becomes the larger of the scale that is there
+ * and that of the new values, and where it grows the codes in front are made anew from the values that
+ * they stand for, once rounded.  A run that starts at place 0 starts the block anew, whatever was there.
+ * Places behind the run are not written.  A slot that is named twice, or a block whose places come in
+ * several runs of one call, ends up with one run's scale and codes of either.
+ *
+ * format            DGQ_BLOCK8_INT8 or DGQ_BLOCK8_E4M3.
+ * k_bf16, v_bf16    rows [num_tokens][Hkv][128] bf16, device, tokens k_token_stride / v_token_stride
+ *                   elements apart (a multiple of 8, at least Hkv * 128: slices of a fused projection);
+ *                   finite, |x| < 2^100.
+ * slots_dev         [num_tokens] int32, device; -1: the token is left out.  Any other slot outside
+ *                   [0, num_blocks * block_size) is flagged in the workspace and left out.
+ * workspace         >= dgq_block8_workspace_size() bytes, zero-filled before first use.
+ * Blocks that a fork shares need dgq_pool_own_row first, as before any write.  No tokens: nothing is launched.
+ * Supported: num_tokens * Hkv < 2^27.
+ */
+#define DGQ_BLOCK8_INT8 0
+#define DGQ_BLOCK8_E4M3 1
+
+dgq_status dgq_store_block8(int32_t format, const void *k_bf16, const void *v_bf16, int64_t k_token_stride,
+                            int64_t v_token_stride, int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                            const int32_t *slots_dev, uint8_t *k_pool, uint8_t *v_pool, float *k_scales,
+                            float *v_scales, int32_t num_blocks, int32_t block_size, void *workspace,
+                            size_t workspace_bytes, void *cuda_stream);
+
+size_t dgq_block8_workspace_size(void);
+
+/* Rows of an 8-bit block cache back in bf16 (each value rounded once), packed as dgq_prompt_attn and
+ * dgq_compress read them: for the attention of a prompt chunk behind an 8-bit history.
+ * cu_kv_dev         [batch+1] int32, device: request b's first cu_kv[b+1] - cu_kv[b] tokens go to rows
+ *                   cu_kv[b] .. (a request outside the total_kv rows, or longer than its table row, is
+ *                   flagged in the workspace and cut).  Rows that no request owns are not written.
+ * k_bf16, v_bf16    [total_kv, Hkv, 128] bf16, device.
+ * A block-table entry outside [0, num_blocks) is flagged in the workspace (block 0 read instead). */
+dgq_status dgq_load_block8(int32_t format, const uint8_t *k_pool, const uint8_t *v_pool, const float *k_scales,
+                           const float *v_scales, int32_t num_blocks, int32_t block_size,
+                           const int32_t *block_tables_dev, int32_t max_blocks_per_seq, const int32_t *cu_kv_dev,
+                           int32_t batch, int32_t num_kv_heads, int32_t head_dim, void *k_bf16, void *v_bf16,
+                           int32_t total_kv, void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/* dgq_paged_decode_attn over an 8-bit block cache (scales 0 or 2^-100 .. 2^100), of all cached tokens
+ * (window == 0 and sinks == 0) or of a window and sinks as above.  Same kernel, work split, merge order,
+ * limits and workspace (dgq_attn_workspace_size). */
+dgq_status dgq_paged_decode_attn_block8(int32_t format, const void *q_bf16, const void *k_new_bf16,
+                                        const void *v_new_bf16, const uint8_t *k_pool, const uint8_t *v_pool,
+                                        const float *k_scales, const float *v_scales, const int32_t *block_tables_dev,
+                                        const int32_t *seq_lens_dev, int32_t max_seqlen, int32_t batch,
+                                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t block_size, int32_t max_blocks_per_seq, int32_t num_blocks,
+                                        int32_t window, int32_t sinks, void *out_bf16, void *workspace,
+                                        size_t workspace_bytes, void *cuda_stream);
+
+/* ---------------------------------------------------------------------------------------
  * dgq_prompt_attn -- causal grouped-query attention of whole prompts over bf16 K and V: what a
  * layer computes at prefill, on the rows dgq_compress then encodes.
  *
@@ -375,6 +470,25 @@ dgq_status dgq_prompt_attn_paged(const void *q_bf16, int32_t total_q, const int3
                                  int32_t max_src_blocks_per_seq, const int32_t *seq_lens_dev, int32_t batch,
                                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                  void *out_bf16, void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/* Prompt attention with a sliding window and sinks: the row at position p = m - n + i sees the keys t <= p
+ * with t > p - window or t < sinks (window >= 1, sinks >= 0, else DGQ_ERR_INVALID_ARG).  Only key tiles
+ * that a row of a tile of rows sees are read.  Paged: the table entries of blocks without a key that any row of the
+ * request sees may hold anything, and those blocks' contents too; the tokens of every other block have to
+ * be finite.  Other arguments, limits and the workspace as dgq_prompt_attn and dgq_prompt_attn_paged. */
+dgq_status dgq_prompt_attn_window(const void *q_bf16, const void *k_bf16, const void *v_bf16, int32_t total_q,
+                                  int32_t total_kv, const int32_t *cu_q_dev, const int32_t *cu_kv_dev, int32_t batch,
+                                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t window,
+                                  int32_t sinks, void *out_bf16, void *workspace, size_t workspace_bytes,
+                                  void *cuda_stream);
+
+dgq_status dgq_prompt_attn_paged_window(const void *q_bf16, int32_t total_q, const int32_t *cu_q_dev,
+                                        const void *k_src_bf16, const void *v_src_bf16, int32_t num_src_blocks,
+                                        const int32_t *src_block_tables_dev, int32_t max_src_blocks_per_seq,
+                                        const int32_t *seq_lens_dev, int32_t batch, int32_t num_q_heads,
+                                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t window,
+                                        int32_t sinks, void *out_bf16, void *workspace, size_t workspace_bytes,
+                                        void *cuda_stream);
 
 /* ---------------------------------------------------------------------------------------
  * dgq_paged_decode_attn_noalloc -- the same decode attention for callers that cannot
@@ -603,6 +717,52 @@ dgq_status dgq_workspace_init(void *workspace, size_t workspace_bytes, void *cud
  * Returns DGQ_ERR_DEVICE when the word is non-zero.  The workspace must be re-initialised
  * after a device-side error. */
 dgq_status dgq_workspace_error(const void *workspace, void *cuda_stream, int32_t *device_error);
+
+/* ---------------------------------------------------------------------------------------
+ * dgq_extend_tables -- block tables grown and a slot map made on the GPU from the requests' lengths, so that
+ * steps can follow one another (or be replayed as a graph) without the host: the blocks come from a list of
+ * free ids that the host took from its pool ahead (dgq_pool_alloc).
+ *
+ * Request b has L = seq_lens[b] cached tokens in the first ceil(L / bs) entries of its table row and gets
+ * n = new_lens[b] new ones.  Its next ceil((L + n) / bs) - ceil(L / bs) entries are written with the next
+ * ids of the list, in request order; the packed rows of its new tokens start at cu_new[b], and new token i
+ * has slot table[(L + i) / bs] * bs + (L + i) % bs.
+ *
+ * seq_lens_dev, new_lens_dev  [batch] int32, device.
+ * free_ids_dev      [num_free] int32, device; free_used_dev [1] int32, device: how many of them are used.
+ * block_tables_dev  [batch, max_blocks_per_seq] int32, device: new entries are written, no others.
+ * slots_dev         [total_slots] int32, device, written in full: -1 for tokens without a place, and
+ *                   behind the last request's (a padded step).
+ * cu_new_dev        [batch+1] int32, device: exclusive sums of new_lens.
+ * seq_lens_out_dev  [batch] int32, device: L + n; may be seq_lens_dev itself.
+ * free_used_out_dev [1] int32, device; may be free_used_dev itself.
+ * A request for which the list is too short (none behind it gets blocks either; later requests that
+ * need none are served), whose L or n is negative, which outgrows its table row, or whose rows lie
+ * behind total_slots, is flagged in the workspace and gets nothing: slots -1, length and table row as they
+ * were.  An id of the list, or of the table row where its last block has room, outside [0, num_blocks) is
+ * flagged; its tokens' slots are -1 and its entry is not written.
+ * workspace         >= dgq_extend_tables_workspace_size() bytes, zero-filled before first use.
+ * One launch.  Supported: num_blocks * bs < 2^31, max_blocks_per_seq * bs <= 2^30.
+ */
+dgq_status dgq_extend_tables(const int32_t *seq_lens_dev, const int32_t *new_lens_dev, int32_t batch,
+                             int32_t block_size, int32_t num_blocks, const int32_t *free_ids_dev, int32_t num_free,
+                             const int32_t *free_used_dev, int32_t *block_tables_dev, int32_t max_blocks_per_seq,
+                             int32_t *slots_dev, int32_t total_slots, int32_t *cu_new_dev, int32_t *seq_lens_out_dev,
+                             int32_t *free_used_out_dev, void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+size_t dgq_extend_tables_workspace_size(void);
+
+/* Rows of new tokens written to a bf16 paged cache by slot: row i's head h goes to
+ * pages[slots[i] / bs][h][slots[i] % bs].
+ * k_bf16, v_bf16, strides, slots_dev: as dgq_store_block8 (values are copied, whatever they are).  A slot that
+ * is named twice holds one of the rows, or parts of both.
+ * k_pages_bf16, v_pages_bf16  [num_blocks, Hkv, bs, 128] bf16, device: the cache that dgq_compress_paged, the
+ *                   prefill calls and the bf16 attention calls read.
+ * workspace         >= dgq_extend_tables_workspace_size() bytes, zero-filled before first use. */
+dgq_status dgq_write_slots(const void *k_bf16, const void *v_bf16, int64_t k_token_stride, int64_t v_token_stride,
+                           int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim, const int32_t *slots_dev,
+                           void *k_pages_bf16, void *v_pages_bf16, int32_t num_blocks, int32_t block_size,
+                           void *workspace, size_t workspace_bytes, void *cuda_stream);
 
 /* ---------------------------------------------------------------------------------------
  * dgq_copy_pages -- pages copied between slots of a paged cache: the device half of forking a

@@ -24,6 +24,7 @@ FORMAT_DGQ = 0
 FORMAT_FIXED64 = 1
 FORMAT_SYM_INT8 = 2
 FORMAT_FP8_E4M3 = 3
+BLOCK8_FORMATS = {"int8": 0, "e4m3": 1}  # codes of a cache with one scale per block and head
 FORMATS = {"dgq": FORMAT_DGQ, "fixed64": FORMAT_FIXED64, "sym_int8": FORMAT_SYM_INT8, "fp8_e4m3": FORMAT_FP8_E4M3}
 
 __all__ = [
@@ -34,6 +35,8 @@ __all__ = [
     "dgq_prefill_finish", "dgq_paged_decode_attn_split", "dgq_append_split", "dgq_append_ex",
     "dgq_prompt_attn", "dgq_prompt_attn_paged", "dgq_prompt_attn_workspace_size", "dgq_paged_decode_attn_bf16",
     "dgq_copy_pages", "dgq_copy_pages_workspace_size", "dgq_remap_tables", "dgq_fork_records",
+    "dgq_extend_tables", "dgq_extend_tables_workspace_size", "dgq_write_slots", "dgq_store_block8", "dgq_load_block8",
+    "dgq_block8_workspace_size", "dgq_paged_decode_attn_block8", "BLOCK8_FORMATS",
     "dgq_prefill_finish_ex", "RESEG_WINDOW", "RESEG_NGROUPS",
     "dgq_attn_workspace_size", "dgq_workspace_init", "dgq_workspace_error", "BlockPool",
     "seg_record_dtype",
@@ -129,6 +132,27 @@ def lib() -> ctypes.CDLL:
         L.dgq_remap_tables.restype = ctypes.c_int
         L.dgq_fork_records.argtypes = [P, i32, i32, P, i32, P, sz, P]
         L.dgq_fork_records.restype = ctypes.c_int
+        i64 = ctypes.c_int64
+        L.dgq_paged_decode_attn_window.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, i32,
+                                                   i32, P, P, sz, P]
+        L.dgq_paged_decode_attn_bf16_window.argtypes = [P, P, P, P, P, i32, P, i32, P, i32, i32, i32, i32, i32, i32,
+                                                        i32, i32, P, P, sz, P]
+        L.dgq_paged_decode_attn_block8.argtypes = [i32, P, P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32,
+                                                   i32, i32, i32, P, P, sz, P]
+        L.dgq_prompt_attn_window.argtypes = [P, P, P, i32, i32, P, P, i32, i32, i32, i32, i32, i32, P, P, sz, P]
+        L.dgq_prompt_attn_paged_window.argtypes = [P, i32, P, P, P, i32, P, i32, P, i32, i32, i32, i32, i32, i32, i32,
+                                                   P, P, sz, P]
+        L.dgq_extend_tables.argtypes = [P, P, i32, i32, i32, P, i32, P, P, i32, P, i32, P, P, P, P, sz, P]
+        L.dgq_write_slots.argtypes = [P, P, i64, i64, i32, i32, i32, P, P, P, i32, i32, P, sz, P]
+        L.dgq_store_block8.argtypes = [i32, P, P, i64, i64, i32, i32, i32, P, P, P, P, P, i32, i32, P, sz, P]
+        L.dgq_load_block8.argtypes = [i32, P, P, P, P, i32, i32, P, i32, P, i32, i32, i32, P, P, i32, P, sz, P]
+        for f in ("paged_decode_attn_window", "paged_decode_attn_bf16_window", "paged_decode_attn_block8",
+                  "prompt_attn_window", "prompt_attn_paged_window", "extend_tables", "write_slots", "store_block8",
+                  "load_block8"):
+            getattr(L, "dgq_" + f).restype = ctypes.c_int
+        for f in ("extend_tables", "block8"):
+            getattr(L, f"dgq_{f}_workspace_size").argtypes = []
+            getattr(L, f"dgq_{f}_workspace_size").restype = sz
         L.dgq_pool_create.argtypes = [i32]
         L.dgq_pool_create.restype = P
         L.dgq_pool_destroy.argtypes = [P]
@@ -331,12 +355,29 @@ def dgq_compress_paged(k_src, v_src, src_block_tables, cu_seqlens, max_seqlen, b
                                     _nbytes(workspace), ctypes.byref(opts), _stream(stream)), "dgq_compress_paged")
 
 
+def _windowed(what: str, window, sinks) -> bool:
+    """Whether a call has a window (0: none, and then no sinks either)."""
+    if window == 0 and sinks == 0:
+        return False
+    if window < 1 or sinks < 0:
+        raise DGQError(-1, what)
+    return True
+
+
 def dgq_paged_decode_attn(q, k_new, v_new, k_pool, v_pool, seg_table, block_tables, seq_lens, max_seqlen,
-                          out, workspace, stream=None) -> None:
+                          out, workspace, stream=None, window=0, sinks=0) -> None:
     """q bf16 [B, Hq, 128]; k_new, v_new bf16 [B, Hkv, 128]; pools / seg_table / block_tables as
-    written by dgq_compress; seq_lens int32 [B]; out bf16 [B, Hq, 128]."""
+    written by dgq_compress; seq_lens int32 [B]; out bf16 [B, Hq, 128].  window > 0: the new token sees the
+    last `window` tokens (itself among them) and the first `sinks` ones (dgq_paged_decode_attn_window)."""
     B, Hq, D = q.shape
     Hkv = k_new.shape[1]
+    if _windowed("dgq_paged_decode_attn", window, sinks):
+        _check(lib().dgq_paged_decode_attn_window(
+            _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool), _ptr(seg_table), _ptr(block_tables),
+            _ptr(seq_lens), int(max_seqlen), B, Hq, Hkv, D, k_pool.shape[2], block_tables.shape[1], k_pool.shape[0],
+            int(window), int(sinks), _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+            "dgq_paged_decode_attn")
+        return
     _check(lib().dgq_paged_decode_attn(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool),
                                        _ptr(seg_table), _ptr(block_tables), _ptr(seq_lens), int(max_seqlen),
                                        B, Hq, Hkv, D, k_pool.shape[2], block_tables.shape[1], k_pool.shape[0],
@@ -415,10 +456,10 @@ def dgq_paged_decode_attn_split(q, k_new, v_new, k_pool, v_pool, k_seg_table, v_
 
 
 def dgq_paged_decode_attn_bf16(q, k_new, v_new, k_src, v_src, src_block_tables, seq_lens, max_seqlen, out, workspace,
-                               stream=None) -> None:
+                               stream=None, window=0, sinks=0) -> None:
     """dgq_paged_decode_attn over an unquantised cache: k_src, v_src bf16 paged cache
     [num_src_blocks, Hkv, bs, 128] with src_block_tables int32 [B, max_src_blocks]; the other
-    arguments and the workspace (dgq_attn_workspace_size) as there."""
+    arguments and the workspace (dgq_attn_workspace_size) as there, window and sinks too."""
     torch = _torch()
     bf16, i32 = torch.bfloat16, torch.int32
     B, Hq, D = q.shape
@@ -429,6 +470,12 @@ def dgq_paged_decode_attn_bf16(q, k_new, v_new, k_src, v_src, src_block_tables, 
         "dgq_paged_decode_attn_bf16", workspace, (q, bf16, (B, Hq, D)), (k_new, bf16, new), (v_new, bf16, new),
         (k_src, bf16, cache), (v_src, bf16, cache), (src_block_tables, i32, (B, columns)), (seq_lens, i32, (B,)),
         (out, bf16, (B, Hq, D)))
+    if _windowed("dgq_paged_decode_attn_bf16", window, sinks):
+        _check(lib().dgq_paged_decode_attn_bf16_window(q_, kn, vn, k, v, blocks, bt, columns, lens, int(max_seqlen), B,
+                                                       Hq, Hkv, D, bs, int(window), int(sinks), o, ws,
+                                                       _nbytes(workspace), _stream(stream)),
+               "dgq_paged_decode_attn_bf16")
+        return
     _check(lib().dgq_paged_decode_attn_bf16(q_, kn, vn, k, v, blocks, bt, columns, lens, int(max_seqlen), B, Hq, Hkv, D,
                                             bs, o, ws, _nbytes(workspace), _stream(stream)),
            "dgq_paged_decode_attn_bf16")
@@ -486,10 +533,11 @@ def dgq_prompt_attn_workspace_size(batch: int, num_q_heads: int, num_kv_heads: i
     return int(lib().dgq_prompt_attn_workspace_size(batch, num_q_heads, num_kv_heads))
 
 
-def dgq_prompt_attn(q, k, v, cu_q, cu_kv, out, workspace, stream=None) -> None:
+def dgq_prompt_attn(q, k, v, cu_q, cu_kv, out, workspace, stream=None, window=0, sinks=0) -> None:
     """Causal attention of packed prompts: q, out bf16 [Tq, Hq, 128]; k, v bf16 [Tkv, Hkv, 128]; cu_q,
     cu_kv int32 [B+1] (queries and keys of a request end at the same token); workspace uint8
-    (dgq_prompt_attn_workspace_size bytes).  All CUDA tensors."""
+    (dgq_prompt_attn_workspace_size bytes).  All CUDA tensors.  window > 0: a row sees the last `window`
+    keys up to its own and the first `sinks` ones (dgq_prompt_attn_window)."""
     torch = _torch()
     bf16, i32 = torch.bfloat16, torch.int32
     Tq, Hq, D = q.shape
@@ -498,11 +546,16 @@ def dgq_prompt_attn(q, k, v, cu_q, cu_kv, out, workspace, stream=None) -> None:
     q_, k_, v_, cq, ck, o, ws = _operands(
         "dgq_prompt_attn", workspace, (q, bf16, (Tq, Hq, D)), (k, bf16, (T, Hkv, D)), (v, bf16, (T, Hkv, D)),
         (cu_q, i32, (B + 1,)), (cu_kv, i32, (B + 1,)), (out, bf16, (Tq, Hq, D)))
+    if _windowed("dgq_prompt_attn", window, sinks):
+        _check(lib().dgq_prompt_attn_window(q_, k_, v_, Tq, T, cq, ck, B, Hq, Hkv, D, int(window), int(sinks), o, ws,
+                                            _nbytes(workspace), _stream(stream)), "dgq_prompt_attn")
+        return
     _check(lib().dgq_prompt_attn(q_, k_, v_, Tq, T, cq, ck, B, Hq, Hkv, D, o, ws, _nbytes(workspace),
                                  _stream(stream)), "dgq_prompt_attn")
 
 
-def dgq_prompt_attn_paged(q, cu_q, k_src, v_src, src_block_tables, seq_lens, out, workspace, stream=None) -> None:
+def dgq_prompt_attn_paged(q, cu_q, k_src, v_src, src_block_tables, seq_lens, out, workspace, stream=None, window=0,
+                          sinks=0) -> None:
     """dgq_prompt_attn over a bf16 paged cache: k_src, v_src bf16 [num_src_blocks, Hkv, bs, 128],
     src_block_tables int32 [B, max_src_blocks], seq_lens int32 [B] (keys of each request, the chunk's
     own among them); the rest as dgq_prompt_attn."""
@@ -516,8 +569,127 @@ def dgq_prompt_attn_paged(q, cu_q, k_src, v_src, src_block_tables, seq_lens, out
         "dgq_prompt_attn_paged", workspace, (q, bf16, (Tq, Hq, D)), (k_src, bf16, cache), (v_src, bf16, cache),
         (cu_q, i32, (B + 1,)), (seq_lens, i32, (B,)), (src_block_tables, i32, (B, columns)),
         (out, bf16, (Tq, Hq, D)))
+    if _windowed("dgq_prompt_attn_paged", window, sinks):
+        _check(lib().dgq_prompt_attn_paged_window(q_, Tq, cq, k, v, blocks, bt, columns, lens, B, Hq, Hkv, D, bs,
+                                                  int(window), int(sinks), o, ws, _nbytes(workspace),
+                                                  _stream(stream)), "dgq_prompt_attn_paged")
+        return
     _check(lib().dgq_prompt_attn_paged(q_, Tq, cq, k, v, blocks, bt, columns, lens, B, Hq, Hkv, D, bs, o, ws,
                                        _nbytes(workspace), _stream(stream)), "dgq_prompt_attn_paged")
+
+
+def dgq_extend_tables_workspace_size() -> int:
+    return int(lib().dgq_extend_tables_workspace_size())
+
+
+def dgq_extend_tables(seq_lens, new_lens, block_size, num_blocks, free_ids, free_used, block_tables, slots, cu_new,
+                      seq_lens_out, free_used_out, workspace, stream=None) -> None:
+    """Block tables grown and a slot map made on the GPU.  seq_lens, new_lens int32 [B]: tokens there and new
+    ones; free_ids int32 [n], free_used int32 [1]: a list of free block ids and how many of them are used;
+    block_tables int32 [B, max_blocks], updated in place; slots int32 [T] (block * block_size + place of each
+    new token, -1 for one that has none); cu_new int32 [B+1]; seq_lens_out int32 [B] and free_used_out int32
+    [1] (seq_lens and free_used themselves, or others); workspace uint8 (dgq_extend_tables_workspace_size
+    bytes).  All CUDA tensors."""
+    i32 = _torch().int32
+    B, columns = block_tables.shape
+    lens, new, ids, used, table, slots_, cu, lens_out, used_out, ws = _operands(
+        "dgq_extend_tables", workspace, (seq_lens, i32, (B,)), (new_lens, i32, (B,)), (free_ids, i32, (free_ids.numel(),)),
+        (free_used, i32, (1,)), (block_tables, i32, (B, columns)), (slots, i32, (slots.numel(),)), (cu_new, i32, (B + 1,)),
+        (seq_lens_out, i32, (B,)), (free_used_out, i32, (1,)))
+    _check(lib().dgq_extend_tables(lens, new, B, int(block_size), int(num_blocks), ids, free_ids.numel(), used, table,
+                                   columns, slots_, slots.numel(), cu, lens_out, used_out, ws, _nbytes(workspace),
+                                   _stream(stream)), "dgq_extend_tables")
+
+
+def _token_rows(what: str, *xs) -> list:
+    """Addresses and token strides of bf16 rows [T, Hkv, 128] whose heads lie side by side (slices of a fused
+    projection's output)."""
+    bf16, device, shape = _torch().bfloat16, _device(), xs[0].shape
+    at = []
+    for x in xs:
+        step, head, one = x.stride()
+        if x.dtype is not bf16 or x.shape != shape or one != 1 or (head != shape[2] and shape[1] > 1) or \
+                x.get_device() != device:
+            raise DGQError(-1, what)
+        at += [x.data_ptr(), step]
+    return at
+
+
+def dgq_write_slots(k, v, slots, k_pages, v_pages, workspace, stream=None) -> None:
+    """Rows of new tokens into a bf16 paged cache: k, v bf16 [T, Hkv, 128] (slices of a fused projection's
+    output may be passed as they are); slots int32 [T] as dgq_extend_tables makes them (-1: left out);
+    k_pages, v_pages bf16 [num_blocks, Hkv, bs, 128]; workspace uint8 (dgq_extend_tables_workspace_size
+    bytes).  All CUDA tensors."""
+    torch = _torch()
+    T, Hkv, D = k.shape
+    blocks, _, bs, _ = k_pages.shape
+    cache = (torch.bfloat16, (blocks, Hkv, bs, D))
+    k_, k_step, v_, v_step = _token_rows("dgq_write_slots", k, v)
+    at, kp, vp, ws = _operands("dgq_write_slots", workspace, (slots, torch.int32, (T,)), (k_pages, *cache), (v_pages, *cache))
+    _check(lib().dgq_write_slots(k_, v_, k_step, v_step, T, Hkv, D, at, kp, vp, blocks, bs, ws, _nbytes(workspace),
+                                 _stream(stream)), "dgq_write_slots")
+
+
+def dgq_block8_workspace_size() -> int:
+    return int(lib().dgq_block8_workspace_size())
+
+
+def _block8_id(fmt) -> int:
+    return BLOCK8_FORMATS.get(fmt, -1) if isinstance(fmt, str) else int(fmt)
+
+
+def dgq_store_block8(fmt, k, v, slots, k_pool, v_pool, k_scales, v_scales, workspace, stream=None) -> None:
+    """Rows of new tokens into an 8-bit cache with one scale per block and head.  fmt: "int8" or "e4m3";
+    k, v and slots as dgq_write_slots; pools uint8 [num_blocks, Hkv, bs, 128] and scales fp32 [num_blocks, Hkv],
+    updated in place; workspace uint8 (dgq_block8_workspace_size bytes).  All CUDA tensors."""
+    torch = _torch()
+    u8, f32 = torch.uint8, torch.float32
+    T, Hkv, D = k.shape
+    blocks, _, bs, _ = k_pool.shape
+    cache, scale = (blocks, Hkv, bs, D), (blocks, Hkv)
+    k_, k_step, v_, v_step = _token_rows("dgq_store_block8", k, v)
+    at, kp, vp, ks, vs, ws = _operands(
+        "dgq_store_block8", workspace, (slots, torch.int32, (T,)), (k_pool, u8, cache), (v_pool, u8, cache),
+        (k_scales, f32, scale), (v_scales, f32, scale))
+    _check(lib().dgq_store_block8(_block8_id(fmt), k_, v_, k_step, v_step, T, Hkv, D, at, kp, vp, ks, vs, blocks, bs, ws,
+                                  _nbytes(workspace), _stream(stream)), "dgq_store_block8")
+
+
+def dgq_load_block8(fmt, k_pool, v_pool, k_scales, v_scales, block_tables, cu_kv, k, v, workspace, stream=None) -> None:
+    """Rows of an 8-bit block cache in bf16, packed for dgq_prompt_attn or dgq_compress: block_tables int32
+    [B, max_blocks]; cu_kv int32 [B+1]; k, v bf16 [T, Hkv, 128], written; the rest as dgq_store_block8."""
+    torch = _torch()
+    u8, f32, bf16, i32 = torch.uint8, torch.float32, torch.bfloat16, torch.int32
+    T, Hkv, D = k.shape
+    blocks, _, bs, _ = k_pool.shape
+    B, columns = block_tables.shape
+    cache, scale = (blocks, Hkv, bs, D), (blocks, Hkv)
+    kp, vp, ks, vs, table, cu, k_, v_, ws = _operands(
+        "dgq_load_block8", workspace, (k_pool, u8, cache), (v_pool, u8, cache), (k_scales, f32, scale),
+        (v_scales, f32, scale), (block_tables, i32, (B, columns)), (cu_kv, i32, (B + 1,)), (k, bf16, (T, Hkv, D)),
+        (v, bf16, (T, Hkv, D)))
+    _check(lib().dgq_load_block8(_block8_id(fmt), kp, vp, ks, vs, blocks, bs, table, columns, cu, B, Hkv, D, k_, v_, T, ws,
+                                 _nbytes(workspace), _stream(stream)), "dgq_load_block8")
+
+
+def dgq_paged_decode_attn_block8(fmt, q, k_new, v_new, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
+                                 max_seqlen, out, workspace, stream=None, window=0, sinks=0) -> None:
+    """dgq_paged_decode_attn over an 8-bit block cache (fmt, pools and scales as dgq_store_block8); the other
+    arguments and the workspace (dgq_attn_workspace_size) as there, window and sinks too."""
+    torch = _torch()
+    u8, f32, bf16, i32 = torch.uint8, torch.float32, torch.bfloat16, torch.int32
+    B, Hq, D = q.shape
+    blocks, Hkv, bs, _ = k_pool.shape
+    columns = block_tables.shape[1]
+    new, cache, scale = (B, Hkv, D), (blocks, Hkv, bs, D), (blocks, Hkv)
+    q_, kn, vn, kp, vp, ks, vs, bt, lens, o, ws = _operands(
+        "dgq_paged_decode_attn_block8", workspace, (q, bf16, (B, Hq, D)), (k_new, bf16, new), (v_new, bf16, new),
+        (k_pool, u8, cache), (v_pool, u8, cache), (k_scales, f32, scale), (v_scales, f32, scale),
+        (block_tables, i32, (B, columns)), (seq_lens, i32, (B,)), (out, bf16, (B, Hq, D)))
+    _windowed("dgq_paged_decode_attn_block8", window, sinks)
+    _check(lib().dgq_paged_decode_attn_block8(_block8_id(fmt), q_, kn, vn, kp, vp, ks, vs, bt, lens, int(max_seqlen), B,
+                                              Hq, Hkv, D, bs, columns, blocks, int(window), int(sinks), o, ws,
+                                              _nbytes(workspace), _stream(stream)), "dgq_paged_decode_attn_block8")
 
 
 def dgq_copy_pages_workspace_size() -> int:

@@ -25,10 +25,13 @@ UNITS = {
     "dgq_formats.cu": ["-fmad=false", "-prec-div=true", "-prec-sqrt=true"],
     "dgq_prefill.cu": ["-fmad=false", "-prec-div=true", "-prec-sqrt=true"],
     "dgq_attn.cu": [],
+    "dgq_attn_window.cu": [],
+    "dgq_block8.cu": ["-fmad=false", "-prec-div=true"],
     "dgq_host.cu": [],
     "dgq_noalloc.cu": [],
     "dgq_pages.cu": [],
     "dgq_prompt.cu": [],
+    "dgq_tables.cu": [],
 }
 
 

@@ -36,6 +36,11 @@ constexpr int32_t kMaxBatch = dgq::kMaxCallBatch;  // per-call limit (the kernel
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// A window and its sinks as the kernels take them (no request has more keys than this).
+int32_t held(int32_t x) { return x < (1 << 30) ? x : 1 << 30; }
+
+bool window_ok(int32_t window, int32_t sinks) { return window >= 1 && sinks >= 0; }
+
 bool block_size_ok(int32_t bs) { return bs == 16 || bs == 32 || bs == 64; }
 
 int device_sm_count(int *nsm)
@@ -281,7 +286,7 @@ dgq_status attn_impl(int32_t format, const void *q_bf16, const void *k_new_bf16,
                      const int32_t *block_tables_dev, const int32_t *seq_lens_dev, int32_t max_seqlen, int32_t batch,
                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                      int32_t max_blocks_per_seq, int32_t num_blocks, void *out_bf16, void *workspace,
-                     size_t workspace_bytes, void *cuda_stream);
+                     size_t workspace_bytes, void *cuda_stream, int32_t window = 0, int32_t sinks = 0);
 }  // namespace
 
 dgq_status dgq_paged_decode_attn_split(const void *q_bf16, const void *k_new_bf16, const void *v_new_bf16,
@@ -332,6 +337,55 @@ dgq_status dgq_paged_decode_attn_bf16(const void *q_bf16, const void *k_new_bf16
                      cuda_stream);
 }
 
+dgq_status dgq_paged_decode_attn_window(const void *q_bf16, const void *k_new_bf16, const void *v_new_bf16,
+                                        const uint8_t *k_pool, const uint8_t *v_pool, const dgq_seg_record *seg_table,
+                                        const int32_t *block_tables_dev, const int32_t *seq_lens_dev,
+                                        int32_t max_seqlen, int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                        int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
+                                        int32_t num_blocks, int32_t window, int32_t sinks, void *out_bf16,
+                                        void *workspace, size_t workspace_bytes, void *cuda_stream)
+{
+    if (!window_ok(window, sinks)) return DGQ_ERR_INVALID_ARG;
+    return attn_impl(DGQ_FORMAT_DGQ, q_bf16, k_new_bf16, v_new_bf16, k_pool, v_pool, seg_table, nullptr, nullptr,
+                     nullptr, block_tables_dev, seq_lens_dev, max_seqlen, batch, num_q_heads, num_kv_heads, head_dim,
+                     block_size, max_blocks_per_seq, num_blocks, out_bf16, workspace, workspace_bytes, cuda_stream,
+                     window, sinks);
+}
+
+dgq_status dgq_paged_decode_attn_bf16_window(const void *q_bf16, const void *k_new_bf16, const void *v_new_bf16,
+                                             const void *k_src_bf16, const void *v_src_bf16, int32_t num_src_blocks,
+                                             const int32_t *src_block_tables_dev, int32_t max_src_blocks_per_seq,
+                                             const int32_t *seq_lens_dev, int32_t max_seqlen, int32_t batch,
+                                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                             int32_t block_size, int32_t window, int32_t sinks, void *out_bf16,
+                                             void *workspace, size_t workspace_bytes, void *cuda_stream)
+{
+    if (!window_ok(window, sinks)) return DGQ_ERR_INVALID_ARG;
+    return attn_impl(dgq::kFormatBf16Cache, q_bf16, k_new_bf16, v_new_bf16, static_cast<const uint8_t *>(k_src_bf16),
+                     static_cast<const uint8_t *>(v_src_bf16), nullptr, nullptr, nullptr, nullptr,
+                     src_block_tables_dev, seq_lens_dev, max_seqlen, batch, num_q_heads, num_kv_heads, head_dim,
+                     block_size, max_src_blocks_per_seq, num_src_blocks, out_bf16, workspace, workspace_bytes,
+                     cuda_stream, window, sinks);
+}
+
+dgq_status dgq_paged_decode_attn_block8(int32_t format, const void *q_bf16, const void *k_new_bf16,
+                                        const void *v_new_bf16, const uint8_t *k_pool, const uint8_t *v_pool,
+                                        const float *k_scales, const float *v_scales, const int32_t *block_tables_dev,
+                                        const int32_t *seq_lens_dev, int32_t max_seqlen, int32_t batch,
+                                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t block_size, int32_t max_blocks_per_seq, int32_t num_blocks,
+                                        int32_t window, int32_t sinks, void *out_bf16, void *workspace,
+                                        size_t workspace_bytes, void *cuda_stream)
+{
+    if (format != DGQ_BLOCK8_INT8 && format != DGQ_BLOCK8_E4M3) return DGQ_ERR_INVALID_ARG;
+    if (!(window == 0 && sinks == 0) && !window_ok(window, sinks)) return DGQ_ERR_INVALID_ARG;
+    if (!k_scales || !v_scales || !aligned16(k_scales) || !aligned16(v_scales)) return DGQ_ERR_INVALID_ARG;
+    return attn_impl(format == DGQ_BLOCK8_E4M3 ? dgq::kFormatBlockE4m3 : dgq::kFormatBlockInt8, q_bf16, k_new_bf16,
+                     v_new_bf16, k_pool, v_pool, nullptr, nullptr, k_scales, v_scales, block_tables_dev, seq_lens_dev,
+                     max_seqlen, batch, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                     num_blocks, out_bf16, workspace, workspace_bytes, cuda_stream, window, sinks);
+}
+
 namespace {
 dgq_status attn_impl(int32_t format, const void *q_bf16, const void *k_new_bf16, const void *v_new_bf16,
                      const uint8_t *k_pool, const uint8_t *v_pool, const dgq_seg_record *seg_table,
@@ -339,7 +393,7 @@ dgq_status attn_impl(int32_t format, const void *q_bf16, const void *k_new_bf16,
                      const int32_t *block_tables_dev, const int32_t *seq_lens_dev, int32_t max_seqlen, int32_t batch,
                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                      int32_t max_blocks_per_seq, int32_t num_blocks, void *out_bf16, void *workspace,
-                     size_t workspace_bytes, void *cuda_stream)
+                     size_t workspace_bytes, void *cuda_stream, int32_t window, int32_t sinks)
 {
     if (format == DGQ_FORMAT_FIXED64 && (!k_group_params || !v_group_params || !aligned16(k_group_params) ||
                                          !aligned16(v_group_params)))
@@ -356,7 +410,7 @@ dgq_status attn_impl(int32_t format, const void *q_bf16, const void *k_new_bf16,
     if (chunks >= INT32_MAX || (int64_t)num_blocks * num_kv_heads * block_size >= INT32_MAX)
         return DGQ_ERR_UNSUPPORTED;
     if (!q_bf16 || !k_new_bf16 || !v_new_bf16 || !k_pool || !v_pool ||
-        (!seg_table && format != dgq::kFormatBf16Cache) || !block_tables_dev || !seq_lens_dev || !out_bf16)
+        (!seg_table && format < dgq::kFormatBf16Cache) || !block_tables_dev || !seq_lens_dev || !out_bf16)
         return DGQ_ERR_INVALID_ARG;
     if (!aligned16(q_bf16) || !aligned16(k_new_bf16) || !aligned16(v_new_bf16) || !aligned16(k_pool) ||
         !aligned16(v_pool) || !aligned16(seg_table) || !aligned16(out_bf16) || !aligned16(block_tables_dev) ||
@@ -371,7 +425,7 @@ dgq_status attn_impl(int32_t format, const void *q_bf16, const void *k_new_bf16,
     cudaError_t e = dgq::launch_attn(format, q_bf16, k_new_bf16, v_new_bf16, k_pool, v_pool, seg_table,
                                      v_seg_table, k_group_params, v_group_params, block_tables_dev, seq_lens_dev,
                                      max_seqlen, batch, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq,
-                                     num_blocks, out_bf16, workspace, nsm, &map_failed,
+                                     num_blocks, held(window), held(sinks), out_bf16, workspace, nsm, &map_failed,
                                      static_cast<cudaStream_t>(cuda_stream));
     if (map_failed) return DGQ_ERR_INVALID_ARG;
     return e == cudaSuccess ? DGQ_OK : DGQ_ERR_CUDA;
@@ -575,7 +629,7 @@ dgq_status prompt_impl(const void *q, const void *k, const void *v, int32_t tota
                        const int32_t *cu_q, const int32_t *kv, bool paged, const int32_t *bt, int32_t block_size,
                        int32_t max_blocks, int32_t num_blocks, int32_t batch, int32_t num_q_heads,
                        int32_t num_kv_heads, int32_t head_dim, void *out, void *workspace, size_t workspace_bytes,
-                       void *cuda_stream)
+                       void *cuda_stream, int32_t window = 0, int32_t sinks = 0)
 {
     if (head_dim != DGQ_HEAD_DIM || (paged && !block_size_ok(block_size))) return DGQ_ERR_UNSUPPORTED;
     if (batch <= 0 || batch > kMaxBatch || total_q < 0 || total_kv < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
@@ -606,8 +660,8 @@ dgq_status prompt_impl(const void *q, const void *k, const void *v, int32_t tota
     if (total_q == 0) return DGQ_OK;
     bool map_failed = false;
     const cudaError_t e = dgq::launch_prompt(q, k, v, total_q, total_kv, cu_q, kv, paged ? bt : nullptr, block_size,
-                                             max_blocks, num_blocks, batch, num_q_heads, num_kv_heads, out, workspace,
-                                             nsm, &map_failed, static_cast<cudaStream_t>(cuda_stream));
+                                             max_blocks, num_blocks, batch, num_q_heads, num_kv_heads, held(window),
+                                             held(sinks), out, workspace, nsm, &map_failed, static_cast<cudaStream_t>(cuda_stream));
     if (map_failed) return DGQ_ERR_INVALID_ARG;
     return e == cudaSuccess ? DGQ_OK : DGQ_ERR_CUDA;
 }
@@ -631,6 +685,159 @@ dgq_status dgq_prompt_attn_paged(const void *q_bf16, int32_t total_q, const int3
     return prompt_impl(q_bf16, k_src_bf16, v_src_bf16, total_q, 0, cu_q_dev, seq_lens_dev, true, src_block_tables_dev,
                        block_size, max_src_blocks_per_seq, num_src_blocks, batch, num_q_heads, num_kv_heads, head_dim,
                        out_bf16, workspace, workspace_bytes, cuda_stream);
+}
+
+dgq_status dgq_prompt_attn_window(const void *q_bf16, const void *k_bf16, const void *v_bf16, int32_t total_q,
+                                  int32_t total_kv, const int32_t *cu_q_dev, const int32_t *cu_kv_dev, int32_t batch,
+                                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t window,
+                                  int32_t sinks, void *out_bf16, void *workspace, size_t workspace_bytes,
+                                  void *cuda_stream)
+{
+    if (!window_ok(window, sinks)) return DGQ_ERR_INVALID_ARG;
+    return prompt_impl(q_bf16, k_bf16, v_bf16, total_q, total_kv, cu_q_dev, cu_kv_dev, false, nullptr, 0, 0, 0, batch,
+                       num_q_heads, num_kv_heads, head_dim, out_bf16, workspace, workspace_bytes, cuda_stream, window,
+                       sinks);
+}
+
+dgq_status dgq_prompt_attn_paged_window(const void *q_bf16, int32_t total_q, const int32_t *cu_q_dev,
+                                        const void *k_src_bf16, const void *v_src_bf16, int32_t num_src_blocks,
+                                        const int32_t *src_block_tables_dev, int32_t max_src_blocks_per_seq,
+                                        const int32_t *seq_lens_dev, int32_t batch, int32_t num_q_heads,
+                                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t window,
+                                        int32_t sinks, void *out_bf16, void *workspace, size_t workspace_bytes,
+                                        void *cuda_stream)
+{
+    if (!window_ok(window, sinks)) return DGQ_ERR_INVALID_ARG;
+    return prompt_impl(q_bf16, k_src_bf16, v_src_bf16, total_q, 0, cu_q_dev, seq_lens_dev, true, src_block_tables_dev,
+                       block_size, max_src_blocks_per_seq, num_src_blocks, batch, num_q_heads, num_kv_heads, head_dim,
+                       out_bf16, workspace, workspace_bytes, cuda_stream, window, sinks);
+}
+
+// ---- tables from lengths, rows by slot ----------------------------------------------------
+
+size_t dgq_extend_tables_workspace_size(void) { return 256; }  // the workspace header alone
+
+dgq_status dgq_extend_tables(const int32_t *seq_lens_dev, const int32_t *new_lens_dev, int32_t batch,
+                             int32_t block_size, int32_t num_blocks, const int32_t *free_ids_dev, int32_t num_free,
+                             const int32_t *free_used_dev, int32_t *block_tables_dev, int32_t max_blocks_per_seq,
+                             int32_t *slots_dev, int32_t total_slots, int32_t *cu_new_dev, int32_t *seq_lens_out_dev,
+                             int32_t *free_used_out_dev, void *workspace, size_t workspace_bytes, void *cuda_stream)
+{
+    if (!block_size_ok(block_size)) return DGQ_ERR_UNSUPPORTED;
+    if (batch <= 0 || batch > kMaxBatch || num_blocks <= 0 || max_blocks_per_seq <= 0 || num_free < 0 || total_slots < 0)
+        return DGQ_ERR_INVALID_ARG;
+    // slots, and the positions of a request, are 32-bit
+    if ((int64_t)num_blocks * block_size >= INT32_MAX || (int64_t)max_blocks_per_seq * block_size > (1 << 30))
+        return DGQ_ERR_UNSUPPORTED;
+    // an empty buffer has no address
+    if (!seq_lens_dev || !new_lens_dev || (num_free > 0 && !free_ids_dev) || !free_used_dev || !block_tables_dev ||
+        (total_slots > 0 && !slots_dev) || !cu_new_dev || !seq_lens_out_dev || !free_used_out_dev)
+        return DGQ_ERR_INVALID_ARG;
+    if (!aligned16(seq_lens_dev) || !aligned16(new_lens_dev) || !aligned16(free_ids_dev) || !aligned16(free_used_dev) ||
+        !aligned16(block_tables_dev) || !aligned16(slots_dev) || !aligned16(cu_new_dev) ||
+        !aligned16(seq_lens_out_dev) || !aligned16(free_used_out_dev))
+        return DGQ_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < dgq_extend_tables_workspace_size())
+        return DGQ_ERR_WORKSPACE;
+    int nsm = 0;
+    if (device_sm_count(&nsm) != 0) return DGQ_ERR_CUDA;
+    const dgq::ExtendArgs a = {seq_lens_dev,     new_lens_dev, free_ids_dev,       free_used_dev, block_tables_dev,
+                               slots_dev,        cu_new_dev,   seq_lens_out_dev,   free_used_out_dev, batch,
+                               block_size,       max_blocks_per_seq, num_blocks,   num_free,      total_slots};
+    const cudaError_t e = dgq::launch_extend_tables(a, workspace, nsm, static_cast<cudaStream_t>(cuda_stream));
+    return e == cudaSuccess ? DGQ_OK : DGQ_ERR_CUDA;
+}
+
+namespace {
+// Checks of rows that are written by slot (T tokens, k_stride and v_stride elements apart).
+dgq_status rows_checks(const void *k, const void *v, int64_t k_stride, int64_t v_stride, int32_t T, int32_t num_kv_heads,
+                       int32_t head_dim, const int32_t *slots, const void *k_pool, const void *v_pool,
+                       int32_t num_blocks, int32_t block_size, const void *workspace, size_t workspace_bytes)
+{
+    if (head_dim != DGQ_HEAD_DIM || !block_size_ok(block_size)) return DGQ_ERR_UNSUPPORTED;
+    if (T < 0 || num_kv_heads <= 0 || num_blocks <= 0) return DGQ_ERR_INVALID_ARG;
+    // rows in the pools, and 16-byte vectors of the tokens, are counted in 32 bits
+    if ((int64_t)num_blocks * num_kv_heads * block_size >= INT32_MAX || (int64_t)T * num_kv_heads * 16 >= INT32_MAX)
+        return DGQ_ERR_UNSUPPORTED;
+    if (T > 1 && (k_stride < (int64_t)num_kv_heads * DGQ_HEAD_DIM || v_stride < (int64_t)num_kv_heads * DGQ_HEAD_DIM ||
+                  (k_stride & 7) || (v_stride & 7)))
+        return DGQ_ERR_INVALID_ARG;
+    if ((T > 0 && (!k || !v || !slots)) || !k_pool || !v_pool) return DGQ_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(slots) || !aligned16(k_pool) || !aligned16(v_pool))
+        return DGQ_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < 256) return DGQ_ERR_WORKSPACE;
+    return DGQ_OK;
+}
+}  // namespace
+
+dgq_status dgq_write_slots(const void *k_bf16, const void *v_bf16, int64_t k_token_stride, int64_t v_token_stride,
+                           int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim, const int32_t *slots_dev,
+                           void *k_pages_bf16, void *v_pages_bf16, int32_t num_blocks, int32_t block_size,
+                           void *workspace, size_t workspace_bytes, void *cuda_stream)
+{
+    const dgq_status st = rows_checks(k_bf16, v_bf16, k_token_stride, v_token_stride, num_tokens, num_kv_heads, head_dim,
+                                      slots_dev, k_pages_bf16, v_pages_bf16, num_blocks, block_size, workspace,
+                                      workspace_bytes);
+    if (st != DGQ_OK || num_tokens == 0) return st;
+    int nsm = 0;
+    if (device_sm_count(&nsm) != 0) return DGQ_ERR_CUDA;
+    const cudaError_t e = dgq::launch_write_slots(k_bf16, v_bf16, k_token_stride, v_token_stride, num_tokens,
+                                                  num_kv_heads, block_size, slots_dev, k_pages_bf16, v_pages_bf16,
+                                                  num_blocks, workspace, nsm, static_cast<cudaStream_t>(cuda_stream));
+    return e == cudaSuccess ? DGQ_OK : DGQ_ERR_CUDA;
+}
+
+// ---- 8-bit cache with a scale per block and head ------------------------------------------
+
+size_t dgq_block8_workspace_size(void) { return 256; }  // the workspace header alone
+
+dgq_status dgq_store_block8(int32_t format, const void *k_bf16, const void *v_bf16, int64_t k_token_stride,
+                            int64_t v_token_stride, int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                            const int32_t *slots_dev, uint8_t *k_pool, uint8_t *v_pool, float *k_scales,
+                            float *v_scales, int32_t num_blocks, int32_t block_size, void *workspace,
+                            size_t workspace_bytes, void *cuda_stream)
+{
+    if (format != DGQ_BLOCK8_INT8 && format != DGQ_BLOCK8_E4M3) return DGQ_ERR_INVALID_ARG;
+    const dgq_status st = rows_checks(k_bf16, v_bf16, k_token_stride, v_token_stride, num_tokens, num_kv_heads, head_dim,
+                                      slots_dev, k_pool, v_pool, num_blocks, block_size, workspace, workspace_bytes);
+    if (st != DGQ_OK) return st;
+    if (!k_scales || !v_scales || !aligned16(k_scales) || !aligned16(v_scales)) return DGQ_ERR_INVALID_ARG;
+    if (num_tokens == 0) return DGQ_OK;
+    int nsm = 0;
+    if (device_sm_count(&nsm) != 0) return DGQ_ERR_CUDA;
+    const cudaError_t e = dgq::launch_store_block8(
+        format == DGQ_BLOCK8_E4M3, k_bf16, v_bf16, k_token_stride, v_token_stride, num_tokens, num_kv_heads, block_size,
+        slots_dev, k_pool, v_pool, k_scales, v_scales, num_blocks, workspace, nsm, static_cast<cudaStream_t>(cuda_stream));
+    return e == cudaSuccess ? DGQ_OK : DGQ_ERR_CUDA;
+}
+
+dgq_status dgq_load_block8(int32_t format, const uint8_t *k_pool, const uint8_t *v_pool, const float *k_scales,
+                           const float *v_scales, int32_t num_blocks, int32_t block_size,
+                           const int32_t *block_tables_dev, int32_t max_blocks_per_seq, const int32_t *cu_kv_dev,
+                           int32_t batch, int32_t num_kv_heads, int32_t head_dim, void *k_bf16, void *v_bf16,
+                           int32_t total_kv, void *workspace, size_t workspace_bytes, void *cuda_stream)
+{
+    if (format != DGQ_BLOCK8_INT8 && format != DGQ_BLOCK8_E4M3) return DGQ_ERR_INVALID_ARG;
+    if (head_dim != DGQ_HEAD_DIM || !block_size_ok(block_size)) return DGQ_ERR_UNSUPPORTED;
+    if (batch <= 0 || batch > kMaxBatch || num_kv_heads <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || total_kv < 0)
+        return DGQ_ERR_INVALID_ARG;
+    if ((int64_t)num_blocks * num_kv_heads * block_size >= INT32_MAX || (int64_t)total_kv * num_kv_heads >= INT32_MAX)
+        return DGQ_ERR_UNSUPPORTED;
+    if (!k_pool || !v_pool || !k_scales || !v_scales || !block_tables_dev || !cu_kv_dev ||
+        (total_kv > 0 && (!k_bf16 || !v_bf16)))
+        return DGQ_ERR_INVALID_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_scales) || !aligned16(v_scales) ||
+        !aligned16(block_tables_dev) || !aligned16(cu_kv_dev) || !aligned16(k_bf16) || !aligned16(v_bf16))
+        return DGQ_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < dgq_block8_workspace_size()) return DGQ_ERR_WORKSPACE;
+    if (total_kv == 0) return DGQ_OK;
+    int nsm = 0;
+    if (device_sm_count(&nsm) != 0) return DGQ_ERR_CUDA;
+    const cudaError_t e = dgq::launch_load_block8(
+        format == DGQ_BLOCK8_E4M3, k_pool, v_pool, k_scales, v_scales, num_blocks, block_tables_dev, max_blocks_per_seq,
+        cu_kv_dev, batch, num_kv_heads, block_size, k_bf16, v_bf16, total_kv, workspace, nsm,
+        static_cast<cudaStream_t>(cuda_stream));
+    return e == cudaSuccess ? DGQ_OK : DGQ_ERR_CUDA;
 }
 
 // ---- pages ------------------------------------------------------------------------------

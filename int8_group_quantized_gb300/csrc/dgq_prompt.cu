@@ -53,6 +53,12 @@
 //  * What cannot be seen: columns past a row's limit get weight 0; V rows behind a request's end are
 //    zeroed in shared memory, so that values of other requests or of unused slots (NaN too) never
 //    meet a weight.
+//  * With a window (Win; w last tokens, s first ones), a unit's key tiles are those of the sinks and those
+//    from the window of its first row on: step j of the unit is key tile j below `sink`, key tile j + skip
+//    from there on, and everything that counts key tiles (cuts, costs, pieces) counts steps.  The second
+//    tile's rows may see nothing of the first step of the window; their weights are then all 0.  Pages of
+//    a key tile that hold no key that any row of the unit sees are not read (their V rows are zeroed), so
+//    that stale table entries and reused pages never reach a product.
 //  * Every wait is bounded: one that runs out records an error and its role leaves, after which the others'
 //    waits run out too.
 #include "dgq_device.cuh"
@@ -106,6 +112,8 @@ struct PromptArgs {
     float2 *ml;    // per slot and row: maximum and sum
     float *part;   // per slot: O [256][128], unnormalised
     int32_t B, Hq, Hkv, G, lg, total_q, total_kv, bs, max_blocks, num_blocks;
+    int32_t window, sinks;  // Win: the row at position p sees keys t <= p with t > p - window or t < sinks
+    int32_t most;           // Win: keys that a unit's cost counts at most
 };
 
 struct PromptMaps {
@@ -163,25 +171,60 @@ __device__ __forceinline__ int32_t keys_before(const PromptSeq &s, int32_t tok)
 
 __device__ __forceinline__ int32_t key_tiles(int32_t keys) { return (keys + kPmTile - 1) / kPmTile; }
 
-// Cost of a head's first i units (the last one not among them): kPmUnitCost each and the keys of its
-// last token, max(0, off + x U) for unit x = 1 .. i.
-__device__ __forceinline__ int64_t unit_cost(const PromptSeq &s, int32_t U, int32_t i)
+// The key tiles of a unit whose first row sits at position p0: step j is key tile j below `sink` and key
+// tile j + skip from there on.
+struct PromptSpan {
+    int32_t sink, skip;
+};
+
+template <bool Win>
+__device__ __forceinline__ PromptSpan prompt_span(const PromptArgs &a, int32_t p0)
 {
-    const int32_t off = s.m - s.n;
-    const int64_t x0 = off >= 0 ? 0 : min(i, -off >> (__ffs(U) - 1));  // units that see no key
-    const int64_t c = (int64_t)i - x0;
-    return (int64_t)i * kPmUnitCost + c * off + U * (((int64_t)i * (i + 1) - x0 * (x0 + 1)) / 2);
+    if constexpr (!Win) return PromptSpan{0, 0};
+    const int32_t sink = key_tiles(a.sinks);
+    return PromptSpan{sink, max(0, max(0, p0 + 1 - a.window) / kPmTile - sink)};
+}
+
+template <bool Win>
+__device__ __forceinline__ int32_t key_tile_of(const PromptSpan &w, int32_t j)
+{
+    return Win && j >= w.sink ? j + w.skip : j;
+}
+
+// Steps of unit i whose last row (or the last of its first tile) sees `keys` keys, if it had no window.
+template <bool Win>
+__device__ __forceinline__ int32_t unit_steps(const PromptArgs &a, const PromptSeq &s, int32_t U, int32_t i, int32_t keys)
+{
+    return key_tiles(keys) - (Win && keys > 0 ? prompt_span<Win>(a, s.m - s.n + i * U).skip : 0);
+}
+
+// Cost of a head's first i units (the last one not among them): kPmUnitCost each and the keys of its
+// last token, max(0, off + x U) for unit x = 1 .. i; with a window a.most keys at most.
+template <bool Win>
+__device__ __forceinline__ int64_t unit_cost(const PromptArgs &a, const PromptSeq &s, int32_t U, int32_t i)
+{
+    const int32_t off = s.m - s.n, lu = __ffs(U) - 1;
+    const int64_t x0 = off >= 0 ? 0 : min(i, -off >> lu);  // units that see no key
+    int64_t e = i, rest = 0;  // units whose keys all count; the others
+    if constexpr (Win) {
+        e = max(x0, min((int64_t)i, ((int64_t)a.most - off) >> lu));
+        rest = i - e;
+    }
+    const int64_t c = e - x0;
+    return (int64_t)i * kPmUnitCost + c * off + U * ((e * (e + 1) - x0 * (x0 + 1)) / 2) + rest * (Win ? a.most : 0);
 }
 
 // A head's last unit sees all keys; where it has rows in tile 0 only, a key tile costs kPmLoneTile.
 __device__ __forceinline__ bool lone_tile(const PromptSeq &s, int32_t U, int32_t nu) { return s.n - (nu - 1) * U <= U / 2; }
 
 // Cost of a head with nu units.
-__device__ __forceinline__ int64_t head_cost(const PromptSeq &s, int32_t U, int32_t nu)
+template <bool Win>
+__device__ __forceinline__ int64_t head_cost(const PromptArgs &a, const PromptSeq &s, int32_t U, int32_t nu)
 {
     if (nu == 0) return 0;
-    const int64_t last = lone_tile(s, U, nu) ? (uint64_t)s.m * kPmLoneTile / kPmTile : s.m;
-    return unit_cost(s, U, nu - 1) + kPmUnitCost + last;
+    const int32_t keys = Win ? min(s.m, a.most) : s.m;
+    const int64_t last = lone_tile(s, U, nu) ? (uint64_t)keys * kPmLoneTile / kPmTile : keys;
+    return unit_cost<Win>(a, s, U, nu - 1) + kPmUnitCost + last;
 }
 
 __device__ __forceinline__ PromptSeq seq_of_lane(const PromptSeq &s, int l)
@@ -272,6 +315,7 @@ __device__ __forceinline__ int32_t last_where(int32_t n, int lane, F yes)
 }
 
 // The unit and key tile at cost position pos (pre: cost prefix over requests, [B + 1]); the whole warp.
+template <bool Win>
 __device__ PromptPos cut_at(const PromptArgs &a, int32_t U, int32_t R, int64_t pos, const int64_t *pre, int lane)
 {
     PromptPos p = {a.B, 0, 0, 0};
@@ -279,16 +323,16 @@ __device__ PromptPos cut_at(const PromptArgs &a, int32_t U, int32_t R, int64_t p
     p.b = last_where(R, lane, [&](int32_t b) { return pre[b] <= pos; });
     PromptSeq s = prompt_seq(a, p.b, false);  // has units: the next prefix is larger
     const int32_t nu = prompt_units(s, U);
-    const int64_t per_head = head_cost(s, U, nu);
+    const int64_t per_head = head_cost<Win>(a, s, U, nu);
     int64_t r = pos - pre[p.b];
     p.h = (int32_t)__fdividef((float)r, (float)per_head);  // off by one at most below a million heads
     r -= p.h * per_head;
     for (; r < 0; r += per_head) --p.h;
     for (; r >= per_head; r -= per_head) ++p.h;
-    const int32_t lo = last_where(nu, lane, [&](int32_t i) { return unit_cost(s, U, i) <= r; });
+    const int32_t lo = last_where(nu, lane, [&](int32_t i) { return unit_cost<Win>(a, s, U, i) <= r; });
     p.i = lo;
-    r -= unit_cost(s, U, lo) + kPmUnitCost;
-    const int32_t tiles = key_tiles(keys_before(s, (lo + 1) * U));
+    r -= unit_cost<Win>(a, s, U, lo) + kPmUnitCost;
+    const int32_t tiles = unit_steps<Win>(a, s, U, lo, keys_before(s, (lo + 1) * U));
     int32_t j = r > 0 ? (int32_t)r / (lo == nu - 1 && lone_tile(s, U, nu) ? kPmLoneTile : kPmTile) : 0;  // (r <= m < 2^31)
     if (j > tiles - kPmSnap) {
         if (j >= kPmSnap || r > 0) next_unit(a, U, R, lane, p, s);
@@ -518,7 +562,7 @@ struct PromptItem {
     int32_t row;     // row of that token in q and out
     int32_t h;       // KV head
     int32_t slot;    // where its part goes, or -1: a whole unit
-    int32_t pad;
+    int32_t p0;      // Win: position of the unit's first token
 };
 static_assert(sizeof(PromptItem) == 32, "eight words, one per lane");
 constexpr int kPmItems = 4;
@@ -551,21 +595,23 @@ __device__ __forceinline__ bool pm_wait(uint32_t bar, uint32_t parity, WsHeader 
     return false;
 }
 
-// A unit's tiles in the piece [j0, j1): per tile the key tiles to go through, and its keys.
+// A unit's tiles in the piece [j0, j1) of its steps: per tile the key tiles to go through, and its keys.
 struct PromptPiece {
     int32_t j1;        // end of the piece
     int32_t e0, e1;    // key tiles of tile 0, 1 inside the piece (from j0)
     int32_t steps;     // key tiles loaded
 };
 
-__device__ __forceinline__ PromptPiece piece_of(const PromptSeq &s, const PromptPos &p, const PromptPos &end, int32_t U)
+template <bool Win>
+__device__ __forceinline__ PromptPiece piece_of(const PromptArgs &a, const PromptSeq &s, const PromptPos &p,
+                                                const PromptPos &end, int32_t U)
 {
     PromptPiece z;
     const int32_t half = U / 2, tok = p.i * U;
     const int32_t k0 = keys_before(s, tok + half), k1 = keys_before(s, tok + U);
     const bool two = tok + half < s.n;  // tile 1 has rows
-    z.j1 = same_unit(p, end) ? end.j : key_tiles(k1);
-    z.e0 = max(0, min(z.j1, key_tiles(k0)) - p.j);
+    z.j1 = same_unit(p, end) ? end.j : unit_steps<Win>(a, s, U, p.i, k1);
+    z.e0 = max(0, min(z.j1, unit_steps<Win>(a, s, U, p.i, k0)) - p.j);
     z.e1 = two ? max(0, z.j1 - p.j) : 0;
     z.steps = max(z.e0, z.e1);
     return z;
@@ -579,6 +625,7 @@ __device__ __forceinline__ bool before(const PromptPos &x, const PromptPos &end)
     return x.j < end.j;
 }
 
+template <bool Win>
 __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs a, const __grid_constant__ PromptMaps maps)
 {
     extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle repeats every 1024 bytes)
@@ -604,9 +651,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             int64_t c = 0;
             if (b < a.B) {
                 const PromptSeq s = prompt_seq(a, b, blockIdx.x == 0);
-                c = a.Hkv * head_cost(s, U, prompt_units(s, U));
+                c = a.Hkv * head_cost<Win>(a, s, U, prompt_units(s, U));
                 if (s.n > 0) {
-                    longest = max(longest, s.m);
+                    longest = max(longest, Win ? min(s.m, a.most) : s.m);
                     requests = b + 1;
                 }
             }
@@ -668,7 +715,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         } else if (warp < 2) {
             // carry * c / n in steps of 2^-20 (monotone, exact at c = n, no 64-bit division: one took 400 cycles)
             const int64_t f = (uint32_t)((blockIdx.x + warp) << 20) / gridDim.x;
-            const PromptPos c = cut_at(a, U, requests, (carry >> 20) * f + (((carry & 0xfffff) * f) >> 20), pre, lane);
+            const PromptPos c = cut_at<Win>(a, U, requests, (carry >> 20) * f + (((carry & 0xfffff) * f) >> 20), pre, lane);
             if (lane == 0) sb->cut[warp] = c;
         }
         __syncthreads();
@@ -707,6 +754,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         z.row = __shfl_sync(0xffffffffu, w, 4);
         z.h = __shfl_sync(0xffffffffu, w, 5);
         z.slot = __shfl_sync(0xffffffffu, w, 6);
+        if constexpr (Win) z.p0 = __shfl_sync(0xffffffffu, w, 7);
         if (lane == 0) mbar_arrive(&sb->item_empty[i]);
         ++ni;
         return z.e0 >= 0;
@@ -773,7 +821,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         };
         for (bool first = true; ok && more; advance(), first = false) {
             if (queued && lane == 0) ticket = atomicAdd(&a.hdr->tickets, 1u);  // of the next unit
-            const PromptPiece z = piece_of(s, pos, end, U);
+            const PromptPiece z = piece_of<Win>(a, s, pos, end, U);
             const int32_t toks = s.n - pos.i * U, row0 = s.q0 + pos.i * U;
             if (z.steps == 0) {  // rows that see no key
                 for (int32_t x = lane; x < min(U, toks) * G * 16; x += 32) {
@@ -784,16 +832,18 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 continue;
             }
             const bool partial = pos.j > 0 || (same_unit(pos, end) && end.j > 0);
-            if (!hand_out(PromptItem{z.e0, z.e1, s.m - s.n + 1 + pos.i * U - pos.j * kPmTile, toks, row0, pos.h,
-                                     partial ? 2 * (int32_t)blockIdx.x + (first ? 0 : 1) : -1, 0})) {
+            const int32_t p0 = s.m - s.n + pos.i * U;  // position of the unit's first token
+            const PromptSpan span = prompt_span<Win>(a, p0);
+            if (!hand_out(PromptItem{z.e0, z.e1, p0 + 1 - key_tile_of<Win>(span, pos.j) * kPmTile, toks, row0, pos.h,
+                                     partial ? 2 * (int32_t)blockIdx.x + (first ? 0 : 1) : -1, p0})) {
                 ok = false;
                 break;
             }
             // lane l copies half l % 2 of page l / 2 of the key tile
             auto block_of = [&](int32_t j) -> int32_t {
                 int32_t blk = 0;
-                const int32_t t = j * kPmTile + (lane >> 1) * a.bs;
-                if (lane < 2 * pages && t < s.m) {
+                const int32_t t = key_tile_of<Win>(span, j) * kPmTile + (lane >> 1) * a.bs;
+                if (lane < 2 * pages && t < s.m && !(Win && t + a.bs <= p0 + 1 - a.window && t >= a.sinks)) {
                     blk = __ldg(a.bt + (int64_t)pos.b * a.max_blocks + pow2_div(t, a.bs));
                     if ((uint32_t)blk >= (uint32_t)a.num_blocks) {  // not a block of the cache: flagged,
                         record_error(a.hdr, kErrBadBlock);          // and block 0 read instead
@@ -804,10 +854,17 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             };
             int32_t blk = a.bt ? block_of(pos.j) : 0;
             for (int32_t j = pos.j; j < pos.j + z.steps; ++j) {
-                const int32_t valid = min(kPmTile, s.m - j * kPmTile);  // keys of the tile
+                const int32_t tile = key_tile_of<Win>(span, j);
+                const int32_t valid = min(kPmTile, s.m - tile * kPmTile);  // keys of the tile
                 const int32_t blk_next = a.bt && j + 1 < pos.j + z.steps ? block_of(j + 1) : 0;
                 const int32_t used = a.bt ? (valid + a.bs - 1) / a.bs : 0;
-                const uint32_t bytes = a.bt ? (uint32_t)used * a.bs * kD * 2 : (uint32_t)kPmTileBytes;
+                int32_t h0 = 0, h1 = 0;  // Win: rows of the pages that no row of the unit sees
+                if (Win && a.bt) {
+                    const int32_t low = max(0, p0 + 1 - a.window) & -a.bs, k0 = tile * kPmTile;
+                    h0 = min(kPmTile, max(0, ((a.sinks + a.bs - 1) & -a.bs) - k0));
+                    h1 = max(h0, min(kPmTile, low - k0));
+                }
+                const uint32_t bytes = a.bt ? (uint32_t)(used * a.bs - (h1 - h0)) * kD * 2 : (uint32_t)kPmTileBytes;
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t st = it % kPmStages, dst = sring + st * kPmTileBytes;
                     if (it >= kPmStages && !pm_wait(smem_u32(&sb->empty[st]), (it / kPmStages - 1) & 1u, a.hdr)) {
@@ -817,16 +874,26 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                     const CUtensorMap *map = kv ? &maps.v : &maps.k;
                     const bool part = kv == 1 && valid < kPmTile;  // V rows to clear behind the end
                     uint64_t *bar = part ? &sb->v_part : &sb->full[st];
+                    if (Win && kv == 1 && h1 > h0) {  // V rows that are not loaded meet weights 0 and have to be finite
+                        uint8_t *t = smem + 2 * kPmTileBytes + st * kPmTileBytes;
+                        for (int32_t x = h0 * 8 + lane; x < h1 * 8; x += 32) {
+                            *reinterpret_cast<uint4 *>(t + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4 *>(t + kPmHalf + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
                     if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
                     __syncwarp();
                     if (a.bt) {
-                        if (lane < 2 * used) {
+                        const int32_t r = (lane >> 1) * a.bs;
+                        if (lane < 2 * used && !(Win && r >= h0 && r < h1)) {
                             const int32_t row = (blk * a.Hkv + pos.h) * a.bs;
                             tma_tile_2d(dst + (lane & 1) * kPmHalf + (lane >> 1) * a.bs * 128, map, (lane & 1) * 64, row,
                                         bar);
                         }
                     } else if (lane == 0) {
-                        tma_tile_4d(dst, map, 0, s.kv0 + j * kPmTile, pos.h, 0, bar);
+                        tma_tile_4d(dst, map, 0, s.kv0 + tile * kPmTile, pos.h, 0, bar);
                     }
                     v_flight = part;
                     if (part) {
@@ -1011,8 +1078,32 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             // columns from this key tile on that the row sees (a row without a token, whose result nobody
             // takes, sees all: it must not send the warp through the hiding of columns)
             int32_t left = has_row ? z.see + rtok : 1 << 30;
+            // Win: columns in front of the window, and columns of the sinks; steps up to the first that is not
+            // of the sinks' key tiles, and the columns that are passed over there
+            int32_t dark = 0, sunk = 0, jump = -1, over = 0;
+            if constexpr (Win) {
+                const int32_t k0 = z.p0 + 1 - z.see;  // key of the first column
+                const PromptSpan span = prompt_span<Win>(a, z.p0);
+                dark = has_row ? z.p0 + rtok + 1 - a.window - k0 : -(1 << 30);
+                sunk = a.sinks - k0;
+                if (k0 < span.sink * kPmTile) {
+                    jump = span.sink - k0 / kPmTile;
+                    over = span.skip * kPmTile;
+                }
+            }
             float m = -INFINITY, l = 0.0f;
             for (int32_t j = 0; j < e; ++j, left -= kPmTile) {
+                if constexpr (Win) {
+                    if (j > 0) {
+                        dark -= kPmTile;
+                        sunk -= kPmTile;
+                    }
+                    if (j == jump) {
+                        left -= over;
+                        dark -= over;
+                        sunk -= over;
+                    }
+                }
                 if (!pm_wait(smem_u32(&sb->s_full[t]), ns & 1u, a.hdr)) { ok = false; break; }
                 ++ns;
                 tc_fence_after();
@@ -1021,10 +1112,13 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 // below (in tensor memory P overwrites the first 64 columns only)
                 uint32_t x[64], y[32];
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                int32_t high = 0;  // Win: columns that some row of the warp has in front of its window
+                if constexpr (Win) high = __reduce_max_sync(0xffffffffu, dark);
+                auto first = [](int32_t n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
                 auto hide = [&](uint32_t *v, int c0) {  // 32 columns from c0 on, where some row does not see them all
-                    if (low >= c0 + 32) return;
-                    const int32_t n = left - c0;
-                    const uint32_t keep = n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+                    if (low >= c0 + 32 && (!Win || high <= c0 || sunk >= c0 + 32)) return;
+                    uint32_t keep = first(left - c0);
+                    if constexpr (Win) keep &= ~first(dark - c0) | first(sunk - c0);
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
                         if (!(keep & (1u << c))) v[c] = 0xff800000u;  // -inf
@@ -1317,8 +1411,8 @@ size_t prompt_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int nsm)
 
 cudaError_t launch_prompt(const void *q, const void *k, const void *v, int32_t total_q, int32_t total_kv,
                           const int32_t *cu_q, const int32_t *kv, const int32_t *bt, int32_t bs, int32_t max_blocks,
-                          int32_t num_blocks, int32_t B, int32_t Hq, int32_t Hkv, void *out, void *ws, int nsm,
-                          bool *map_failed, cudaStream_t stream)
+                          int32_t num_blocks, int32_t B, int32_t Hq, int32_t Hkv, int32_t window, int32_t sinks,
+                          void *out, void *ws, int nsm, bool *map_failed, cudaStream_t stream)
 {
     *map_failed = true;
     const int32_t G = Hq / Hkv;
@@ -1384,21 +1478,37 @@ cudaError_t launch_prompt(const void *q, const void *k, const void *v, int32_t t
     a.bs = bs;
     a.max_blocks = max_blocks;
     a.num_blocks = num_blocks;
+    const bool win = window > 0;
+    a.window = window;
+    a.sinks = sinks;
+    {   // the sinks' key tiles, the window of the first row, the unit's other rows, and half a tile where the
+        // window begins
+        const int64_t most = ((int64_t)sinks + kPmTile - 1) / kPmTile * kPmTile + window + kPmRows / G + kPmTile / 2;
+        a.most = (int32_t)(most < (1 << 30) ? most : 1 << 30);
+    }
 
-    static thread_local int limit_dev = -1;  // the shared-memory limit is raised once per device and host thread
+    // the shared-memory limit of each instance is raised once per device and host thread
+    static thread_local int limit_devs[2] = {-1, -1};
+    int &limit_dev = limit_devs[win];
+    void (*kern)(const PromptArgs, const PromptMaps) = win ? prompt_kernel<true> : prompt_kernel<false>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev != limit_dev) {
-        e = cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPmSmem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPmSmem);
         if (e != cudaSuccess) return e;
         limit_dev = dev;
     }
-    prompt_kernel<<<(unsigned)nsm, kPmThreads, kPmSmem, stream>>>(a, maps);
+    kern<<<(unsigned)nsm, kPmThreads, kPmSmem, stream>>>(a, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // no request has a unit that may be cut: nothing to merge
-    if ((bt ? (int64_t)max_blocks * bs : (int64_t)total_kv) <= (2 * kPmSnap - 1) * kPmTile) return cudaSuccess;
+    int64_t tiles = ((bt ? (int64_t)max_blocks * bs : (int64_t)total_kv) + kPmTile - 1) / kPmTile;
+    if (win) {  // the sinks' key tiles, and those of the unit's rows and the window in front of them
+        const int64_t seen = ((int64_t)sinks + kPmTile - 1) / kPmTile + (window + kPmRows / G + kPmTile - 3) / kPmTile + 1;
+        if (tiles > seen) tiles = seen;
+    }
+    if (tiles <= 2 * kPmSnap - 1) return cudaSuccess;
 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)nsm, kPmMergeParts);
