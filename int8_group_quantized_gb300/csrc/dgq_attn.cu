@@ -225,13 +225,12 @@ namespace dgq {
 
 size_t attn_smem_bytes(int dec, int32_t B, int32_t G)
 {
-    const int stage = dec == kDecBf16    ? stage_bytes<kDecBf16>()
-                      : dec == kDecFixed ? stage_bytes<kDecFixed>()
-                      : dec == kDecBlockI8 || dec == kDecBlockE4 ? stage_bytes<kDecBlockI8>()
-                                         : stage_bytes<kDecAffine>();
+    const int ring = dec == kDecBf16    ? ring_bytes<kDecBf16>()
+                     : dec == kDecFixed ? ring_bytes<kDecFixed>()
+                     : dec == kDecBlockI8 || dec == kDecBlockE4 ? ring_bytes<kDecBlockI8>()
+                                        : ring_bytes<kDecAffine>();
     const int piece = dec == kDecSplitV ? piece_bytes<kDecSplitV>() : piece_bytes<kDecAffine>();
-    const int depth = dec == kDecBf16 ? ring_depth<kDecBf16>() : kDepth;
-    return 1024 + (size_t)kWarpsPerCta * depth * stage + 2 * (size_t)piece + 16 + (size_t)kWarpsPerCta * G * kPartStride * 4 +
+    return 1024 + (size_t)kWarpsPerCta * ring + 2 * (size_t)piece + 16 + (size_t)kWarpsPerCta * G * kPartStride * 4 +
            8 * 4 + (size_t)(2 * B + 1) * 4;
 }
 

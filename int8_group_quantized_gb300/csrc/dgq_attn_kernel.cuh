@@ -92,13 +92,9 @@ __host__ __device__ constexpr bool is_e4m3() { return Fmt == kDecFp8 || Fmt == k
 template <int Fmt>
 __host__ __device__ constexpr int row_bytes() { return Fmt == kDecBf16 ? 2 * kD : kD; }
 
-// Bytes of one ring stage: the K and V tiles, and for fixed groups their K and V parameters, for block
-// caches their two scales.
+// Bytes of one ring stage: the K and V tiles, and for fixed groups their K and V parameters.
 template <int Fmt>
-__host__ __device__ constexpr int stage_bytes()
-{
-    return 2 * kTile * row_bytes<Fmt>() + (Fmt == kDecFixed ? 2 * kParBytes : (is_block8<Fmt>() ? 16 : 0));
-}
+__host__ __device__ constexpr int stage_bytes() { return 2 * kTile * row_bytes<Fmt>() + (Fmt == kDecFixed ? 2 * kParBytes : 0); }
 
 // CTAs per SM and tiles in flight per warp: a bf16 tile takes twice the shared memory, so its instance
 // runs two CTAs, and at depth 2 (128 KB in flight per SM) measured 2 to 4% faster than at 3 on all
@@ -108,6 +104,10 @@ template <int Fmt>
 __host__ __device__ constexpr int ctas_per_sm() { return Fmt == kDecBf16 ? 2 : kMaxCtasPerSm; }
 template <int Fmt>
 __host__ __device__ constexpr int ring_depth() { return Fmt == kDecBf16 ? 2 : kDepth; }
+// Bytes of a warp's ring: its stages, and for block caches the two scales of each behind them (128 bytes, so
+// that the rows of all warps' stages keep their place in the banks).
+template <int Fmt>
+__host__ __device__ constexpr int ring_bytes() { return ring_depth<Fmt>() * stage_bytes<Fmt>() + (is_block8<Fmt>() ? 128 : 0); }
 constexpr int kPartStride = 132;                   // floats per (piece, head) partial: m, l, pad, pad, O[128]
 constexpr int32_t kMaxGroup = 8;                   // largest query-head group the entry points accept
 constexpr float kLog2eOverSqrtD = 0.12751743074570180f;  // log2(e) / sqrt(128)
@@ -185,9 +185,13 @@ template <int Fmt, bool Hi>
 __device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sc2, uint32_t mn2)
 {
     if constexpr (is_e4m3<Fmt>()) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(Hi ? (w >> 16) : (w & 0xFFFFu)),
-                                                         __NV_E4M3);
-        return (uint32_t)h.x | ((uint32_t)h.y << 16);
+        // (the 16-bit halves named in PTX: the header's function packs and unpacks them around the conversion)
+        uint32_t y;
+        if constexpr (Hi)
+            asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(y) : "r"(w));
+        else
+            asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(w));
+        return y;
     } else {
         const uint32_t x = prmt(w, 0x64646464u, Hi ? 0x4342 : 0x4140);
         if constexpr (Fmt == kDecFixed) {
@@ -221,6 +225,14 @@ __device__ __forceinline__ uint4 ldmatrix_x4_trans(uint32_t addr)
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(addr));
     return v;
+}
+
+// An 8 x 8 matrix of 16-bit values (lane l: row l / 4, columns 2 (l % 4) and the next) transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 // 8-byte shared-memory load by 32-bit shared address (volatile: stays after the copy wait)
@@ -318,11 +330,13 @@ __device__ __forceinline__ TileLoc locate_tile(int32_t x, const int32_t *s_tpre,
     return c;
 }
 
+// The tile n further in the list (which has one).
 template <bool Win>
-__device__ __forceinline__ void advance(TileLoc &c, const int32_t *s_len, const AttnArgs &a)
+__device__ __forceinline__ void advance(TileLoc &c, int32_t n, const int32_t *s_len, const AttnArgs &a)
 {
-    if (++c.j == c.ntl) {
-        c.j = 0;
+    c.j += n;
+    while (c.j >= c.ntl) {
+        c.j -= c.ntl;
         if (++c.h == a.Hkv) {
             c.h = 0;
             ++c.b;
@@ -438,7 +452,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
     constexpr int kTileSmem = 2 * kTileBytes;  // K tile + V tile
     constexpr int kStage = stage_bytes<Fmt>();
     constexpr int kDeep = ring_depth<Fmt>();   // the warp's ring, tiles
-    constexpr int kWarpSmem = kDeep * kStage;
+    constexpr int kWarpSmem = ring_bytes<Fmt>();
     constexpr int kPieceBytes = piece_bytes<Fmt>();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
@@ -589,13 +603,12 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
                 cp_async16(dst + kTileSmem + lane * 16, src);
             }
             if constexpr (is_block8<Fmt>()) {  // the block's scales of K and V
-                if (lane < 2) cp_async4(dst + kTileSmem + lane * 4, (lane ? a.vscale : a.kscale) + (int64_t)blk * Hkv + ic.h);
+                if (lane < 2) cp_async4(ring + kDeep * kStage + st * 8 + lane * 4, (lane ? a.vscale : a.kscale) + (int64_t)blk * Hkv + ic.h);
             }
         }
         cp_async_commit();
         if (kn < nmine) {
-            if (kn + 1 < nmine)
-                for (int i = 0; i < kWarpsPerCta; ++i) advance<Win>(ic, s_len, a);
+            if (kn + 1 < nmine) advance<Win>(ic, kWarpsPerCta, s_len, a);
             ++kn;
         }
     };
@@ -652,6 +665,13 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
             qs += __shfl_xor_sync(0xffffffffu, qs, 2);
             qsum = qs;
         }
+        // block caches: this lane's tokens are tau(r) and 8 + tau(r), its heads 2cq and 2cq + 1
+        float qs[2] = {0.f, 0.f}, mb[2] = {0.f, 0.f}, lb[2] = {0.f, 0.f}, wsum[4] = {0.f, 0.f, 0.f, 0.f};
+        bool fresh = true;
+        if constexpr (is_block8<Fmt>()) {
+            qs[0] = __shfl_sync(0xffffffffu, qsum, 8 * cq);
+            qs[1] = __shfl_sync(0xffffffffu, qsum, 8 * cq + 4);
+        }
         int seg = -1, vseg = -1;
         float ak = 0.f, bk = 0.f, cv = 0.f;
         bool vflat = false;
@@ -668,6 +688,97 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
             const int32_t tok0 = j * kTile;
             const int32_t valid = min(kTile, cur.L - tok0);
             if (valid > 0) {
+                if constexpr (is_block8<Fmt>()) {
+                    // S = K Q^T: the tile's 16 tokens are the rows (row r: token tau(r), row 8 + r: 8 + tau(r)),
+                    // so that one instruction takes all of them
+                    const uint32_t tile = ring + st * kStage;
+                    const uint2 sc = ld_shared_v2(ring + kDeep * kStage + st * 8);
+                    const uint32_t kr0 = tile + tr * kRow, kr1 = tile + (8 + tr) * kRow;
+                    const uint4 k0 = ld_shared_v4(kr0 + ((cq ^ tr) << 4)), k1 = ld_shared_v4(kr0 + (((cq + 4) ^ tr) << 4));
+                    const uint4 k2 = ld_shared_v4(kr1 + ((cq ^ tr) << 4)), k3 = ld_shared_v4(kr1 + (((cq + 4) ^ tr) << 4));
+                    const uint32_t vt = tile + kTileBytes;  // rows cq + 4i, column tau(r)
+                    uint4 va = ld_shared_v4(vt + cq * kD + ((tr ^ cq) << 4));
+                    uint4 vb = ld_shared_v4(vt + (cq + 4) * kD + ((tr ^ (cq + 4)) << 4));
+                    uint4 vc = ld_shared_v4(vt + (cq + 8) * kD + ((tr ^ cq) << 4));
+                    uint4 vd = ld_shared_v4(vt + (cq + 12) * kD + ((tr ^ (cq + 4)) << 4));
+                    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int jj = 0; jj < 8; ++jj) {
+                        const uint32_t wa = word(jj < 4 ? k0 : k1, jj & 3), wb = word(jj < 4 ? k2 : k3, jj & 3);
+                        mma16816(jj & 1 ? s1 : s0, codes2<Fmt, false>(wa, 0u, 0u), codes2<Fmt, false>(wb, 0u, 0u),
+                                 codes2<Fmt, true>(wa, 0u, 0u), codes2<Fmt, true>(wb, 0u, 0u), qa0[jj], qa2[jj]);
+                    }
+                    const float ve = lg2(fmaxf(__uint_as_float(sc.y), 0x1p-100f));  // (a block of zeros has scale 0)
+                    const float ks = __uint_as_float(sc.x) * kLog2eOverSqrtD;
+                    float z[4];  // z + log2(scale of V) - m of (token, head): (0, 0) (0, 1) (1, 0) (1, 1)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        // INT8 codes came in as 1152 + q (1024 of the fp16 form, 128 of the code)
+                        const float c = (Fmt == kDecBlockI8 ? fmaf(-1152.0f * ks, qs[g], ve) : ve) - mb[g];
+                        z[g] = fmaf(ks, s0[g] + s1[g], c);
+                        z[2 + g] = fmaf(ks, s0[2 + g] + s1[2 + g], c);
+                    }
+                    const int32_t lo = Win ? cur.L - a.window + 1 - tok0 : 0, sk = Win ? a.sinks - tok0 : 0;
+                    if (valid < kTile || (Win && lo > 0 && sk < kTile)) {  // tokens behind the end, or not in sight
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int32_t t = tr + 8 * e;
+                            if (t >= valid || (Win && t < lo && t >= sk)) z[2 * e] = z[2 * e + 1] = -INFINITY;
+                        }
+                    }
+                    const float top0 = fmaxf(z[0], z[2]), top1 = fmaxf(z[1], z[3]);
+                    if (__any_sync(0xffffffffu, fresh || fmaxf(top0, top1) > kLazyRescale)) {
+                        float up[2] = {top0, top1};
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) {
+                            up[0] = fmaxf(up[0], __shfl_xor_sync(0xffffffffu, up[0], off));
+                            up[1] = fmaxf(up[1], __shfl_xor_sync(0xffffffffu, up[1], off));
+                        }
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            if (!fresh && !(up[g] > kLazyRescale)) continue;
+                            const float alpha = fresh ? 0.0f : ex2(-up[g]);
+                            mb[g] += up[g];
+                            lb[g] *= alpha;
+                            z[g] -= up[g];
+                            z[2 + g] -= up[g];
+                            wsum[g] *= alpha;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                o[i][g] *= alpha;
+                                o[i][2 + g] *= alpha;
+                            }
+                        }
+                        fresh = false;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[e] = ex2(z[e]);
+                    const float unit = ex2(-ve);  // w 2^-log2(scale) of the weights before their rounding
+                    lb[0] = fmaf(z[0] + z[2], unit, lb[0]);
+                    lb[1] = fmaf(z[1] + z[3], unit, lb[1]);
+                    // the weights as the tensor cores take them: tokens cq, cq + 4 (pb0) and 8 + cq, 12 + cq of head r
+                    const uint32_t pb0 = transpose8(f32x2_to_f16x2(z[0], z[1])), pb1 = transpose8(f32x2_to_f16x2(z[2], z[3]));
+                    // the sum of the rounded weights, against which INT8's 1152 is taken off again
+                    if constexpr (Fmt == kDecBlockI8) mma16816(wsum, 0x3C003C00u, 0u, 0x3C003C00u, 0u, pb0, pb1);
+                    if (Fmt == kDecBlockE4 && valid < kTile) {  // slots past the end hold any byte, NaN codes too
+                        const uint4 z4 = make_uint4(0u, 0u, 0u, 0u);
+                        if (cq >= valid) va = z4;
+                        if (cq + 4 >= valid) vb = z4;
+                        if (cq + 8 >= valid) vc = z4;
+                        if (cq + 12 >= valid) vd = z4;
+                    }
+#pragma unroll
+                    for (int wi = 0; wi < 4; ++wi) {
+                        const uint32_t xab01 = prmt(word(va, wi), word(vb, wi), 0x5140);
+                        const uint32_t xab23 = prmt(word(va, wi), word(vb, wi), 0x7362);
+                        const uint32_t xcd01 = prmt(word(vc, wi), word(vd, wi), 0x5140);
+                        const uint32_t xcd23 = prmt(word(vc, wi), word(vd, wi), 0x7362);
+                        mma16816(o[2 * wi], codes2<Fmt, false>(xab01, 0u, 0u), codes2<Fmt, true>(xab01, 0u, 0u),
+                                 codes2<Fmt, false>(xcd01, 0u, 0u), codes2<Fmt, true>(xcd01, 0u, 0u), pb0, pb1);
+                        mma16816(o[2 * wi + 1], codes2<Fmt, false>(xab23, 0u, 0u), codes2<Fmt, true>(xab23, 0u, 0u),
+                                 codes2<Fmt, false>(xcd23, 0u, 0u), codes2<Fmt, true>(xcd23, 0u, 0u), pb0, pb1);
+                    }
+                } else {
                 // segment constants (record words: start 2..6, k_min 7.., k_scale 12.., v_min 17.., v_scale 22..)
                 // (independent V segmentation: K's segment sgk from `recw`, V's sgv from `recw_v`)
                 int sgk = 0, sgv = 0, sg = 0;
@@ -685,7 +796,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
                     ak = kLog2eOverSqrtD;
                     bk = 0.0f;
                     cv = 0.0f;
-                } else if (!is_block8<Fmt>() && sg != seg) {
+                } else if (sg != seg) {
                     seg = sg;
                     const uint32_t vw = Fmt == kDecSplitV ? recw_v : recw;
                     const float kmin = __uint_as_float(__shfl_sync(0xffffffffu, recw, 7 + sgk));
@@ -711,16 +822,6 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
                 }
 
                 const uint32_t tile = ring + st * kStage;
-                float ve = 0.0f, vunit = 1.0f;  // block caches: log2 of V's scale, and 2^-that
-                if constexpr (is_block8<Fmt>()) {
-                    const uint2 sc = ld_shared_v2(tile + kTileSmem);
-                    const float ks = __uint_as_float(sc.x);
-                    ve = lg2(fmaxf(__uint_as_float(sc.y), 0x1p-100f));  // (a block of zeros has scale 0)
-                    vunit = ex2(-ve);
-                    ak = ks * kLog2eOverSqrtD;
-                    bk = Fmt == kDecBlockI8 ? -1152.0f * qsum * ak : 0.0f;  // 1024 of the fp16 form, 128 of the code
-                    cv = Fmt == kDecBlockI8 ? -1152.0f : 0.0f;
-                }
                 // fixed groups: this lane's K rows tau(r), 8 + tau(r) (columns cq < 4: values 0-63;
                 // cq + 4: 64-127) and V rows cq, cq + 4, cq + 8, cq + 12 (column tau(r): half tau(r) / 4)
                 uint32_t ksc[2][2] = {{0u, 0u}, {0u, 0u}}, kmn[2][2] = {{0u, 0u}, {0u, 0u}};
@@ -792,10 +893,6 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
                 z[1] = (cq + 4 < valid) ? fmaf(ak, sa[0][1] + sb[0][1], bk) : -INFINITY;
                 z[2] = (cq + 8 < valid) ? fmaf(ak, sa[1][0] + sb[1][0], bk) : -INFINITY;
                 z[3] = (cq + 12 < valid) ? fmaf(ak, sa[1][1] + sb[1][1], bk) : -INFINITY;
-                if constexpr (is_block8<Fmt>()) {  // (the maximum and the weights are of z + log2 of V's scale)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) z[e] += ve;
-                }
                 if constexpr (Win) {  // tokens between the sinks and the window
                     const int32_t lo = cur.L - a.window + 1 - tok0, sk = a.sinks - tok0;
 #pragma unroll
@@ -842,8 +939,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
                     pb1 = f32x2_to_f16x2(pr[2], pr[3]);
                     psum = (f16lo(pb0) + f16hi(pb0)) + (f16lo(pb1) + f16hi(pb1));
                 }
-                // (block caches: w 2^-log2(scale) of the weights before their rounding)
-                l_run += is_block8<Fmt>() ? ((pr[0] + pr[1]) + (pr[2] + pr[3])) * vunit : psum;
+                l_run += psum;
                 bsum = fmaf(cv, psum, bsum);
 
                 // O^T += V^T P^T: rows (d) 16*tr + 2i (+1), k = tokens cq, cq+4, 8+cq, 12+cq
@@ -873,7 +969,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
                     uint4 vb = ld_shared_v4(vt + (cq + 4) * kD + ((tr ^ (cq + 4)) << 4));
                     uint4 vc = ld_shared_v4(vt + (cq + 8) * kD + ((tr ^ cq) << 4));
                     uint4 vd = ld_shared_v4(vt + (cq + 12) * kD + ((tr ^ (cq + 4)) << 4));
-                    if constexpr (is_e4m3<Fmt>()) {
+                    if constexpr (Fmt == kDecFp8) {
                         // slots past the end hold any byte, E4M3 NaN patterns too (0 * NaN would
                         // reach the sums): their codes become +0
                         if (valid < kTile) {
@@ -898,6 +994,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
                                  codes2<Fmt, true>(xcd23, vsc_cd, vmn_cd), pb0, pb1);
                     }
                 }
+                }
             }
             issue(st);  // refill this stage kDeep tiles ahead (its reads above are complete)
         }
@@ -910,12 +1007,28 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
             bs_ += __shfl_xor_sync(0xffffffffu, bs_, 1);
             bs_ += __shfl_xor_sync(0xffffffffu, bs_, 2);
             float *cw = s_comb + warp * G * kPartStride;
-            if (gvalid && cq == 0) {
-                cw[r * kPartStride + 0] = m_run;
-                cw[r * kPartStride + 1] = l;
-            }
             const int g0 = 2 * cq, g1 = 2 * cq + 1;
-            const float b0 = __shfl_sync(0xffffffffu, bs_, 8 * cq), b1 = __shfl_sync(0xffffffffu, bs_, 8 * cq + 4);
+            float b0, b1;
+            if constexpr (is_block8<Fmt>()) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) lb[g] += __shfl_xor_sync(0xffffffffu, lb[g], off);
+                    if (r == 0 && g0 + g < G) {
+                        cw[(g0 + g) * kPartStride + 0] = fresh ? -INFINITY : mb[g];
+                        cw[(g0 + g) * kPartStride + 1] = lb[g];
+                    }
+                }
+                b0 = Fmt == kDecBlockI8 ? -1152.0f * __shfl_sync(0xffffffffu, wsum[0], cq) : 0.0f;
+                b1 = Fmt == kDecBlockI8 ? -1152.0f * __shfl_sync(0xffffffffu, wsum[1], cq) : 0.0f;
+            } else {
+                if (gvalid && cq == 0) {
+                    cw[r * kPartStride + 0] = m_run;
+                    cw[r * kPartStride + 1] = l;
+                }
+                b0 = __shfl_sync(0xffffffffu, bs_, 8 * cq);
+                b1 = __shfl_sync(0xffffffffu, bs_, 8 * cq + 4);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if constexpr (Fmt == kDecBf16) {  // rows d = 16i + r, 16i + 8 + r; heads g0, g1
