@@ -95,6 +95,9 @@ constexpr int kPmSnap = 2;
 // CTA) take as long as in slices, 124 us with launch; at two, 2 prompts of 2048 do, 77 us.
 constexpr int kPmQueued = 3;
 constexpr int kPmRows = 2 * kPmTile;              // packed rows of a unit
+// Sinks up to this many take a step of 32 keys in place of 128 (two of eight products with P, a quarter of the
+// scores).
+constexpr int kPmNarrow = 32;
 // A wait ends after this many polls.  One that finds its barrier open took 7776 cycles (4 us), which makes a
 // second of them; how long a poll suspends is up to the hardware, so the time is not a promise.
 constexpr uint32_t kPmWaitPolls = 1u << 18;
@@ -401,7 +404,9 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r)
 
 // D (fp32, 128 x 128) (+)= A B, 16 deep, bf16 operands; B n-by-k (K-major) in shared memory.
 constexpr uint32_t kIdescQK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-// the same with B k-by-n as it lies (MN-major: bit 16)
+// the same for 32 keys
+constexpr uint32_t kIdescQK32 = (1u << 4) | (1u << 7) | (1u << 10) | ((32u >> 3) << 17) | ((128u >> 4) << 24);
+// the same (128) with B k-by-n as it lies (MN-major: bit 16)
 constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
 
 // Shared-memory operand descriptors of a pair of [128][64] halves under the 128-byte swizzle: address
@@ -595,6 +600,27 @@ __device__ __forceinline__ bool pm_wait(uint32_t bar, uint32_t parity, WsHeader 
     return false;
 }
 
+// What a window lets a piece pass over; the piece's first key tile is k0.
+struct PromptSkips {
+    int32_t step;  // the first step behind the sinks' key tiles (-1: in front of the piece)
+    int32_t over;  // keys passed over in front of it
+    bool hole;     // no row of tile 1 sees that step (tiles are 128 rows: one step at most)
+    bool narrow;   // the piece's first key tile is seen for the sinks alone, and they are few
+};
+
+template <bool Win>
+__device__ __forceinline__ PromptSkips prompt_skips(const PromptArgs &a, int32_t U, int32_t p0, int32_t k0)
+{
+    const PromptSpan w0 = prompt_span<Win>(a, p0), w1 = prompt_span<Win>(a, p0 + U / 2);
+    const int32_t j0 = k0 < w0.sink ? k0 : k0 - w0.skip;  // the piece's first step in the unit
+    PromptSkips z;
+    z.step = j0 <= w0.sink ? w0.sink - j0 : -1;
+    z.over = j0 < w0.sink ? w0.skip * kPmTile : 0;
+    z.hole = w1.skip > w0.skip;
+    z.narrow = j0 == 0 && w0.skip > 0 && a.sinks > 0 && a.sinks <= kPmNarrow;
+    return z;
+}
+
 // A unit's tiles in the piece [j0, j1) of its steps: per tile the key tiles to go through, and its keys.
 struct PromptPiece {
     int32_t j1;        // end of the piece
@@ -613,6 +639,11 @@ __device__ __forceinline__ PromptPiece piece_of(const PromptArgs &a, const Promp
     z.j1 = same_unit(p, end) ? end.j : unit_steps<Win>(a, s, U, p.i, k1);
     z.e0 = max(0, min(z.j1, unit_steps<Win>(a, s, U, p.i, k0)) - p.j);
     z.e1 = two ? max(0, z.j1 - p.j) : 0;
+    if constexpr (Win) {  // a cut right behind the step that tile 1 passes over
+        const int32_t p0 = s.m - s.n + tok;
+        const PromptSkips x = prompt_skips<Win>(a, U, p0, key_tile_of<Win>(prompt_span<Win>(a, p0), p.j));
+        if (x.hole && z.e1 > 0 && x.step == z.e1 - 1) --z.e1;
+    }
     z.steps = max(z.e0, z.e1);
     return z;
 }
@@ -953,6 +984,15 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
         auto wrap = [](uint32_t x) { return x >= kPmStages ? x - kPmStages : x; };
         for (PromptItem z; ok && next_item(z);) {
             const int32_t steps = max(z.e0, z.e1);
+            int32_t hole = -1;  // Win: the step that tile 1 passes over
+            uint32_t idesc = kIdescQK;
+            bool few = false;
+            if constexpr (Win) {
+                const PromptSkips x = prompt_skips<Win>(a, U, z.p0, (z.p0 + 1 - z.see) / kPmTile);
+                hole = x.hole ? x.step : -1;
+                few = x.narrow;
+                idesc = __shfl_sync(0xffffffffu, few ? kIdescQK32 : kIdescQK, 0);
+            }
             // S of the first key tile
             if (!wait(full0 + 8 * st, ph)) break;
             uint32_t kb = __shfl_sync(0xffffffffu, k_desc + st * (kPmTileBytes >> 4), 0);
@@ -961,11 +1001,12 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 if ((t ? z.e1 : z.e0) == 0) continue;
                 if (!wait(smem_u32(&sb->q_full[t]), (qpar >> t) & 1u)) { ok = false; break; }
                 qpar ^= 1u << t;
+                if (Win && t == 1 && hole == 0) continue;
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         tc_mma_ss(base + kPmColS + t * 128, q_desc + t * (kPmTileBytes >> 4) + kstep(k), kb + kstep(k),
-                                  kIdescQK, k > 0);
+                                  idesc, k > 0);
                     tc_commit(smem_u32(&sb->s_full[t]));
                 }
                 __syncwarp();
@@ -985,17 +1026,20 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             for (int32_t j = 0; j < steps; ++j) {
                 const bool more = j + 1 < steps;
                 if (!(got & 1u) && (!wait(full0 + 8 * sv, hv) || (more && !wait(full0 + 8 * sk, hk)))) { ok = false; break; }
-                const uint32_t acc = __shfl_sync(0xffffffffu, j > 0 ? 1u : 0u, 0);
                 uint32_t vn = 0, kn = 0;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const int32_t e = t ? z.e1 : z.e0;
                     if (j >= e) continue;
                     const uint32_t pbar = smem_u32(&sb->p_ready[t]), par = (ppar >> t) & 1u;
+                    const bool pass = Win && t == 1 && j == hole;  // no row of the tile sees this step
+                    const bool narrow = Win && few && j == 0;
+                    const uint32_t acc = __shfl_sync(0xffffffffu, j > (Win && t == 1 && hole == 0 ? 1 : 0) ? 1u : 0u, 0);
+                    uint32_t g = 0;
+                    if (!pass) {
                     if (!(got & (2u << t)) && !wait(smem_u32(&sb->p_most[t]), par)) { ok = false; break; }
                     tc_fence_after();
-                    uint32_t g = 0;
-                    if (elect_one()) {
+                    if (!narrow && elect_one()) {
                         // keys 96 .. 127 and 0 .. 63, then 64 .. 95, as the softmax stores them
 #pragma unroll
                         for (int i = 0; i < 6; ++i) {
@@ -1007,19 +1051,30 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                     }
                     if (!__any_sync(0xffffffffu, g) && !wait(pbar, par)) { ok = false; break; }
                     tc_fence_after();
+                    ppar ^= 1u << t;
+                    }
                     g = 0;
                     if (elect_one()) {
+                        if (narrow) {  // keys 0 .. 31 are all there is
 #pragma unroll
-                        for (int k = 4; k < 6; ++k)
-                            tc_mma_ts(base + kPmColO + t * 128, base + kPmColS + t * 128 + k * 8, vb + k * (2048 >> 4),
-                                      kIdescPV, 1u);
+                            for (int k = 0; k < 2; ++k)
+                                tc_mma_ts(base + kPmColO + t * 128, base + kPmColS + t * 128 + k * 8, vb + k * (2048 >> 4),
+                                          kIdescPV, k > 0 ? 1u : acc);
+                        } else if (!pass) {
+#pragma unroll
+                            for (int k = 4; k < 6; ++k)
+                                tc_mma_ts(base + kPmColO + t * 128, base + kPmColS + t * 128 + k * 8, vb + k * (2048 >> 4),
+                                          kIdescPV, 1u);
+                        }
                         const bool last = t == 1 || j >= z.e1;  // the step's last turn
                         if (last) {
                             vn = wrap(sv + 2);
                             kn = wrap(sk + 2);
                             g = bar_test(full0 + 8 * vn, hv ^ (vn < sv)) & (j + 2 < steps ? bar_test(full0 + 8 * kn, hk ^ (kn < sk)) : 1u);
                         }
-                        if (j + 1 < e) {
+                        if (Win && t == 1 && j + 1 == hole && j + 1 < e) {
+                            // S of the step behind it comes with that step's turn
+                        } else if (j + 1 < e) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
                                 tc_mma_ss(base + kPmColS + t * 128, q_desc + t * (kPmTileBytes >> 4) + kstep(k), kb + kstep(k),
@@ -1038,7 +1093,6 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                             kn = k_desc + kn * (kPmTileBytes >> 4);
                         }
                     }
-                    ppar ^= 1u << t;
                     got = __reduce_or_sync(0xffffffffu, g);
                 }
                 if (!ok) break;
@@ -1078,30 +1132,63 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
             // columns from this key tile on that the row sees (a row without a token, whose result nobody
             // takes, sees all: it must not send the warp through the hiding of columns)
             int32_t left = has_row ? z.see + rtok : 1 << 30;
-            // Win: columns in front of the window, and columns of the sinks; steps up to the first that is not
-            // of the sinks' key tiles, and the columns that are passed over there
-            int32_t dark = 0, sunk = 0, jump = -1, over = 0;
+            float m = -INFINITY, l = 0.0f;
+            int32_t j = 0;
+            // Win: columns in front of the window, and columns of the sinks; the first step behind the sinks' key
+            // tiles, and the columns passed over there (bit 0: this tile's rows do not see that step)
+            int32_t dark = 0, sunk = 0, step = -1, over = 0;
             if constexpr (Win) {
                 const int32_t k0 = z.p0 + 1 - z.see;  // key of the first column
-                const PromptSpan span = prompt_span<Win>(a, z.p0);
-                dark = has_row ? z.p0 + rtok + 1 - a.window - k0 : -(1 << 30);
+                dark = has_row ? left - a.window : -(1 << 30);
                 sunk = a.sinks - k0;
-                if (k0 < span.sink * kPmTile) {
-                    jump = span.sink - k0 / kPmTile;
-                    over = span.skip * kPmTile;
+                const PromptSkips w = prompt_skips<Win>(a, U, z.p0, k0 / kPmTile);
+                step = w.step;
+                over = w.over | (t == 1 && w.hole ? 1 : 0);  // (columns: a multiple of 128)
+                if (w.narrow && e > 0) {  // a step of the sinks alone, at most 32 columns, all in sight
+                    if (!pm_wait(smem_u32(&sb->s_full[t]), ns & 1u, a.hdr)) break;
+                    ++ns;
+                    tc_fence_after();
+                    uint32_t x[32];
+                    tc_ld32(ts, x);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < kPmNarrow; ++c) {
+                        if (c >= a.sinks) x[c] = 0xff800000u;
+                        m = fmaxf(m, __uint_as_float(x[c]));
+                    }
+                    const float sc = fabsf(m) < kPmFar ? kPmScale : 0.125f, ref = -m * sc;
+                    uint32_t p[16];
+#pragma unroll
+                    for (int c = 0; c < kPmNarrow; c += 2) {
+                        const float lo = pm_ex2(fmaf(__uint_as_float(x[c]), sc, ref)), hi = pm_ex2(fmaf(__uint_as_float(x[c + 1]), sc, ref));
+                        l += lo + hi;
+                        p[c >> 1] = pm_pack_bf16(lo, hi);
+                    }
+                    tc_st16(ts, p);
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sb->p_most[t]);
+                        mbar_arrive(&sb->p_ready[t]);
+                    }
+                    j = 1;
+                    left -= kPmTile;
+                    dark -= kPmTile;
+                    sunk -= kPmTile;
                 }
             }
-            float m = -INFINITY, l = 0.0f;
-            for (int32_t j = 0; j < e; ++j, left -= kPmTile) {
+            for (; j < e; ++j, left -= kPmTile) {
                 if constexpr (Win) {
-                    if (j > 0) {
-                        dark -= kPmTile;
-                        sunk -= kPmTile;
-                    }
-                    if (j == jump) {
-                        left -= over;
-                        dark -= over;
-                        sunk -= over;
+                    if (j == step) {
+                        left -= over & ~1;
+                        dark -= over & ~1;
+                        sunk -= over & ~1;
+                        if (over & 1) {
+                            dark -= kPmTile;
+                            sunk -= kPmTile;
+                            continue;
+                        }
                     }
                 }
                 if (!pm_wait(smem_u32(&sb->s_full[t]), ns & 1u, a.hdr)) { ok = false; break; }
@@ -1206,6 +1293,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) prompt_kernel(const PromptArgs 
                 float lo, hi;
                 unpack2(add2(sum[0], sum[1]), lo, hi);
                 l += lo + hi;
+                if constexpr (Win) {
+                    dark -= kPmTile;
+                    sunk -= kPmTile;
+                }
             }
             if (!ok) break;
             // ---- the piece's end: the rows, or their part for the merge.  A thread has a row, so the warp
