@@ -119,11 +119,11 @@ __device__ __forceinline__ float b8_amax(const uint4 *x)
 }
 
 template <bool E4>
-__global__ void __launch_bounds__(kB8Threads, 4) store_block8_kernel(const Block8Args a)
+__global__ void __launch_bounds__(kB8Threads, 7) store_block8_kernel(const Block8Args a)
 {
     __shared__ int32_t s_start[kB8Window];            // tokens of the window that start a run
     __shared__ int32_t s_count[kB8Warps];
-    __shared__ float s_max[2][2][kB8Warps];
+    __shared__ float s_max[2][kB8Warps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t bs = a.bs, shift = __ffs(bs) - 1;
     const int32_t w0 = blockIdx.x * a.window;
@@ -150,18 +150,21 @@ __global__ void __launch_bounds__(kB8Threads, 4) store_block8_kernel(const Block
 #pragma unroll
     for (int w = 0; w < kB8Warps; ++w) runs += s_count[w];
 
-    const int per = bs / kB8Rows;                     // warps of a run: 1, 2 or 4
+    const int per = bs / kB8Rows;                     // warps of an item: 1, 2 or 4
     const int group = warp / per, part = warp % per, groups = kB8Warps / per;
-    const int32_t items = runs * a.Hkv;
+    const int32_t items = runs * 2 * a.Hkv;           // (run, K or V, head)
     const int32_t y0 = blockIdx.y * groups, step = gridDim.y * groups;
     int flip = 0;
     for (int32_t base = y0; base < items; base += step, flip ^= 1) {  // (the same turns for all warps: barriers inside)
         const int32_t item = base + group;
         const bool live = item < items;
         int32_t t0 = 0, h = 0, blk = 0, r0 = 0, n = 0;
+        bool is_v = false;
         if (live) {
-            t0 = s_start[item / a.Hkv];
-            h = item % a.Hkv;
+            const int32_t q = item / a.Hkv;
+            h = item - q * a.Hkv;
+            is_v = q & 1;
+            t0 = s_start[q >> 1];
             const int32_t slot = __ldg(a.slots + t0);
             blk = slot >> shift;
             r0 = slot & (bs - 1);
@@ -174,71 +177,55 @@ __global__ void __launch_bounds__(kB8Threads, 4) store_block8_kernel(const Block
         }
         // this lane: rows 2i + lane / 16 of the warp's 16, 16-byte vector lane % 16
         const int32_t row0 = part * kB8Rows + (lane >> 4), vec = lane & 15;
-        uint4 x[2][kB8Vecs];
-        const uint4 *kr = a.k + (int64_t)(t0 - r0 + row0) * a.k_stride + h * 16 + vec;
-        const uint4 *vr = a.v + (int64_t)(t0 - r0 + row0) * a.v_stride + h * 16 + vec;
+        const int64_t stride = is_v ? a.v_stride : a.k_stride;
+        const uint4 *from = (is_v ? a.v : a.k) + (int64_t)(t0 - r0 + row0) * stride + h * 16 + vec;
+        float *scale = (is_v ? a.vscale : a.kscale) + (int64_t)blk * a.Hkv + h;
+        uint4 x[kB8Vecs];
 #pragma unroll
         for (int i = 0; i < kB8Vecs; ++i) {
             const int32_t r = row0 + 2 * i - r0;
-            const bool mine = r >= 0 && r < n;
-            x[0][i] = mine ? __ldcs(kr + 2 * i * a.k_stride) : make_uint4(0u, 0u, 0u, 0u);
-            x[1][i] = mine ? __ldcs(vr + 2 * i * a.v_stride) : make_uint4(0u, 0u, 0u, 0u);
+            x[i] = r >= 0 && r < n ? __ldcs(from + 2 * i * stride) : make_uint4(0u, 0u, 0u, 0u);
         }
-        const int64_t sc = (int64_t)blk * a.Hkv + h;
-        float had[2] = {0.0f, 0.0f};
-        if (live && r0 > 0) {  // tokens are there already
-            had[0] = __ldcg(a.kscale + sc);
-            had[1] = __ldcg(a.vscale + sc);
-        }
-        float amax[2] = {b8_amax(x[0]), b8_amax(x[1])};
-        if (per > 1) {  // the warps of the run
-            if (lane == 0) {
-                s_max[flip][0][warp] = amax[0];
-                s_max[flip][1][warp] = amax[1];
-            }
-            __syncthreads();  // (also: every warp has read the scales)
-            for (int w = group * per; w < (group + 1) * per; ++w) {
-                amax[0] = fmaxf(amax[0], s_max[flip][0][w]);
-                amax[1] = fmaxf(amax[1], s_max[flip][1][w]);
-            }
+        const float had = live && r0 > 0 ? __ldcg(scale) : 0.0f;  // tokens are there already
+        float amax = b8_amax(x);
+        if (per > 1) {  // the warps of the item
+            if (lane == 0) s_max[flip][warp] = amax;
+            __syncthreads();  // (also: every warp has read the scale)
+            for (int w = group * per; w < (group + 1) * per; ++w) amax = fmaxf(amax, s_max[flip][w]);
         }
         if (!live) continue;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            const float s = fmaxf(had[kv], b8_scale<E4>(amax[kv]));
-            const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
-            uint2 *pool = reinterpret_cast<uint2 *>(kv ? a.vpool : a.kpool) + ((sc * bs) + row0) * 16 + vec;
-            if (part == 0 && lane == 0 && (r0 == 0 || s != had[kv])) (kv ? a.vscale : a.kscale)[sc] = s;
-            if (r0 > 0 && s > had[kv]) {  // the codes of the tokens in front, anew
-                for (int i = 0; i < kB8Vecs; ++i) {
-                    if (row0 + 2 * i >= r0) break;
-                    uint2 c = pool[2 * i * 16];
-                    const float4 p = b8_decode4<E4>(c.x), q = b8_decode4<E4>(c.y);
-                    // code times scale is exact (15 bits); the quotient is rounded once, and is a tie exactly
-                    // or 2^-16 away from one at least, which fp32 tells apart
-                    auto again = [&](float u) { return __fdiv_rn(u * had[kv], s); };
-                    const float one = 1.0f;
-                    if constexpr (E4) {
-                        c.x = __nv_cvt_float2_to_fp8x2(make_float2(again(p.x), again(p.y)), __NV_SATFINITE, __NV_E4M3) |
-                              ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(again(p.z), again(p.w)), __NV_SATFINITE, __NV_E4M3) << 16);
-                        c.y = __nv_cvt_float2_to_fp8x2(make_float2(again(q.x), again(q.y)), __NV_SATFINITE, __NV_E4M3) |
-                              ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(again(q.z), again(q.w)), __NV_SATFINITE, __NV_E4M3) << 16);
-                    } else {
-                        c.x = b8_encode4<E4>(rintf(again(p.x)), rintf(again(p.y)), rintf(again(p.z)), rintf(again(p.w)), one);
-                        c.y = b8_encode4<E4>(rintf(again(q.x)), rintf(again(q.y)), rintf(again(q.z)), rintf(again(q.w)), one);
-                    }
-                    pool[2 * i * 16] = c;
-                }
-            }
-#pragma unroll
+        const float s = fmaxf(had, b8_scale<E4>(amax));
+        const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+        uint2 *pool = reinterpret_cast<uint2 *>(is_v ? a.vpool : a.kpool) + (((int64_t)blk * a.Hkv + h) * bs + row0) * 16 + vec;
+        if (part == 0 && lane == 0 && (r0 == 0 || s != had)) *scale = s;
+        if (r0 > 0 && s > had) {  // the codes of the tokens in front, anew
             for (int i = 0; i < kB8Vecs; ++i) {
-                const int32_t r = row0 + 2 * i - r0;
-                const uint4 w = x[kv][i];
-                uint2 c;
-                c.x = b8_encode4<E4>(bf16lo_to_f32(w.x), bf16hi_to_f32(w.x), bf16lo_to_f32(w.y), bf16hi_to_f32(w.y), inv);
-                c.y = b8_encode4<E4>(bf16lo_to_f32(w.z), bf16hi_to_f32(w.z), bf16lo_to_f32(w.w), bf16hi_to_f32(w.w), inv);
-                if (r >= 0 && r < n) pool[2 * i * 16] = c;
+                if (row0 + 2 * i >= r0) break;
+                uint2 c = pool[2 * i * 16];
+                const float4 p = b8_decode4<E4>(c.x), q = b8_decode4<E4>(c.y);
+                // code times scale is exact (15 bits); the quotient is rounded once, and is a tie exactly
+                // or 2^-16 away from one at least, which fp32 tells apart
+                auto again = [&](float u) { return __fdiv_rn(u * had, s); };
+                if constexpr (E4) {
+                    c.x = __nv_cvt_float2_to_fp8x2(make_float2(again(p.x), again(p.y)), __NV_SATFINITE, __NV_E4M3) |
+                          ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(again(p.z), again(p.w)), __NV_SATFINITE, __NV_E4M3) << 16);
+                    c.y = __nv_cvt_float2_to_fp8x2(make_float2(again(q.x), again(q.y)), __NV_SATFINITE, __NV_E4M3) |
+                          ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(again(q.z), again(q.w)), __NV_SATFINITE, __NV_E4M3) << 16);
+                } else {
+                    c.x = b8_encode4<E4>(rintf(again(p.x)), rintf(again(p.y)), rintf(again(p.z)), rintf(again(p.w)), 1.0f);
+                    c.y = b8_encode4<E4>(rintf(again(q.x)), rintf(again(q.y)), rintf(again(q.z)), rintf(again(q.w)), 1.0f);
+                }
+                pool[2 * i * 16] = c;
             }
+        }
+#pragma unroll
+        for (int i = 0; i < kB8Vecs; ++i) {
+            const int32_t r = row0 + 2 * i - r0;
+            const uint4 w = x[i];
+            uint2 c;
+            c.x = b8_encode4<E4>(bf16lo_to_f32(w.x), bf16hi_to_f32(w.x), bf16lo_to_f32(w.y), bf16hi_to_f32(w.y), inv);
+            c.y = b8_encode4<E4>(bf16lo_to_f32(w.z), bf16hi_to_f32(w.z), bf16lo_to_f32(w.w), bf16hi_to_f32(w.w), inv);
+            if (r >= 0 && r < n) pool[2 * i * 16] = c;
         }
     }
 }
@@ -267,7 +254,7 @@ cudaError_t launch_store_block8(bool e4m3, const void *k, const void *v, int64_t
     a.window = kB8Window;
     const int64_t want = 8 * (int64_t)nsm;
     const int groups = kB8Warps / (bs / kB8Rows);
-    const int32_t heads = (Hkv + groups - 1) / groups;  // turns that one run's heads take
+    const int32_t heads = (2 * Hkv + groups - 1) / groups;  // turns that one run's heads of K and V take
     while (a.window > 1 && ((int64_t)T + a.window - 1) / a.window * heads < want) a.window /= 2;
     const dim3 grid((unsigned)((T + (int64_t)a.window - 1) / a.window), (unsigned)(heads < 65535 ? heads : 65535));
     if (e4m3) store_block8_kernel<true><<<grid, kB8Threads, 0, stream>>>(a);
@@ -297,7 +284,7 @@ __device__ __forceinline__ int2 load8_rows(const Load8Args &a, int32_t b, bool f
 }
 
 template <bool E4>
-__global__ void __launch_bounds__(kB8Threads, 8) load_block8_kernel(const Load8Args a)
+__global__ void __launch_bounds__(kB8Threads, 12) load_block8_kernel(const Load8Args a)
 {
     extern __shared__ int32_t s_pre[];  // [B + 1] tiles of 16 tokens before each request
     __shared__ int32_t s_sum[kB8Warps];
@@ -326,11 +313,11 @@ __global__ void __launch_bounds__(kB8Threads, 8) load_block8_kernel(const Load8A
     if (tid == 0) s_pre[a.B] = carry;
     __syncthreads();
 
-    const int64_t items = (int64_t)carry * a.Hkv;
+    const int64_t items = (int64_t)carry * a.Hkv * 2;
     const int32_t shift = __ffs(a.bs) - 1;
     for (int64_t item = (int64_t)blockIdx.x * kB8Warps + warp; item < items; item += (int64_t)gridDim.x * kB8Warps) {
         // neighbouring warps: heads of the same tokens, whose rows lie side by side in the output
-        const int32_t tile = (int32_t)(item / a.Hkv), h = (int32_t)(item - (int64_t)tile * a.Hkv);
+        const int32_t q = (int32_t)(item / a.Hkv), h = (int32_t)(item - (int64_t)q * a.Hkv), tile = q >> 1, kv = q & 1;
         int32_t lo = 0, hi = a.B - 1;
         while (lo < hi) {
             const int32_t mid = (lo + hi + 1) >> 1;
@@ -349,26 +336,22 @@ __global__ void __launch_bounds__(kB8Threads, 8) load_block8_kernel(const Load8A
         const int32_t row0 = lane >> 4, vec = lane & 15;
         const int64_t src = (sc * a.bs + (t0 & (a.bs - 1)) + row0) * 16 + vec;
         const int64_t dst = ((int64_t)(rows.x + t0 + row0) * a.Hkv + h) * 16 + vec;
-        uint2 c[2][kB8Vecs];
+        uint2 c[kB8Vecs];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
+        for (int i = 0; i < kB8Vecs; ++i)
+            if (row0 + 2 * i < n) c[i] = __ldg(reinterpret_cast<const uint2 *>(kv ? a.vpool : a.kpool) + src + 32 * i);
+        const float s = __ldg((kv ? a.vscale : a.kscale) + sc);
 #pragma unroll
-            for (int i = 0; i < kB8Vecs; ++i)
-                if (row0 + 2 * i < n) c[kv][i] = __ldg(reinterpret_cast<const uint2 *>(kv ? a.vpool : a.kpool) + src + 32 * i);
-        const float s[2] = {__ldg(a.kscale + sc), __ldg(a.vscale + sc)};
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-            for (int i = 0; i < kB8Vecs; ++i) {
-                if (row0 + 2 * i >= n) continue;
-                const float4 p = b8_decode4<E4>(c[kv][i].x), q = b8_decode4<E4>(c[kv][i].y);
-                auto two = [&](float x, float y) {
-                    const __nv_bfloat162 w = __floats2bfloat162_rn(x * s[kv], y * s[kv]);
-                    return *reinterpret_cast<const uint32_t *>(&w);
-                };
-                __stcs((kv ? a.v : a.k) + dst + (int64_t)2 * i * a.Hkv * 16,
-                       make_uint4(two(p.x, p.y), two(p.z, p.w), two(q.x, q.y), two(q.z, q.w)));
-            }
+        for (int i = 0; i < kB8Vecs; ++i) {
+            if (row0 + 2 * i >= n) continue;
+            const float4 p = b8_decode4<E4>(c[i].x), q = b8_decode4<E4>(c[i].y);
+            auto two = [&](float x, float y) {
+                const __nv_bfloat162 w = __floats2bfloat162_rn(x * s, y * s);
+                return *reinterpret_cast<const uint32_t *>(&w);
+            };
+            __stcs((kv ? a.v : a.k) + dst + (int64_t)2 * i * a.Hkv * 16,
+                   make_uint4(two(p.x, p.y), two(p.z, p.w), two(q.x, q.y), two(q.z, q.w)));
+        }
     }
 }
 
@@ -393,8 +376,8 @@ cudaError_t launch_load_block8(bool e4m3, const uint8_t *kpool, const uint8_t *v
     a.max_blocks = max_blocks;
     a.num_blocks = num_blocks;
     a.total = total;
-    const int64_t most = ((int64_t)(total / kB8Rows) + B) * Hkv;  // tiles there can be
-    const int64_t need = (most + kB8Warps - 1) / kB8Warps, cap = (int64_t)nsm * 8;
+    const int64_t most = ((int64_t)(total / kB8Rows) + B) * Hkv * 2;  // tiles there can be
+    const int64_t need = (most + kB8Warps - 1) / kB8Warps, cap = B <= kB8Threads ? 0x7fffffff : (int64_t)nsm * 32;
     const unsigned grid = (unsigned)(need < cap ? (need < 1 ? 1 : need) : cap);
     const size_t smem = (size_t)(B + 1) * sizeof(int32_t);  // (33 KB at the largest batch)
     if (e4m3) load_block8_kernel<true><<<grid, kB8Threads, smem, stream>>>(a);

@@ -96,25 +96,16 @@ __global__ void __launch_bounds__(kExtendThreads) extend_tables_kernel(const Ext
         }
         __syncthreads();
     }
+    uint32_t before = 0u;
     if (tid == 0) {
         s_cu[a.B] = (int32_t)min(tok_carry, (int64_t)a.total_slots);
-        __threadfence();  // everything above was read; the last block may overwrite it
-        const uint32_t before = atomicAdd(&hdr->ended_ctas, 1u);
-        s_last = before + 1u == gridDim.x;
-        if (s_last) hdr->ended_ctas = 0u;  // for the next call
+        if (gridDim.x > 1) {
+            __threadfence();  // everything above was read; the last block may overwrite it
+            before = atomicAdd(&hdr->ended_ctas, 1u);  // (its answer is looked at behind the slots)
+        }
     }
     __syncthreads();
     const int32_t total = s_cu[a.B];
-    if (s_last) {
-        __threadfence();
-        for (int32_t b = tid; b < a.B; b += kExtendThreads) {
-            const int32_t L = s_len[b];
-            // (a request that gets nothing keeps its length; the inputs are as they were until here)
-            a.seq_lens_out[b] = L < 0 ? __ldcg(a.seq_lens + b) : L + (s_cu[b + 1] - s_cu[b]);
-        }
-        for (int32_t b = tid; b <= a.B; b += kExtendThreads) a.cu_new[b] = s_cu[b];
-        if (tid == 0) *a.free_used_out = s_used;
-    }
 
     const int64_t stride = (int64_t)gridDim.x * kExtendThreads * kExtendTokens;
     for (int64_t t0 = ((int64_t)blockIdx.x * kExtendThreads + tid) * kExtendTokens; t0 < a.total_slots; t0 += stride) {
@@ -155,6 +146,21 @@ __global__ void __launch_bounds__(kExtendThreads) extend_tables_kernel(const Ext
                 if (t0 + k < a.total_slots) a.slots[t0 + k] = slot[k];
         }
     }
+
+    if (tid == 0) {
+        s_last = before + 1u == gridDim.x;
+        if (s_last && gridDim.x > 1) hdr->ended_ctas = 0u;  // for the next call
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    for (int32_t b = tid; b < a.B; b += kExtendThreads) {
+        const int32_t L = s_len[b];
+        // (a request that gets nothing keeps its length; the inputs are as they were until here)
+        a.seq_lens_out[b] = L < 0 ? __ldcg(a.seq_lens + b) : L + (s_cu[b + 1] - s_cu[b]);
+    }
+    for (int32_t b = tid; b <= a.B; b += kExtendThreads) a.cu_new[b] = s_cu[b];
+    if (tid == 0) *a.free_used_out = s_used;
 }
 
 size_t extend_smem_bytes(int32_t B) { return (size_t)(3 * B + 1) * sizeof(int32_t); }
