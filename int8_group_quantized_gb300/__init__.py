@@ -227,6 +227,12 @@ def _operands(what: str, workspace, *specs) -> list:
     """Addresses of the operands and the workspace.  Refuses what the raw pointers would misread: each spec is
     (tensor, dtype, shape); tensors, and the workspace, must be contiguous and on the current CUDA device."""
     device = _device()
+    native = _native()
+    if native is not None:
+        at = native.operands(device, workspace, *specs)
+        if at is None:
+            raise DGQError(-1, what)
+        return at
     at = []
     for x, dtype, shape in specs:
         if x.dtype is not dtype or x.shape != shape or not x.is_contiguous() or x.get_device() != device:
@@ -236,6 +242,23 @@ def _operands(what: str, workspace, *specs) -> list:
         raise DGQError(-1, what)
     at.append(workspace.data_ptr())
     return at
+
+
+_native_module = False  # False: not looked for yet
+
+
+def _native():
+    """The module with the checks on tensors as one native call, None where it is not built (the checks then
+    run here)."""
+    global _native_module
+    if _native_module is False:
+        _torch()  # (its libraries are loaded first)
+        try:
+            from . import _tensors as module
+        except ImportError:
+            module = None
+        _native_module = module
+    return _native_module
 
 
 def _device() -> int:
@@ -359,7 +382,7 @@ def _windowed(what: str, window, sinks) -> bool:
     """Whether a call has a window (0: none, and then no sinks either)."""
     if window == 0 and sinks == 0:
         return False
-    if window < 1 or sinks < 0:
+    if not (1 <= window < 1 << 31 and 0 <= sinks < 1 << 31):  # (ctypes would cut a larger number to 32 bits)
         raise DGQError(-1, what)
     return True
 
@@ -605,6 +628,12 @@ def _token_rows(what: str, *xs) -> list:
     """Addresses and token strides of bf16 rows [T, Hkv, 128] whose heads lie side by side (slices of a fused
     projection's output)."""
     bf16, device, shape = _torch().bfloat16, _device(), xs[0].shape
+    native = _native()
+    if native is not None:
+        at = native.token_rows(device, *xs)
+        if at is None:
+            raise DGQError(-1, what)
+        return at
     at = []
     for x in xs:
         step, head, one = x.stride()

@@ -7,6 +7,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -14,6 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdgq.so")
+TENSORS = os.path.join(PKG, "_tensors.so")  # the binding's checks on tensors
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -54,7 +56,38 @@ def stale() -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+def build_tensors() -> None:
+    """Compiles _tensors.so against this machine's torch and Python.  The binding has the same checks in
+    Python, so a machine without the headers is told and goes without."""
+    import sysconfig
+    import torch
+    src = os.path.join(CSRC, "dgq_tensors.cpp")
+    root = os.path.dirname(torch.__file__)
+    inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    tmp = TENSORS + f".{os.getpid()}.tmp"
+    res = subprocess.run(
+        ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+         "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+         f"-Wl,-rpath,{lib}"], capture_output=True, text=True)
+    if res.returncode == 0:
+        os.replace(tmp, TENSORS)
+    else:
+        print(f"_tensors.so is not built, its checks run in Python:\n{res.stderr[-2000:]}", file=sys.stderr)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    src = os.path.join(CSRC, "dgq_tensors.cpp")
+    if force or not os.path.exists(TENSORS) or os.path.getmtime(src) > os.path.getmtime(TENSORS):
+        with cf.ThreadPoolExecutor(max_workers=1) as ex:
+            job = ex.submit(build_tensors)
+            lib = build_lib(force, verbose)
+            job.result()
+        return lib
+    return build_lib(force, verbose)
+
+
+def build_lib(force: bool = False, verbose: bool = False) -> str:
     if not force and not stale():
         return LIB
     nvcc = _nvcc()

@@ -1,0 +1,88 @@
+// dgq_tensors.cpp -- the binding's checks on tensors, as one native call: type, shape, contiguity and device
+// of every operand of an entry point, and their addresses.  In Python they take 0.35 us for each operand
+// (3.2 us of the 9.6 us of a call with nine of them), here 0.02; the smallest calls' kernels take 2 to 4 us.
+// __init__.py has the same checks for a tree in which this module is not built.
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+namespace {
+
+const at::Tensor *tensor_of(PyObject *x) { return THPVariable_Check(x) ? &THPVariable_Unpack(x) : nullptr; }
+
+bool on_device(const at::Tensor &t, long device) { return t.is_cuda() && t.get_device() == device; }
+
+PyObject *address(const at::Tensor &t) { return PyLong_FromVoidPtr(const_cast<void *>(t.const_data_ptr())); }
+
+// operands(device, workspace, (tensor, dtype, shape), ...): addresses of the tensors and of the workspace, or
+// None: one of them is not what the raw pointers would be read as.
+PyObject *operands(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    if (n < 2) {
+        PyErr_SetString(PyExc_TypeError, "operands(device, workspace, ...)");
+        return nullptr;
+    }
+    const long device = PyLong_AsLong(args[0]);
+    if (device == -1 && PyErr_Occurred()) return nullptr;
+    const at::Tensor *ws = tensor_of(args[1]);
+    if (!ws || !ws->is_contiguous() || !on_device(*ws, device)) Py_RETURN_NONE;
+    PyObject *out = PyList_New(n - 1);
+    if (!out) return nullptr;
+    for (Py_ssize_t i = 2; i < n; ++i) {
+        PyObject *spec = args[i];
+        bool ok = PyTuple_Check(spec) && PyTuple_GET_SIZE(spec) == 3;
+        const at::Tensor *t = ok ? tensor_of(PyTuple_GET_ITEM(spec, 0)) : nullptr;
+        PyObject *dtype = ok ? PyTuple_GET_ITEM(spec, 1) : nullptr, *shape = ok ? PyTuple_GET_ITEM(spec, 2) : nullptr;
+        ok = t && THPDtype_Check(dtype) && PyTuple_Check(shape) &&
+             t->scalar_type() == reinterpret_cast<THPDtype *>(dtype)->scalar_type && t->dim() == PyTuple_GET_SIZE(shape) &&
+             t->is_contiguous() && on_device(*t, device);
+        for (Py_ssize_t d = 0; ok && d < t->dim(); ++d)
+            ok = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, d)) == t->size(d);
+        PyObject *at = ok && !PyErr_Occurred() ? address(*t) : nullptr;
+        if (!at) {
+            Py_DECREF(out);
+            if (PyErr_Occurred()) return nullptr;
+            Py_RETURN_NONE;
+        }
+        PyList_SET_ITEM(out, i - 2, at);
+    }
+    PyList_SET_ITEM(out, n - 2, address(*ws));
+    return out;
+}
+
+// token_rows(device, tensor, ...): address and token stride of bf16 rows [T, heads, D] of one shape whose heads
+// lie side by side, or None.
+PyObject *token_rows(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    if (n < 2) {
+        PyErr_SetString(PyExc_TypeError, "token_rows(device, rows, ...)");
+        return nullptr;
+    }
+    const long device = PyLong_AsLong(args[0]);
+    if (device == -1 && PyErr_Occurred()) return nullptr;
+    const at::Tensor *first = tensor_of(args[1]);
+    for (Py_ssize_t i = 1; i < n; ++i) {
+        const at::Tensor *t = tensor_of(args[i]);
+        if (!first || !t || t->dim() != 3 || t->scalar_type() != at::kBFloat16 || t->sizes() != first->sizes() ||
+            t->stride(2) != 1 || (t->stride(1) != t->size(2) && t->size(1) > 1) || !on_device(*t, device))
+            Py_RETURN_NONE;
+    }
+    PyObject *out = PyList_New(2 * (n - 1));
+    if (!out) return nullptr;
+    for (Py_ssize_t i = 1; i < n; ++i) {
+        const at::Tensor *t = tensor_of(args[i]);
+        PyList_SET_ITEM(out, 2 * (i - 1), address(*t));
+        PyList_SET_ITEM(out, 2 * (i - 1) + 1, PyLong_FromLongLong(t->stride(0)));
+    }
+    return out;
+}
+
+PyMethodDef methods[] = {
+    {"operands", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(operands)), METH_FASTCALL, nullptr},
+    {"token_rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(token_rows)), METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__tensors(void) { return PyModule_Create(&module); }

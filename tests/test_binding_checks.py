@@ -1,0 +1,62 @@
+"""The checks on tensors run natively where that module is built and in Python elsewhere: both give the same
+answers to the same operands.  CPU only: the device is a stand-in where there is no GPU."""
+import pytest
+import torch
+
+
+@pytest.fixture
+def dgq(monkeypatch):
+    import int8_group_quantized_gb300 as dgq
+    return dgq
+
+
+def test_native_module_is_built_and_found(dgq):
+    from int8_group_quantized_gb300 import _build
+    _build.build()
+    assert dgq._native() is not None
+    assert dgq._native().__name__.endswith("_tensors")
+
+
+def test_host_tensors_are_refused_by_both(dgq, monkeypatch):
+    x, ws = torch.zeros(3, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
+    for native in (dgq._native(), None):
+        monkeypatch.setattr(dgq, "_native", lambda: native)
+        with pytest.raises(dgq.DGQError):
+            dgq._operands("x", ws, (x, torch.int32, (3,)))
+        with pytest.raises(dgq.DGQError):
+            dgq._token_rows("x", torch.zeros(2, 2, 128, dtype=torch.bfloat16))
+
+
+@pytest.mark.gpu
+def test_both_give_the_same_answers(dgq, monkeypatch):
+    d = "cuda"
+    i, f = torch.arange(12, dtype=torch.int32, device=d), torch.zeros(3, 4, device=d)
+    ws = torch.zeros(256, dtype=torch.uint8, device=d)
+    empty = torch.zeros(0, dtype=torch.int32, device=d)
+    fused = torch.zeros(5, 6, 128, dtype=torch.bfloat16, device=d)
+    operands = [
+        (ws, ((i, torch.int32, (12,)), (f, torch.float32, (3, 4)))), (ws, ((empty, torch.int32, (0,)),)), (ws, ()),
+        (ws, ((i, torch.int64, (12,)),)), (ws, ((i, torch.int32, (11,)),)), (ws, ((i, torch.int32, (12, 1)),)),
+        (ws, ((i, torch.int32, ()),)), (ws, ((f.t(), torch.float32, (4, 3)),)), (ws, ((f[:, :2], torch.float32, (3, 2)),)),
+        (ws, ((i.cpu(), torch.int32, (12,)),)), (ws[::2], ((i, torch.int32, (12,)),)), (ws.cpu(), ((i, torch.int32, (12,)),)),
+        (ws, ((torch.nn.Parameter(f), torch.float32, (3, 4)),)), (ws, ((i.view(3, 4), torch.int32, (3, torch.Size([4])[0])),)),
+    ]
+    token_rows = [(fused[:, :2], fused[:, 2:4]), (fused[:, :1],), (fused[:, ::2],), (fused[:, :2], fused[:, :3]), (fused[:0],),
+                  (fused.half(),), (fused.cpu(),), (fused[..., :64],), (fused[:, :1, ::2],), (fused[:1].expand(5, 6, 128),),
+                  (fused[:, 3:4].transpose(0, 1),)]
+
+    def answers():
+        for w, specs in operands:
+            try:
+                yield dgq._operands("x", w, *specs)
+            except dgq.DGQError as e:
+                yield e.status
+        for xs in token_rows:
+            try:
+                yield dgq._token_rows("x", *xs)
+            except dgq.DGQError as e:
+                yield e.status
+    native = list(answers())
+    monkeypatch.setattr(dgq, "_native", lambda: None)
+    assert native == list(answers())
+    assert native[0] == [i.data_ptr(), f.data_ptr(), ws.data_ptr()] and native.count(-1) == 9 + 7  # refused operands, refused rows
