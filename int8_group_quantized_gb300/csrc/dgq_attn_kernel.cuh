@@ -48,16 +48,28 @@
 //    to the tensor cores as they are, values transposed on the way out of shared memory
 //    (ldmatrix.trans), weights rounded to bf16.
 //  * A cache in 8 bits with one scale per block and head (INT8 or E4M3 codes): a tile lies in one block,
-//    so its two scales (copied into the ring beside it) are constants of the tile.  K's goes into the score;
+//    so its two scales (copied behind the warp's ring) are constants of the tile.  K's goes into the score;
 //    V's would change the unit of O at every tile, so it goes into the weight instead: with e = log2 of it,
 //    w = 2^(z + e - m) multiplies the codes themselves, m is the running maximum of z + e, and the
 //    normalising sum takes w 2^-e.  A block whose values are small then has small weights, and one whose
 //    scores are small too; neither leaves the range of fp16 for the other's sake.  The sum takes the
 //    weights before their rounding to fp16 (which may make a weight 0 that counts in the sum).
+//    These instances have the 16 tokens as the rows of S = K Q^T (8 products a tile where S^T = Q K^T takes
+//    16), turn the weights with two movmatrix, and look for the maximum over tokens only where one score
+//    exceeds the reference by 8: a vote per tile in place of six shuffles.  The sum of the rounded weights, against
+//    which INT8's offset of 1152 is taken off, is one more product with ones.  Measured, us in a graph over
+//    inputs larger than L2: 131072 tokens (269 MB) 51.0 INT8, 51.3 E4M3; 32 of 2048 (135 MB) 31.6, 31.7;
+//    56.0, 62.8, 34.4 and 38.9 with S^T as the other formats.  Of that the scales behind the ring in place of
+//    beside each stage (rows then keep to 128-byte lines of shared memory) made 4 us, E4M3 pairs converted
+//    without the header function's packing 5 (bit operations in place of half the conversions: 59.2).  Four
+//    blocks per SM at depth 2, and two at depth 5, were slower (51.7 to 60.9); refilling a stage before its
+//    arithmetic changed nothing.  What is left above the floor (39.5, 19.9): the first tile lands 5 to 8 us
+//    after the start, blocks end between 21 and 28 us (32 of 2048), the merge takes 3.
 //  * With a window (Win), a pair's tiles are those of the first tokens that stay visible and those of the
 //    window: tile j of the list is tile j of the request up to the last sink tile, then `skip` further.
 //    Tiles without a visible token are not in the list, so what lies there is never read, and every tile
-//    that is in it moves the running maximum off -inf.
+//    that is in it moves the running maximum off -inf.  64 requests of 128 to 32768, window 4096, bf16 (592 MB
+//    seen): 96.8 us, 90% of the copy rate; 32 of 32768, window 8192, INT8 (546 MB): 93.5 us, 86%.
 #pragma once
 
 #include "dgq_device.cuh"

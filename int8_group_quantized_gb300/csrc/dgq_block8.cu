@@ -17,11 +17,15 @@
 //
 // Bound by HBM: a token's row of a head is 256 bytes read and 128 written by the store, the other way
 // round by the load.  Work of the store: a run of tokens that lie one behind the other in a block, for one
-// head: a warp for 16 of the block's rows, 16 bytes a lane, all its rows of K and V in registers (16 loads
-// in flight), so that values are read once for amax and codes.  The four warps of a block of threads take
+// head of K or V: a warp for 16 of the block's rows, 16 bytes a lane, its rows in registers (8 loads in
+// flight), so that values are read once for amax and codes.  The four warps of a block of threads take
 // four blocks of 16 tokens, or share one of 64.  Runs are found on the fly: a block of threads looks at a
 // window of slots, from one token (decode steps: more blocks of threads than SMs) to 128.
-// Load: a warp for 16 tokens of one head, 2 KB of codes.
+// Load: a warp for 16 tokens of one head of K or V, 2 KB of codes.
+// Measured, us in a graph: four chunks of 2048 tokens into blocks of 64, 8 heads (50 MB): 15.0 (floor 7.4;
+// blocks of 16: 12.7), 16.3 with K and V in one item at four blocks of threads per SM; it is two waves of
+// three dependent loads (slots, scale and rows, codes).  53000 tokens loaded (255 MB, two thirds of it
+// written): 44.9, 5.7 TB/s; 49.4 from a grid of eight blocks of threads per SM that walk the list.
 #include "dgq_device.cuh"
 #include "dgq.h"
 #include "dgq_launch.h"

@@ -56,9 +56,18 @@
 //  * With a window (Win; w last tokens, s first ones), a unit's key tiles are those of the sinks and those
 //    from the window of its first row on: step j of the unit is key tile j below `sink`, key tile j + skip
 //    from there on, and everything that counts key tiles (cuts, costs, pieces) counts steps.  The second
-//    tile's rows may see nothing of the first step of the window; their weights are then all 0.  Pages of
+//    tile's rows may see nothing of the first step of the window: it then passes over that step.  Few sinks
+//    (at most 32) take a step of 32 keys, S with N = 32 and two of the eight products with P.  Pages of
 //    a key tile that hold no key that any row of the unit sees are not read (their V rows are zeroed), so
 //    that stale table entries and reused pages never reach a product.
+//    Measured, us in a graph: 16384 tokens over pages, window 4096, 64 sinks, 32/8 heads: 590 to 630 (floor 501
+//    at the burst rate; under the power cap); window 1024, 4 sinks: 210 (218 with the sinks as a whole step);
+//    eight of 2048, window 128, 4 sinks: 85 (91), 64/8 heads 154 (167); sixteen ragged prompts, 32/32 heads,
+//    window 256: 106.  With windows this short a unit is a chain: two or three steps of 2300 to 3300 cycles
+//    (softmax, P's products, the next scores), the last product 400, rows out 1800, the next item 700.
+//    Measured and not kept: edge steps in rolled passes over 32 columns, unseen ones left out (eight of 2048
+//    94); unseen quarters left out in place (16384 656); Q prefetched into L2 (eight of 2048 90): each
+//    change of the softmax code moves all windows by 4 to 10%.
 //  * Every wait is bounded: one that runs out records an error and its role leaves, after which the others'
 //    waits run out too.
 #include "dgq_device.cuh"

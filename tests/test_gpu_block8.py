@@ -401,3 +401,75 @@ def test_binding_refuses_other_shapes_and_types():
     for window, sinks in ((0, 1), (-1, 0), (4, -1)):
         with pytest.raises(dgq.DGQError):
             dgq.dgq_paged_decode_attn_block8(*good.values(), window=window, sinks=sinks)
+
+
+@FMT
+def test_windows_of_slots_with_many_runs_and_heads(fmt):
+    """Calls large enough for the largest window of slots: whole blocks of a long prompt, and short runs."""
+    blocks, hkv = 320, 32
+    c = Cache(fmt, blocks, hkv, 64)
+    x, y = tokens(20000, hkv, 21), tokens(20000, hkv, 22)
+    order = np.random.default_rng(1).permutation(blocks)
+    c.store(x, y, slots_of(order, 64, 0, 20000))
+    c.verify()
+    slots = [int(64 * b + b % 61 + r) for b in order[:312] for r in range(3)]  # (whole blocks, written again inside)
+    k, v = tokens(len(slots), hkv, 23), tokens(len(slots), hkv, 24)
+    c.store(k, v, slots)
+    c.verify()
+
+
+@pytest.mark.parametrize("batch", [300, 8192])
+def test_load_of_many_requests(batch):
+    import int8_group_quantized_gb300 as dgq
+    lens = np.random.default_rng(batch).integers(0, 40, batch).tolist()
+    c, table = filled("int8", lens, 1, 16, 31)
+    out = [torch.zeros(sum(lens), 1, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    dgq.dgq_load_block8("int8", *c.d_codes, *c.d_scales, i32(table), i32(np.concatenate([[0], np.cumsum(lens)])), *out, c.ws)
+    c.verify()
+    for which, o in enumerate(out):
+        want = torch.cat([torch.from_numpy(values(c, table, b, n, which)[0]) for b, n in enumerate(lens)])
+        assert torch.equal(o.cpu(), want.float().to(torch.bfloat16))
+
+
+@FMT
+@pytest.mark.parametrize("window", [0, 300])
+def test_decode_scores_of_any_size(fmt, window):
+    """Scores of 10^4 to 10^9: one token's lies above all others by its own size, far more than fp32 loses
+    (136 2^-24 of it), so its value is the result, rounded to bf16."""
+    for size, big in ((30.0, 30.0), (3e4, 100.0), (6e4, 3e4)):
+        s = Step(fmt, [1000], 4, 1, 16, 40)
+        at = 900
+        s.q[:] = (torch.sign(s.q.float()) * size).to(torch.bfloat16)
+        sign = torch.sign(s.q[0, 0].float())
+        s.q[:] = s.q[0, 0]
+        k = (-big * sign).expand(1000, 1, 128).clone()
+        k[at] = big * sign
+        v = tokens(1000, 1, 41)
+        s.kn[:] = (-big * sign).to(torch.bfloat16)
+        s.c.store(k.to(torch.bfloat16), v, slots_of(s.table[0], 16, 0, 1000))
+        out = s.run(window, 0).cpu()
+        want = torch.from_numpy(values(s.c, s.table, 0, 1000, 1)[0][at, 0])
+        assert ((out[0].double() - want).abs() <= 2.0 ** -8 * want.abs() * 1.01).all()
+
+
+def test_threads_on_streams_of_their_own():
+    import threading
+    import int8_group_quantized_gb300 as dgq
+    steps = [Step(fmt, [700, 33 + i, 0], 8, 2, 16, 50 + i) for i, fmt in enumerate(["int8", "e4m3"] * 3)]
+    want = [s.run(100 if i % 3 else 0, 3 if i % 3 else 0) for i, s in enumerate(steps)]
+    got, errors = [None] * 6, []
+
+    def work(i, s):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    got[i] = s.run(100 if i % 3 else 0, 3 if i % 3 else 0)
+        except Exception as e:  # (shown by the main thread)
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=x) for x in enumerate(steps)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
