@@ -234,6 +234,13 @@ size_t attn_smem_bytes(int dec, int32_t B, int32_t G)
            8 * 4 + (size_t)(2 * B + 1) * 4;
 }
 
+// Short pairs (of the instances that can): every CTA takes whole pairs, and there is no merge, its launch and
+// its reads.  Four warps then go through a pair's tiles alone, so it pays up to so many tiles of the longest
+// pair, more where there are pairs for most SMs.  us, whole against split: 4 pairs of 256 tokens 7.2 / 8.7, of 512
+// 9.8 / 8.8; 64 pairs of 512 10.8 / 11.3, of 1024 14.9 / 12.3; 256 pairs of 512 13.7 / 17.3; 1024 pairs of 512
+// 34.1 / 36.1, of 1024 56.4 / 54.9; window 128 of 64 requests up to 32768 15.8 / 19.2, window 512 28.8 / 30.2.
+constexpr int64_t kWholeTiles = 24, kWholeTilesMany = 40, kWholeMany = 64;
+
 int attn_max_ctas(int nsm) { return nsm * kMaxCtasPerSm; }
 
 AttnLayout attn_layout(int32_t batch, int32_t Hq, int32_t Hkv, int nsm)
@@ -351,11 +358,14 @@ cudaError_t launch_attn(int32_t format, const void *q, const void *knew, const v
     }
     const int64_t tiles = (int64_t)B * Hkv * per_pair;
     int64_t grid = (int64_t)nsm * shape.occ;
+    a.whole = (win || dec == kDecBlockI8 || dec == kDecBlockE4) &&
+              per_pair <= ((int64_t)B * Hkv >= kWholeMany ? kWholeTilesMany : kWholeTiles);
+    if (a.whole && grid > (int64_t)B * Hkv) grid = (int64_t)B * Hkv;
     if (grid > tiles) grid = tiles;
     if (grid < 1) grid = 1;
     kern<<<(unsigned)grid, kAttnThreads, smem, stream>>>(a);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.whole) return e;
 
     // merge of shared pairs, chained with programmatic dependent launch
     cudaLaunchConfig_t cfg = {};

@@ -67,6 +67,7 @@
 //    after the start, blocks end between 21 and 28 us (32 of 2048), the merge takes 3.
 //  * With a window (Win), a pair's tiles are those of the first tokens that stay visible and those of the
 //    window: tile j of the list is tile j of the request up to the last sink tile, then `skip` further.
+//    (Calls of these instances whose pairs are all short are sliced at pairs and need no merge: dgq_attn.cu.)
 //    Tiles without a visible token are not in the list, so what lies there is never read, and every tile
 //    that is in it moves the running maximum off -inf.  64 requests of 128 to 32768, window 4096, bf16 (592 MB
 //    seen): 96.8 us, 90% of the copy rate; 32 of 32768, window 8192, INT8 (546 MB): 93.5 us, 86%.
@@ -146,6 +147,7 @@ struct AttnArgs {
     int32_t *held;    // per CTA of the main kernel: 1 when its slice holds tiles
     float *part;
     int32_t B, Hq, Hkv, G, bs, max_blocks, num_blocks;
+    int32_t whole;          // (instances of dgq_attn_window.cu) 1: every CTA takes whole pairs, nothing is merged
     int32_t window, sinks;  // Win: cached tokens t are seen where t > L - window or t < sinks
 };
 
@@ -516,8 +518,18 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
     // C cta / ncta and C (cta + 1) / ncta from one quotient (a 64-bit division takes 400 cycles)
     const int64_t share = C >> 32 ? C / ncta : (int64_t)((uint32_t)C / (uint32_t)ncta);
     const int32_t rest = (int32_t)(C - share * ncta);  // < ncta
-    const int32_t c0 = tile_at<Win>(share * cta + rest * cta / ncta, s_tpre, s_len, a);
-    const int32_t c1 = tile_at<Win>(share * (cta + 1) + rest * (cta + 1) / ncta, s_tpre, s_len, a);
+    int32_t c0, c1;
+    if ((Win || is_block8<Fmt>()) && a.whole) {  // pairs P cta / ncta .. P (cta + 1) / ncta
+        auto pair_start = [&](int32_t i) {
+            const int32_t p = (int32_t)((int64_t)B * Hkv * i / ncta), b = p / Hkv;
+            return b < B ? s_tpre[b] + (p - b * Hkv) * tiles_of<Win>(s_len[b], a) : T;
+        };
+        c0 = pair_start(cta);
+        c1 = pair_start(cta + 1);
+    } else {
+        c0 = tile_at<Win>(share * cta + rest * cta / ncta, s_tpre, s_len, a);
+        c1 = tile_at<Win>(share * (cta + 1) + rest * (cta + 1) / ncta, s_tpre, s_len, a);
+    }
     if (tid == 0) a.held[cta] = c0 < c1 ? 1 : 0;  // read by the merge kernels
     if (cta == 0 && tid == 0) a.hdr->pad[kHdrAllHeld] = share > kPieceCost ? 1u : 0u;
     if (c0 >= c1) return;  // the whole CTA: no barrier follows for it
