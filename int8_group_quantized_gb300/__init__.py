@@ -255,10 +255,17 @@ def _native():
         _torch()  # (its libraries are loaded first)
         try:
             from . import _tensors as module
+            lib()
+            module.load(_build.LIB)
         except ImportError:
             module = None
         _native_module = module
     return _native_module
+
+
+def _entries():
+    """Where the entry points of small calls are: the native module, or ctypes where it is not built."""
+    return _native() or lib()
 
 
 def _device() -> int:
@@ -619,7 +626,7 @@ def dgq_extend_tables(seq_lens, new_lens, block_size, num_blocks, free_ids, free
         "dgq_extend_tables", workspace, (seq_lens, i32, (B,)), (new_lens, i32, (B,)), (free_ids, i32, (free_ids.numel(),)),
         (free_used, i32, (1,)), (block_tables, i32, (B, columns)), (slots, i32, (slots.numel(),)), (cu_new, i32, (B + 1,)),
         (seq_lens_out, i32, (B,)), (free_used_out, i32, (1,)))
-    _check(lib().dgq_extend_tables(lens, new, B, int(block_size), int(num_blocks), ids, free_ids.numel(), used, table,
+    _check(_entries().dgq_extend_tables(lens, new, B, int(block_size), int(num_blocks), ids, free_ids.numel(), used, table,
                                    columns, slots_, slots.numel(), cu, lens_out, used_out, ws, _nbytes(workspace),
                                    _stream(stream)), "dgq_extend_tables")
 
@@ -655,7 +662,7 @@ def dgq_write_slots(k, v, slots, k_pages, v_pages, workspace, stream=None) -> No
     cache = (torch.bfloat16, (blocks, Hkv, bs, D))
     k_, k_step, v_, v_step = _token_rows("dgq_write_slots", k, v)
     at, kp, vp, ws = _operands("dgq_write_slots", workspace, (slots, torch.int32, (T,)), (k_pages, *cache), (v_pages, *cache))
-    _check(lib().dgq_write_slots(k_, v_, k_step, v_step, T, Hkv, D, at, kp, vp, blocks, bs, ws, _nbytes(workspace),
+    _check(_entries().dgq_write_slots(k_, v_, k_step, v_step, T, Hkv, D, at, kp, vp, blocks, bs, ws, _nbytes(workspace),
                                  _stream(stream)), "dgq_write_slots")
 
 
@@ -680,7 +687,7 @@ def dgq_store_block8(fmt, k, v, slots, k_pool, v_pool, k_scales, v_scales, works
     at, kp, vp, ks, vs, ws = _operands(
         "dgq_store_block8", workspace, (slots, torch.int32, (T,)), (k_pool, u8, cache), (v_pool, u8, cache),
         (k_scales, f32, scale), (v_scales, f32, scale))
-    _check(lib().dgq_store_block8(_block8_id(fmt), k_, v_, k_step, v_step, T, Hkv, D, at, kp, vp, ks, vs, blocks, bs, ws,
+    _check(_entries().dgq_store_block8(_block8_id(fmt), k_, v_, k_step, v_step, T, Hkv, D, at, kp, vp, ks, vs, blocks, bs, ws,
                                   _nbytes(workspace), _stream(stream)), "dgq_store_block8")
 
 
@@ -697,7 +704,7 @@ def dgq_load_block8(fmt, k_pool, v_pool, k_scales, v_scales, block_tables, cu_kv
         "dgq_load_block8", workspace, (k_pool, u8, cache), (v_pool, u8, cache), (k_scales, f32, scale),
         (v_scales, f32, scale), (block_tables, i32, (B, columns)), (cu_kv, i32, (B + 1,)), (k, bf16, (T, Hkv, D)),
         (v, bf16, (T, Hkv, D)))
-    _check(lib().dgq_load_block8(_block8_id(fmt), kp, vp, ks, vs, blocks, bs, table, columns, cu, B, Hkv, D, k_, v_, T, ws,
+    _check(_entries().dgq_load_block8(_block8_id(fmt), kp, vp, ks, vs, blocks, bs, table, columns, cu, B, Hkv, D, k_, v_, T, ws,
                                  _nbytes(workspace), _stream(stream)), "dgq_load_block8")
 
 
@@ -716,7 +723,7 @@ def dgq_paged_decode_attn_block8(fmt, q, k_new, v_new, k_pool, v_pool, k_scales,
         (k_pool, u8, cache), (v_pool, u8, cache), (k_scales, f32, scale), (v_scales, f32, scale),
         (block_tables, i32, (B, columns)), (seq_lens, i32, (B,)), (out, bf16, (B, Hq, D)))
     _windowed("dgq_paged_decode_attn_block8", window, sinks)
-    _check(lib().dgq_paged_decode_attn_block8(_block8_id(fmt), q_, kn, vn, kp, vp, ks, vs, bt, lens, int(max_seqlen), B,
+    _check(_entries().dgq_paged_decode_attn_block8(_block8_id(fmt), q_, kn, vn, kp, vp, ks, vs, bt, lens, int(max_seqlen), B,
                                               Hq, Hkv, D, bs, columns, blocks, int(window), int(sinks), o, ws,
                                               _nbytes(workspace), _stream(stream)), "dgq_paged_decode_attn_block8")
 

@@ -68,7 +68,7 @@ def build_tensors() -> None:
     res = subprocess.run(
         ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
          "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-         "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+         "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, src, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-ldl",
          f"-Wl,-rpath,{lib}"], capture_output=True, text=True)
     if res.returncode == 0:
         os.replace(tmp, TENSORS)
@@ -77,8 +77,8 @@ def build_tensors() -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    src = os.path.join(CSRC, "dgq_tensors.cpp")
-    if force or not os.path.exists(TENSORS) or os.path.getmtime(src) > os.path.getmtime(TENSORS):
+    made_of = [os.path.join(CSRC, "dgq_tensors.cpp"), os.path.join(INCLUDE, "dgq.h")]
+    if force or not os.path.exists(TENSORS) or any(os.path.getmtime(f) > os.path.getmtime(TENSORS) for f in made_of):
         with cf.ThreadPoolExecutor(max_workers=1) as ex:
             job = ex.submit(build_tensors)
             lib = build_lib(force, verbose)

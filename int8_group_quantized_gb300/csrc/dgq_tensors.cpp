@@ -1,11 +1,85 @@
-// dgq_tensors.cpp -- the binding's checks on tensors, as one native call: type, shape, contiguity and device
-// of every operand of an entry point, and their addresses.  In Python they take 0.35 us for each operand
-// (3.2 us of the 9.6 us of a call with nine of them), here 0.02; the smallest calls' kernels take 2 to 4 us.
-// __init__.py has the same checks for a tree in which this module is not built.
+// dgq_tensors.cpp -- the binding's checks on tensors, as one native call (type, shape, contiguity and device
+// of every operand of an entry point, and their addresses), and the entry points of the smallest calls
+// without ctypes' conversions.  In Python the checks take 0.35 us for each operand (3.2 us of the 9.6 us of a
+// call with nine of them), here 1 us for ten; ctypes takes 1.4 to 1.9 us for 18 to 24 arguments, here 0.3.
+// The smallest calls' kernels take 2 to 4 us.  __init__.py has the same checks, and ctypes, for a tree in
+// which this module is not built.
+#include <dlfcn.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <tuple>
+#include <type_traits>
+#include <utility>
+
+#include "dgq.h"
+
 namespace {
+
+// ---- entry points -----------------------------------------------------------------------------------
+
+void *library = nullptr;  // libdgq.so, as the binding opened it
+
+template <typename A>
+A argument(PyObject *x)
+{
+    if constexpr (std::is_pointer_v<A>) {
+        return static_cast<A>(PyLong_AsVoidPtr(x));
+    } else if constexpr (std::is_unsigned_v<A>) {
+        return static_cast<A>(PyLong_AsSize_t(x));
+    } else {
+        const long long v = PyLong_AsLongLong(x);
+        if (!PyErr_Occurred() && v != static_cast<A>(v)) PyErr_SetString(PyExc_OverflowError, "argument out of range");
+        return static_cast<A>(v);
+    }
+}
+
+template <typename... A, size_t... I>
+PyObject *invoke(dgq_status (*f)(A...), PyObject *const *args, Py_ssize_t n, std::index_sequence<I...>)
+{
+    if (!f || n != static_cast<Py_ssize_t>(sizeof...(A))) {
+        PyErr_SetString(PyExc_TypeError, f ? "wrong number of arguments" : "the library is not loaded");
+        return nullptr;
+    }
+    const std::tuple<A...> a{argument<A>(args[I])...};
+    if (PyErr_Occurred()) return nullptr;
+    dgq_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = f(std::get<I>(a)...);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(status);
+}
+
+template <typename... A>
+PyObject *invoke(dgq_status (*f)(A...), PyObject *const *args, Py_ssize_t n)
+{
+    return invoke(f, args, n, std::index_sequence_for<A...>{});
+}
+
+#define ENTRY(name)                                                                                            \
+    PyObject *call_##name(PyObject *, PyObject *const *args, Py_ssize_t n)                                      \
+    {                                                                                                          \
+        static const auto f = reinterpret_cast<decltype(&name)>(library ? dlsym(library, #name) : nullptr);     \
+        return invoke(f, args, n);                                                                             \
+    }
+ENTRY(dgq_extend_tables)
+ENTRY(dgq_write_slots)
+ENTRY(dgq_store_block8)
+ENTRY(dgq_load_block8)
+ENTRY(dgq_paged_decode_attn_block8)
+#undef ENTRY
+
+// load(path): opens the library (the one that ctypes has open already).
+PyObject *load(PyObject *, PyObject *path)
+{
+    const char *p = PyUnicode_AsUTF8(path);
+    if (!p) return nullptr;
+    if (!library) library = dlopen(p, RTLD_NOW | RTLD_LOCAL);
+    if (!library) return PyErr_Format(PyExc_RuntimeError, "%s", dlerror());
+    Py_RETURN_NONE;
+}
+
+// ---- checks -------------------------------------------------------------------------------------------
 
 const at::Tensor *tensor_of(PyObject *x) { return THPVariable_Check(x) ? &THPVariable_Unpack(x) : nullptr; }
 
@@ -76,7 +150,14 @@ PyObject *token_rows(PyObject *, PyObject *const *args, Py_ssize_t n)
     return out;
 }
 
+#define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(call_##name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
+    ENTRY(dgq_extend_tables),
+    ENTRY(dgq_write_slots),
+    ENTRY(dgq_store_block8),
+    ENTRY(dgq_load_block8),
+    ENTRY(dgq_paged_decode_attn_block8),
+    {"load", load, METH_O, nullptr},
     {"operands", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(operands)), METH_FASTCALL, nullptr},
     {"token_rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(token_rows)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -17,6 +17,23 @@ def test_native_module_is_built_and_found(dgq):
     assert dgq._native().__name__.endswith("_tensors")
 
 
+def test_entry_points_without_ctypes(dgq):
+    """Same statuses; an argument that does not fit its C type is an error and not cut."""
+    native, fake = dgq._native(), 0x10000
+    rows = [fake, fake, 256, 256, 5, 2, 128, fake, fake, fake, 8, 16, fake, 256, 0]
+    for change, status in (({}, None), ({4: 0}, 0), ({4: -1}, -1), ({6: 64}, -2), ({13: 255}, -3), ({0: fake + 4}, -1)):
+        args = [change.get(i, a) for i, a in enumerate(rows)]
+        if status is not None:
+            assert native.dgq_write_slots(*args) == status == dgq.lib().dgq_write_slots(*args)
+    for bad in ({4: 1 << 32}, {13: -1}, {2: 1 << 70}):
+        with pytest.raises(OverflowError):
+            native.dgq_write_slots(*[bad.get(i, a) for i, a in enumerate(rows)])
+    with pytest.raises(TypeError):
+        native.dgq_write_slots(*rows[:-1])
+    with pytest.raises(TypeError):
+        native.dgq_write_slots(*[None] + rows[1:])
+
+
 def test_host_tensors_are_refused_by_both(dgq, monkeypatch):
     x, ws = torch.zeros(3, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
     for native in (dgq._native(), None):
