@@ -485,34 +485,60 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
         mbar_init(&pbar[1], 1);
         fence_barrier_init();
     }
-    for (int i = tid; i < B; i += kAttnThreads) {
+    auto length_of = [&](int i) -> int32_t {
         int32_t L = __ldg(a.seq_lens + i);
         if (L < 0 || L > a.max_blocks * a.bs) {  // beyond the block table's row: flagged, clamped
             record_error(a.hdr, kErrBadLength);
             L = L < 0 ? 0 : a.max_blocks * a.bs;
         }
-        s_len[i] = L;
-    }
-    __syncthreads();
-    if (warp == 0) {  // exclusive scan of Hkv * tiles_of(L_b)
-        int32_t carry = 0;
-        for (int base = 0; base < B; base += 32) {
-            const int i = base + lane;
-            const int32_t v = i < B ? Hkv * tiles_of<Win>(s_len[i], a) : 0;
-            int32_t x = v;
+        return L;
+    };
+    // Up to 32 requests: every warp holds them in its lanes and finds the slice's ends by votes, with one
+    // barrier in front of the tiles.  (Scan, searches and two barriers through shared memory, as for more
+    // requests, took 1.7 us of the 5 in front of the first tile.)
+    const bool few = B <= 32;
+    int32_t my_len = 0, my_pre = 0, T;  // few: this lane's request, its length and its first tile
+    if (few) {
+        my_len = lane < B ? length_of(lane) : 0;
+        const int32_t v = lane < B ? Hkv * tiles_of<Win>(my_len, a) : 0;
+        int32_t x = v;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            if (i < B) s_tpre[i] = carry + x - v;
-            carry += __shfl_sync(0xffffffffu, x, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
         }
-        if (lane == 0) s_tpre[B] = carry;
+        my_pre = x - v;
+        T = __shfl_sync(0xffffffffu, x, 31);
+        if (warp == 0) {
+            if (lane < B) {
+                s_len[lane] = my_len;
+                s_tpre[lane] = my_pre;
+            }
+            if (lane == 0) s_tpre[B] = T;
+        }
+    } else {
+        for (int i = tid; i < B; i += kAttnThreads) s_len[i] = length_of(i);
+        __syncthreads();
+        if (warp == 0) {  // exclusive scan of Hkv * tiles_of(L_b)
+            int32_t carry = 0;
+            for (int base = 0; base < B; base += 32) {
+                const int i = base + lane;
+                const int32_t v = i < B ? Hkv * tiles_of<Win>(s_len[i], a) : 0;
+                int32_t x = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (i < B) s_tpre[i] = carry + x - v;
+                carry += __shfl_sync(0xffffffffu, x, 31);
+            }
+            if (lane == 0) s_tpre[B] = carry;
+        }
+        __syncthreads();
+        T = s_tpre[B];
     }
-    __syncthreads();
 
-    const int32_t T = s_tpre[B];
     const int64_t C = (int64_t)T + (int64_t)kPieceCost * B * Hkv;  // total cost
     const int32_t ncta = gridDim.x, cta = blockIdx.x;
     // C cta / ncta and C (cta + 1) / ncta from one quotient (a 64-bit division takes 400 cycles)
@@ -520,12 +546,27 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
     const int32_t rest = (int32_t)(C - share * ncta);  // < ncta
     int32_t c0, c1;
     if ((Win || is_block8<Fmt>()) && a.whole) {  // pairs P cta / ncta .. P (cta + 1) / ncta
-        auto pair_start = [&](int32_t i) {
-            const int32_t p = (int32_t)((int64_t)B * Hkv * i / ncta), b = p / Hkv;
+        const uint32_t P = (uint32_t)B * Hkv, each = P / ncta, more = P - each * ncta;
+        if (few) __syncthreads();  // (the lengths are looked up)
+        auto pair_start = [&](uint32_t i) {
+            const int32_t p = (int32_t)(each * i + more * i / ncta), b = p / Hkv;
             return b < B ? s_tpre[b] + (p - b * Hkv) * tiles_of<Win>(s_len[b], a) : T;
         };
         c0 = pair_start(cta);
         c1 = pair_start(cta + 1);
+    } else if (few) {
+        const int64_t kh = (int64_t)kPieceCost * Hkv, my_cost = my_pre + kh * lane;
+        auto at = [&](int64_t q) -> int32_t {  // as tile_at
+            if (q >= C) return T;
+            const int b = __popc(__ballot_sync(0xffffffffu, lane < B && my_cost <= q)) - 1;
+            const int32_t base = __shfl_sync(0xffffffffu, my_pre, b);
+            const int32_t ntl = tiles_of<Win>(__shfl_sync(0xffffffffu, my_len, b), a);
+            const uint32_t r = (uint32_t)(q - (base + kh * b)), u = (uint32_t)(ntl + kPieceCost), h = r / u;
+            return base + (int32_t)h * ntl + max(0, (int32_t)(r - h * u) - kPieceCost);
+        };
+        c0 = at(share * cta + rest * cta / ncta);
+        c1 = at(share * (cta + 1) + rest * (cta + 1) / ncta);
+        __syncthreads();
     } else {
         c0 = tile_at<Win>(share * cta + rest * cta / ncta, s_tpre, s_len, a);
         c1 = tile_at<Win>(share * (cta + 1) + rest * (cta + 1) / ncta, s_tpre, s_len, a);
@@ -543,7 +584,14 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
 
     // ---- pieces of this CTA's slice, and the staging of their data two pieces ahead
     Piece cur;
-    {
+    if (few) {
+        cur.b = __popc(__ballot_sync(0xffffffffu, lane < B && my_pre <= c0)) - 1;
+        cur.L = __shfl_sync(0xffffffffu, my_len, cur.b);
+        cur.ntl = tiles_of<Win>(cur.L, a);
+        const int32_t base = __shfl_sync(0xffffffffu, my_pre, cur.b);
+        cur.h = (c0 - base) / cur.ntl;
+        cur.fp = base + cur.h * cur.ntl;
+    } else {
         const TileLoc c = locate_tile<Win>(c0, s_tpre, s_len, a);
         cur.b = c.b; cur.h = c.h; cur.ntl = c.ntl; cur.L = c.L;
         cur.fp = s_tpre[c.b] + c.h * c.ntl;
@@ -559,16 +607,6 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
         bulk_load(dst + kPbVnew, a.vnew + ((int64_t)pz.b * Hkv + pz.h) * kD, 256, &pbar[buf]);
         bulk_load(dst + kPbQ, a.q + ((int64_t)pz.b * a.Hq + pz.h * G) * kD, (uint32_t)(256 * G), &pbar[buf]);
     };
-    Piece ahead = cur;  // the next piece to stage
-    if (tid == 0) {
-        stage_piece(ahead, 0);
-        next_piece<Win>(ahead, s_tpre, s_len, a);
-        if (ahead.fp < c1) stage_piece(ahead, 1);
-    } else {
-        next_piece<Win>(ahead, s_tpre, s_len, a);
-    }
-    next_piece<Win>(ahead, s_tpre, s_len, a);  // ahead = piece 2
-
     // This warp's tiles: x = xw0 + 4k, k = 0 .. nmine-1, inside the CTA's slice [c0, c1).
     const int32_t xw0 = c0 + warp;
     const int32_t nmine = c1 > xw0 ? (c1 - xw0 + kWarpsPerCta - 1) / kWarpsPerCta : 0;
@@ -578,7 +616,16 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
         const int32_t k = kbase + lane;
         int32_t blk = 0;
         if (k < nmine) {
-            const TileLoc c = locate_tile<Win>(xw0 + kWarpsPerCta * k, s_tpre, s_len, a);
+            const int32_t x = xw0 + kWarpsPerCta * k;
+            TileLoc c;
+            if (x < s_tpre[cur.b + 1]) {  // in the current piece's request: no search
+                c.b = cur.b;
+                c.L = cur.L;
+                c.j = x - s_tpre[cur.b];
+                c.j -= c.j / cur.ntl * cur.ntl;
+            } else {
+                c = locate_tile<Win>(x, s_tpre, s_len, a);
+            }
             const int32_t jr = real_tile<Win>(c.j, c.L, a);
             if (Win ? jr * kTile < c.L : c.L > 0) blk = __ldg(a.bt + (int64_t)c.b * a.max_blocks + pow2_div(jr, per_blk));
         }
@@ -591,12 +638,22 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
     };
     int32_t kb = 0;
     int32_t bq_cur = fetch_batch(0), bq_next = fetch_batch(32);  // bq_next is checked when its turn comes
+    // the first two pieces' data (while the ids are on their way)
+    Piece ahead = cur;  // the next piece to stage
+    if (tid == 0) {
+        stage_piece(ahead, 0);
+        next_piece<Win>(ahead, s_tpre, s_len, a);
+        if (ahead.fp < c1) stage_piece(ahead, 1);
+    } else {
+        next_piece<Win>(ahead, s_tpre, s_len, a);
+    }
+    next_piece<Win>(ahead, s_tpre, s_len, a);  // ahead = piece 2
     bq_cur = checked(bq_cur);
 
     // ---- copies of one tile into ring stage `st`; the issue point runs kDeep tiles ahead of the
     // compute point and always lies in the two fetched batches
-    TileLoc ic;
-    if (nmine > 0) ic = locate_tile<Win>(xw0, s_tpre, s_len, a);
+    TileLoc ic = {cur.b, cur.h, c0 - cur.fp, cur.ntl, cur.L};
+    if (nmine > 0) advance<Win>(ic, warp, s_len, a);
     int32_t kn = 0;  // next of this warp's tiles to issue
     auto issue = [&](int st) {
         if (kn - kb >= 32) {
@@ -638,6 +695,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
     };
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) issue(k);
+
 
     uint32_t qa0[8], qa2[8];
     float o[8][4];
