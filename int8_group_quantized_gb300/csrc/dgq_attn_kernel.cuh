@@ -59,18 +59,18 @@
 //    exceeds the reference by 8: a vote per tile in place of six shuffles.  The sum of the rounded weights, against
 //    which INT8's offset of 1152 is taken off, is one more product with ones.  Measured, us in a graph over
 //    inputs larger than L2: 131072 tokens (269 MB) 51.0 INT8, 51.3 E4M3; 32 of 2048 (135 MB) 31.6, 31.7;
-//    56.0, 62.8, 34.4 and 38.9 with S^T as the other formats.  Of that the scales behind the ring in place of
+//    56.0, 62.8, 34.4 and 38.9 with S^T as the other formats (with today's start 50.6 and 30.3).  Of that the scales behind the ring in place of
 //    beside each stage (rows then keep to 128-byte lines of shared memory) made 4 us, E4M3 pairs converted
 //    without the header function's packing 5 (bit operations in place of half the conversions: 59.2).  Four
 //    blocks per SM at depth 2, and two at depth 5, were slower (51.7 to 60.9); refilling a stage before its
-//    arithmetic changed nothing.  What is left above the floor (39.5, 19.9): the first tile lands 5 to 8 us
-//    after the start, blocks end between 21 and 28 us (32 of 2048), the merge takes 3.
+//    arithmetic changed nothing.  What is left above the floor (39.5, 19.9): the first tile lands 4 to 7 us
+//    after the start, blocks end over 7 us (the same SMs first in every run), the merge takes 3.
 //  * With a window (Win), a pair's tiles are those of the first tokens that stay visible and those of the
 //    window: tile j of the list is tile j of the request up to the last sink tile, then `skip` further.
 //    (Calls of these instances whose pairs are all short are sliced at pairs and need no merge: dgq_attn.cu.)
 //    Tiles without a visible token are not in the list, so what lies there is never read, and every tile
 //    that is in it moves the running maximum off -inf.  64 requests of 128 to 32768, window 4096, bf16 (592 MB
-//    seen): 96.8 us, 90% of the copy rate; 32 of 32768, window 8192, INT8 (546 MB): 93.5 us, 86%.
+//    seen): 94.9 us, 92% of the copy rate; 32 of 32768, window 8192, INT8 (546 MB): 91.1 us, 88%.
 #pragma once
 
 #include "dgq_device.cuh"
