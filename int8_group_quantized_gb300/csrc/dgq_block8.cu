@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(kB8Threads, 12) load_block8_kernel(const Load8
         }
         const int2 rows = load8_rows(a, lo, false);
         const int32_t t0 = (tile - s_pre[lo]) * kB8Rows, n = min(kB8Rows, rows.y - t0);
+        if ((uint32_t)t0 >= (uint32_t)rows.y) continue;  // (lengths so far off that their tiles pass 32 bits)
         int32_t blk = __ldg(a.bt + (int64_t)lo * a.max_blocks + (t0 >> shift));
         if ((uint32_t)blk >= (uint32_t)a.num_blocks) {  // not a block: flagged, and block 0 read instead
             record_error(a.hdr, kErrBadBlock);

@@ -779,11 +779,9 @@ dgq_status dgq_write_slots(const void *k_bf16, const void *v_bf16, int64_t k_tok
                                       slots_dev, k_pages_bf16, v_pages_bf16, num_blocks, block_size, workspace,
                                       workspace_bytes);
     if (st != DGQ_OK || num_tokens == 0) return st;
-    int nsm = 0;
-    if (device_sm_count(&nsm) != 0) return DGQ_ERR_CUDA;
     const cudaError_t e = dgq::launch_write_slots(k_bf16, v_bf16, k_token_stride, v_token_stride, num_tokens,
                                                   num_kv_heads, block_size, slots_dev, k_pages_bf16, v_pages_bf16,
-                                                  num_blocks, workspace, nsm, static_cast<cudaStream_t>(cuda_stream));
+                                                  num_blocks, workspace, static_cast<cudaStream_t>(cuda_stream));
     return e == cudaSuccess ? DGQ_OK : DGQ_ERR_CUDA;
 }
 

@@ -120,7 +120,7 @@ struct ExtendArgs {
 cudaError_t launch_extend_tables(const ExtendArgs &a, void *ws, int nsm, cudaStream_t stream);
 cudaError_t launch_write_slots(const void *k, const void *v, int64_t k_stride, int64_t v_stride, int32_t T, int32_t Hkv,
                                int32_t bs, const int32_t *slots, void *k_pages, void *v_pages, int32_t num_blocks,
-                               void *ws, int nsm, cudaStream_t stream);
+                               void *ws, cudaStream_t stream);
 
 // 8-bit cache with a scale per block and head: rows stored by slot, and read back in bf16.
 cudaError_t launch_store_block8(bool e4m3, const void *k, const void *v, int64_t k_stride, int64_t v_stride, int32_t T,

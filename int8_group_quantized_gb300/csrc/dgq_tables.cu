@@ -235,9 +235,8 @@ __global__ void __launch_bounds__(kWriteThreads) write_slots_kernel(const WriteA
 
 cudaError_t launch_write_slots(const void *k, const void *v, int64_t k_stride, int64_t v_stride, int32_t T, int32_t Hkv,
                                int32_t bs, const int32_t *slots, void *k_pages, void *v_pages, int32_t num_blocks,
-                               void *ws, int nsm, cudaStream_t stream)
+                               void *ws, cudaStream_t stream)
 {
-    (void)nsm;
     WriteArgs a;
     a.k = static_cast<const uint4 *>(k);
     a.v = static_cast<const uint4 *>(v);

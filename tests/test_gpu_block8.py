@@ -473,3 +473,18 @@ def test_threads_on_streams_of_their_own():
     assert not errors
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_load_stays_inside_its_buffers_when_lengths_overlap():
+    """Cumulative lengths that go down are flagged; what overlaps holds values of either request."""
+    import int8_group_quantized_gb300 as dgq
+    c, table = filled("int8", [40] * 6, 1, 16, 60)
+    out = [torch.full((44, 1, 128), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    dgq.dgq_load_block8("int8", *c.d_codes, *c.d_scales, i32(table), i32([2, 42, 2, 42, 2, 42, 2]), *out, c.ws)
+    assert dgq.dgq_workspace_error(c.ws) == 6
+    for which, o in enumerate(out):
+        o = o.cpu()
+        assert (o[:2] == 9).all() and (o[42:] == 9).all()
+        rows_of = torch.stack([torch.from_numpy(values(c, table, b, 40, which)[0]).float().to(torch.bfloat16) for b in (0, 2, 4)])
+        same = (rows_of == o[2:42]).view(3, 40, 16, 8).all(dim=-1)           # (written 16 bytes at a time)
+        assert same.any(dim=0).all()
