@@ -22,8 +22,8 @@
 // four blocks of 16 tokens, or share one of 64.  Runs are found on the fly: a block of threads looks at a
 // window of slots, from one token (decode steps: more blocks of threads than SMs) to 128.
 // Load: a warp for 16 tokens of one head of K or V, 2 KB of codes.
-// Measured, us in a graph: four chunks of 2048 tokens into blocks of 64, 8 heads (50 MB): 15.0 (floor 7.4;
-// blocks of 16: 12.7), 16.3 with K and V in one item at four blocks of threads per SM; it is two waves of
+// Measured, us in a graph: four chunks of 2048 tokens into blocks of 64, 8 heads (50 MB): E4M3 14.6, INT8
+// 13.8 (floor 7.4; blocks of 16: 12.6), 16.3 with K and V in one item at four blocks of threads per SM; it is two waves of
 // three dependent loads (slots, scale and rows, codes).  53000 tokens loaded (255 MB, two thirds of it
 // written): 44.9, 5.7 TB/s; 49.4 from a grid of eight blocks of threads per SM that walk the list.
 #include "dgq_device.cuh"
@@ -31,7 +31,7 @@
 #include "dgq_launch.h"
 
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 namespace dgq {
@@ -63,6 +63,30 @@ __device__ __forceinline__ float b8_scale(float amax)
     return __uint_as_float((__float_as_uint(__fdiv_rn(amax, b8_top<E4>())) + 0xFFFFu) & 0xFFFF0000u);
 }
 
+// Four E4M3 codes, and the values of four.  (The halves are named in PTX: the header's functions pack and unpack
+// them around each conversion.)
+__device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x3)
+{
+    uint32_t w;
+    asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(w)
+        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+    return w;
+}
+
+__device__ __forceinline__ float4 e4m3x4_values(uint32_t w)
+{
+    uint32_t a, b;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+    return make_float4(x.x, x.y, y.x, y.y);
+}
+
 // Four codes of the values x (inv = the rounded 1 / s, or 0 where s is 0).
 template <bool E4>
 __device__ __forceinline__ uint32_t b8_encode4(float x0, float x1, float x2, float x3, float inv)
@@ -70,9 +94,7 @@ __device__ __forceinline__ uint32_t b8_encode4(float x0, float x1, float x2, flo
     if constexpr (E4) {
         // to 16 significant bits (a carry into the exponent is right), then to E4M3
         auto snap = [&](float x) { return __uint_as_float((__float_as_uint(x * inv) + 0x80u) & ~0xFFu); };
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(snap(x0), snap(x1)), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(snap(x2), snap(x3)), __NV_SATFINITE, __NV_E4M3);
-        return lo | (hi << 16);
+        return e4m3x4(snap(x0), snap(x1), snap(x2), snap(x3));
     } else {
         // 12288 + y in fp32 is y to multiples of 2^-10; 1.5 2^23 + 128 + that is the whole number, ties to
         // even, in the low bits
@@ -89,10 +111,7 @@ template <bool E4>
 __device__ __forceinline__ float4 b8_decode4(uint32_t w)
 {
     if constexpr (E4) {
-        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
-        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-        const float2 x = __half22float2(__half2(a)), y = __half22float2(__half2(b));
-        return make_float4(x.x, x.y, y.x, y.y);
+        return e4m3x4_values(w);
     } else {
         // 2^23 + code as fp32
         auto value = [&](uint32_t sel) { return __uint_as_float(__byte_perm(w, 0x4B000000u, sel)) - 8388736.0f; };
@@ -211,10 +230,8 @@ __global__ void __launch_bounds__(kB8Threads, 7) store_block8_kernel(const Block
                 // or 2^-16 away from one at least, which fp32 tells apart
                 auto again = [&](float u) { return __fdiv_rn(u * had, s); };
                 if constexpr (E4) {
-                    c.x = __nv_cvt_float2_to_fp8x2(make_float2(again(p.x), again(p.y)), __NV_SATFINITE, __NV_E4M3) |
-                          ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(again(p.z), again(p.w)), __NV_SATFINITE, __NV_E4M3) << 16);
-                    c.y = __nv_cvt_float2_to_fp8x2(make_float2(again(q.x), again(q.y)), __NV_SATFINITE, __NV_E4M3) |
-                          ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(again(q.z), again(q.w)), __NV_SATFINITE, __NV_E4M3) << 16);
+                    c.x = e4m3x4(again(p.x), again(p.y), again(p.z), again(p.w));
+                    c.y = e4m3x4(again(q.x), again(q.y), again(q.z), again(q.w));
                 } else {
                     c.x = b8_encode4<E4>(rintf(again(p.x)), rintf(again(p.y)), rintf(again(p.z)), rintf(again(p.w)), 1.0f);
                     c.y = b8_encode4<E4>(rintf(again(q.x)), rintf(again(q.y)), rintf(again(q.z)), rintf(again(q.w)), 1.0f);

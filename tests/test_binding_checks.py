@@ -10,15 +10,17 @@ def dgq(monkeypatch):
     return dgq
 
 
-def test_native_module_is_built_and_found(dgq):
+def test_native_module_is_built_and_found(dgq, monkeypatch):
     from int8_group_quantized_gb300 import _build
     _build.build()
+    monkeypatch.setattr(dgq, "_native_module", False)       # (looked for before it was built)
     assert dgq._native() is not None
     assert dgq._native().__name__.endswith("_tensors")
 
 
-def test_entry_points_without_ctypes(dgq):
+def test_entry_points_without_ctypes(dgq, monkeypatch):
     """Same statuses; an argument that does not fit its C type is an error and not cut."""
+    monkeypatch.setattr(dgq, "_native_module", False)
     native, fake = dgq._native(), 0x10000
     rows = [fake, fake, 256, 256, 5, 2, 128, fake, fake, fake, 8, 16, fake, 256, 0]
     for change, status in (({}, None), ({4: 0}, 0), ({4: -1}, -1), ({6: 64}, -2), ({13: 255}, -3), ({0: fake + 4}, -1)):
