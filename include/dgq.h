@@ -334,7 +334,7 @@ dgq_status dgq_paged_decode_attn_bf16(const void *q_bf16, const void *k_new_bf16
 /* ---------------------------------------------------------------------------------------
  * Decode with a sliding window and sinks: the same step where the new token (position L_b) sees the last
  * `window` tokens, itself among them, and the first `sinks` ones: the cached tokens t < L_b with
- * t > L_b - window or t < sinks.  A window that reaches the start of a request changes nothing for it.
+ * t > L_b - window or t < sinks.  Where the window reaches the start of a request, all of it is seen.
  *
  * window            >= 1 (1: the new token and the sinks); sinks >= 0.  Else DGQ_ERR_INVALID_ARG.
  * Only tiles of 16 tokens with a visible one are read, from the first to the last by the block table: the
@@ -387,7 +387,9 @@ dgq_status dgq_paged_decode_attn_bf16_window(const void *q_bf16, const void *k_n
  * slots_dev         [num_tokens] int32, device; -1: the token is left out.  Any other slot outside
  *                   [0, num_blocks * block_size) is flagged in the workspace and left out.
  * workspace         >= dgq_block8_workspace_size() bytes, zero-filled before first use.
- * Blocks that a fork shares need dgq_pool_own_row first, as before any write.  No tokens: nothing is launched.
+ * Blocks that a fork shares need dgq_pool_own_row first, as before any write.  dgq_copy_pages copies the pages
+ * of the pools, and a block's scales like a page where Hkv is a multiple of 4 (its pages are multiples of 16
+ * bytes; the caller copies other ones).  No tokens: nothing is launched.
  * Supported: num_tokens * Hkv < 2^27.
  */
 #define DGQ_BLOCK8_INT8 0

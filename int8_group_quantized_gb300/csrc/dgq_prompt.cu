@@ -66,8 +66,9 @@
 //    window 256: 106.  With windows this short a unit is a chain: two or three steps of 2300 to 3300 cycles
 //    (softmax, P's products, the next scores), the last product 400, rows out 1800, the next item 700.
 //    Measured and not kept: edge steps in rolled passes over 32 columns, unseen ones left out (eight of 2048
-//    94); unseen quarters left out in place (16384 656); Q prefetched into L2 (eight of 2048 90): each
-//    change of the softmax code moves all windows by 4 to 10%.
+//    94); unseen quarters left out in place (16384 656); Q prefetched into L2 (eight of 2048 87 to 90); 32 rows
+//    of few sinks loaded in place of 128 (eight of 2048 87): neither the loads nor the softmax's
+//    instructions are what a short unit waits for.
 //  * Every wait is bounded: one that runs out records an error and its role leaves, after which the others'
 //    waits run out too.
 #include "dgq_device.cuh"

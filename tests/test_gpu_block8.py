@@ -488,3 +488,29 @@ def test_load_stays_inside_its_buffers_when_lengths_overlap():
         rows_of = torch.stack([torch.from_numpy(values(c, table, b, 40, which)[0]).float().to(torch.bfloat16) for b in (0, 2, 4)])
         same = (rows_of == o[2:42]).view(3, 40, 16, 8).all(dim=-1)           # (written 16 bytes at a time)
         assert same.any(dim=0).all()
+
+
+@FMT
+def test_a_fork_goes_on_with_its_own_page_and_scale(fmt):
+    """A request forked inside a block: the page and its scales copied, then different tokens to both sides."""
+    import int8_group_quantized_gb300 as dgq
+    hkv, bs = 4, 16
+    c = Cache(fmt, 8, hkv, bs)
+    pool, table = dgq.BlockPool(8), np.zeros((2, 3), dtype=np.int32)
+    pool.alloc_table_row(20, bs, table, 0)
+    c.store(tokens(20, hkv, 71), tokens(20, hkv, 72), slots_of(table[0], bs, 0, 20))
+    pairs = pool.fork_row(20, bs, table, 0, 1)
+    assert len(pairs) == 1
+    ws, d_pairs = workspace(), i32(pairs)
+    dgq.dgq_copy_pages(c.d_codes, d_pairs, ws)
+    dgq.dgq_copy_pages(c.d_scales, d_pairs, ws)
+    for host in (*c.codes, *c.scales):
+        host[pairs[0][1]] = host[pairs[0][0]]
+    c.verify()
+    for step in range(3):
+        x = (tokens(2, hkv, 73 + step).float() * torch.tensor([4.0 ** step, 1.0])[:, None, None]).to(torch.bfloat16)
+        c.store(x, -x, [slots_of(table[b], bs, 20 + step, 21 + step)[0] for b in (0, 1)])
+        c.verify()
+    assert dgq.dgq_workspace_error(ws) == 0
+    a, b = (c.scales[0][table[r, 1]] for r in (0, 1))
+    assert (a > b).any()                                     # one side's scale grew, the other's did not
