@@ -73,6 +73,8 @@ def build_tensors() -> None:
     if res.returncode == 0:
         os.replace(tmp, TENSORS)
     else:
+        if os.path.exists(TENSORS):  # (of an earlier source)
+            os.remove(TENSORS)
         print(f"_tensors.so is not built, its checks run in Python:\n{res.stderr[-2000:]}", file=sys.stderr)
 
 

@@ -4,6 +4,7 @@
 // call with nine of them), here 1 us for ten; ctypes takes 1.4 to 1.9 us for 18 to 24 arguments, here 0.3.
 // The smallest calls' kernels take 2 to 4 us.  __init__.py has the same checks, and ctypes, for a tree in
 // which this module is not built.
+#include <c10/util/SmallVector.h>
 #include <dlfcn.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -85,8 +86,6 @@ const at::Tensor *tensor_of(PyObject *x) { return THPVariable_Check(x) ? &THPVar
 
 bool on_device(const at::Tensor &t, long device) { return t.is_cuda() && t.get_device() == device; }
 
-PyObject *address(const at::Tensor &t) { return PyLong_FromVoidPtr(const_cast<void *>(t.const_data_ptr())); }
-
 // operands(device, workspace, (tensor, dtype, shape), ...): addresses of the tensors and of the workspace, or
 // None: one of them is not what the raw pointers would be read as.
 PyObject *operands(PyObject *, PyObject *const *args, Py_ssize_t n)
@@ -99,8 +98,7 @@ PyObject *operands(PyObject *, PyObject *const *args, Py_ssize_t n)
     if (device == -1 && PyErr_Occurred()) return nullptr;
     const at::Tensor *ws = tensor_of(args[1]);
     if (!ws || !ws->is_contiguous() || !on_device(*ws, device)) Py_RETURN_NONE;
-    PyObject *out = PyList_New(n - 1);
-    if (!out) return nullptr;
+    c10::SmallVector<const void *, 16> found;  // (the list is made when nothing can throw any more)
     for (Py_ssize_t i = 2; i < n; ++i) {
         PyObject *spec = args[i];
         bool ok = PyTuple_Check(spec) && PyTuple_GET_SIZE(spec) == 3;
@@ -111,15 +109,13 @@ PyObject *operands(PyObject *, PyObject *const *args, Py_ssize_t n)
              t->is_contiguous() && on_device(*t, device);
         for (Py_ssize_t d = 0; ok && d < t->dim(); ++d)
             ok = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, d)) == t->size(d);
-        PyObject *at = ok && !PyErr_Occurred() ? address(*t) : nullptr;
-        if (!at) {
-            Py_DECREF(out);
-            if (PyErr_Occurred()) return nullptr;
-            Py_RETURN_NONE;
-        }
-        PyList_SET_ITEM(out, i - 2, at);
+        if (PyErr_Occurred()) return nullptr;
+        if (!ok) Py_RETURN_NONE;
+        found.push_back(t->const_data_ptr());
     }
-    PyList_SET_ITEM(out, n - 2, address(*ws));
+    found.push_back(ws->const_data_ptr());
+    PyObject *out = PyList_New(n - 1);
+    for (Py_ssize_t i = 0; out && i < n - 1; ++i) PyList_SET_ITEM(out, i, PyLong_FromVoidPtr(const_cast<void *>(found[i])));
     return out;
 }
 
@@ -140,14 +136,29 @@ PyObject *token_rows(PyObject *, PyObject *const *args, Py_ssize_t n)
             t->stride(2) != 1 || (t->stride(1) != t->size(2) && t->size(1) > 1) || !on_device(*t, device))
             Py_RETURN_NONE;
     }
+    c10::SmallVector<const void *, 4> found;
+    for (Py_ssize_t i = 1; i < n; ++i) found.push_back(tensor_of(args[i])->const_data_ptr());
     PyObject *out = PyList_New(2 * (n - 1));
-    if (!out) return nullptr;
-    for (Py_ssize_t i = 1; i < n; ++i) {
-        const at::Tensor *t = tensor_of(args[i]);
-        PyList_SET_ITEM(out, 2 * (i - 1), address(*t));
-        PyList_SET_ITEM(out, 2 * (i - 1) + 1, PyLong_FromLongLong(t->stride(0)));
+    for (Py_ssize_t i = 1; out && i < n; ++i) {
+        PyList_SET_ITEM(out, 2 * (i - 1), PyLong_FromVoidPtr(const_cast<void *>(found[i - 1])));
+        PyList_SET_ITEM(out, 2 * (i - 1) + 1, PyLong_FromLongLong(tensor_of(args[i])->stride(0)));
     }
     return out;
+}
+
+// No C++ exception reaches the interpreter: torch throws for what a tensor of another kind (sparse, without
+// storage) cannot answer.
+template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
+PyObject *guarded(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    try {
+        return F(self, args, n);
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        PyErr_SetString(PyExc_RuntimeError, "an operand could not be looked at");
+    }
+    return nullptr;
 }
 
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(call_##name)), METH_FASTCALL, nullptr}
@@ -158,8 +169,8 @@ PyMethodDef methods[] = {
     ENTRY(dgq_load_block8),
     ENTRY(dgq_paged_decode_attn_block8),
     {"load", load, METH_O, nullptr},
-    {"operands", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(operands)), METH_FASTCALL, nullptr},
-    {"token_rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(token_rows)), METH_FASTCALL, nullptr},
+    {"operands", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(guarded<operands>)), METH_FASTCALL, nullptr},
+    {"token_rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(guarded<token_rows>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -46,6 +46,25 @@ def test_host_tensors_are_refused_by_both(dgq, monkeypatch):
             dgq._token_rows("x", torch.zeros(2, 2, 128, dtype=torch.bfloat16))
 
 
+def test_tensors_of_other_kinds_are_errors_and_not_the_end_of_the_process(dgq, monkeypatch):
+    ws = torch.zeros(256, dtype=torch.uint8)
+    sparse = torch.eye(3).to_sparse()
+    others = [(ws, (sparse, torch.float32, (3, 3))), (sparse, (ws, torch.uint8, (256,))),
+              (ws, (torch.empty(3, device="meta"), torch.float32, (3,))), (ws, (None, torch.float32, (3,))),
+              (ws, ("x", torch.float32, (3,))), (None, (ws, torch.uint8, (256,)))]
+    rows = [torch.eye(3).to_sparse(), torch.empty(2, 2, 128, dtype=torch.bfloat16, device="meta"),
+            torch.zeros(2, 128, dtype=torch.bfloat16)]
+    monkeypatch.setattr(dgq, "_native_module", False)
+    for native in (dgq._native(), None):
+        monkeypatch.setattr(dgq, "_native", lambda: native)
+        for w, spec in others:
+            with pytest.raises((RuntimeError, AttributeError)):
+                dgq._operands("x", w, spec)
+        for x in rows:
+            with pytest.raises((RuntimeError, AttributeError, ValueError)):
+                dgq._token_rows("x", x)
+
+
 @pytest.mark.gpu
 def test_both_give_the_same_answers(dgq, monkeypatch):
     d = "cuda"
