@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import shlex
 import shutil
 import subprocess
 import sys
@@ -56,37 +57,47 @@ def stale() -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
-def build_tensors() -> None:
-    """Compiles _tensors.so against this machine's torch and Python.  The binding has the same checks in
-    Python, so a machine without the headers is told and goes without."""
+def build_tensors(force: bool = False) -> None:
+    """Compiles _tensors.so against this machine's torch and Python.  The binding has the same checks in Python,
+    and a caller of the C ABI needs neither: a machine without torch, its headers or a C++ compiler (CXX, or g++)
+    is told and goes without.  A source that did not compile is not tried again before it changes."""
     import sysconfig
-    import torch
-    src = os.path.join(CSRC, "dgq_tensors.cpp")
-    root = os.path.dirname(torch.__file__)
-    inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
-    tmp = TENSORS + f".{os.getpid()}.tmp"
-    res = subprocess.run(
-        ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-         "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-         "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, src, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-ldl",
-         f"-Wl,-rpath,{lib}"], capture_output=True, text=True)
-    if res.returncode == 0:
-        os.replace(tmp, TENSORS)
-    else:
-        if os.path.exists(TENSORS):  # (of an earlier source)
-            os.remove(TENSORS)
-        print(f"_tensors.so is not built, its checks run in Python:\n{res.stderr[-2000:]}", file=sys.stderr)
+    made_of = [os.path.join(CSRC, "dgq_tensors.cpp"), os.path.join(INCLUDE, "dgq.h")]
+    src, failed = made_of[0], os.path.join(OUT_DIR, os.path.basename(TENSORS) + ".failed")
+    newest = max(os.path.getmtime(f) for f in made_of)
+    if not force and any(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (TENSORS, failed)):
+        return
+    if os.path.exists(TENSORS):  # (of an earlier source)
+        os.remove(TENSORS)
+    try:
+        import torch
+        root = os.path.dirname(torch.__file__)
+        inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+        tmp = TENSORS + f".{os.getpid()}.tmp"
+        res = subprocess.run(
+            [*shlex.split(os.environ.get("CXX") or "g++"), "-std=c++17", "-O2", "-fPIC", "-shared",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+             "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, src, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch",
+             "-ltorch_cpu", "-lc10", "-ldl", f"-Wl,-rpath,{lib}"], capture_output=True, text=True)
+        if res.returncode == 0:
+            os.replace(tmp, TENSORS)
+            return
+        why = res.stderr[-2000:]
+        os.makedirs(OUT_DIR, exist_ok=True)
+        with open(failed, "w") as f:
+            f.write(why)
+    except (ImportError, OSError) as e:  # no torch, no compiler
+        why = str(e)
+    print(f"_tensors.so is not built, its checks run in Python:\n{why}", file=sys.stderr)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    made_of = [os.path.join(CSRC, "dgq_tensors.cpp"), os.path.join(INCLUDE, "dgq.h")]
-    if force or not os.path.exists(TENSORS) or any(os.path.getmtime(f) > os.path.getmtime(TENSORS) for f in made_of):
-        with cf.ThreadPoolExecutor(max_workers=1) as ex:
-            job = ex.submit(build_tensors)
-            lib = build_lib(force, verbose)
-            job.result()
-        return lib
-    return build_lib(force, verbose)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        job = ex.submit(build_tensors, force)
+        lib = build_lib(force, verbose)
+        job.result()
+    return lib
 
 
 def build_lib(force: bool = False, verbose: bool = False) -> str:
