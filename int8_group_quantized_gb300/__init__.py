@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import importlib.util
 import os
 from operator import attrgetter
 
@@ -254,7 +255,9 @@ def _native():
     if _native_module is False:
         _torch()  # (its libraries are loaded first)
         try:
-            from . import _tensors as module
+            name, path = f"{__name__}._tensors", _build.tensors_path()  # (of this torch and Python, no other)
+            spec = importlib.util.spec_from_file_location(name, path)
+            module = importlib.util.module_from_spec(spec)
             lib()
             module.load(_build.LIB)
         except ImportError:

@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdgq.so")
-TENSORS = os.path.join(PKG, "_tensors.so")  # the binding's checks on tensors
+TENSORS_DIR = PKG  # of the binding's checks on tensors
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -57,31 +57,41 @@ def stale() -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+def tensors_path() -> str:
+    """The native module of the running torch and Python: it reads tensors where this torch's headers say that their
+    fields are, so what was built for another one is another file and never opened.  (ImportError without torch.)"""
+    import sysconfig
+    import torch
+    key = f"{torch.__version__}-{(torch.version.git_version or '')[:12]}-{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(TENSORS_DIR, f"_tensors-{key}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_tensors(force: bool = False) -> None:
-    """Compiles _tensors.so against this machine's torch and Python.  The binding has the same checks in Python,
-    and a caller of the C ABI needs neither: a machine without torch, its headers or a C++ compiler (CXX, or g++)
-    is told and goes without.  A source that did not compile is not tried again before it changes."""
+    """Compiles the binding's native checks on tensors (tensors_path).  The binding has the same checks in Python, and a
+    caller of the C ABI needs neither: a machine without torch, its headers or a C++ compiler (CXX, or g++) is
+    told and goes without.  A source that did not compile is not tried again before it changes."""
     import sysconfig
     made_of = [os.path.join(CSRC, "dgq_tensors.cpp"), os.path.join(INCLUDE, "dgq.h")]
-    src, failed = made_of[0], os.path.join(OUT_DIR, os.path.basename(TENSORS) + ".failed")
-    newest = max(os.path.getmtime(f) for f in made_of)
-    if not force and any(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (TENSORS, failed)):
-        return
-    if os.path.exists(TENSORS):  # (of an earlier source)
-        os.remove(TENSORS)
     try:
         import torch
+        path = tensors_path()
+        failed = os.path.join(OUT_DIR, os.path.basename(path) + ".failed")
+        newest = max(os.path.getmtime(f) for f in made_of)
+        if not force and any(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (path, failed)):
+            return
+        if os.path.exists(path):  # (of an earlier source)
+            os.remove(path)
         root = os.path.dirname(torch.__file__)
         inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
-        tmp = TENSORS + f".{os.getpid()}.tmp"
+        tmp = path + f".{os.getpid()}.tmp"
         res = subprocess.run(
             [*shlex.split(os.environ.get("CXX") or "g++"), "-std=c++17", "-O2", "-fPIC", "-shared",
              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
              "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-             "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, src, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch",
+             "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, made_of[0], "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch",
              "-ltorch_cpu", "-lc10", "-ldl", f"-Wl,-rpath,{lib}"], capture_output=True, text=True)
         if res.returncode == 0:
-            os.replace(tmp, TENSORS)
+            os.replace(tmp, path)
             return
         why = res.stderr[-2000:]
         os.makedirs(OUT_DIR, exist_ok=True)
@@ -89,7 +99,7 @@ def build_tensors(force: bool = False) -> None:
             f.write(why)
     except (ImportError, OSError) as e:  # no torch, no compiler
         why = str(e)
-    print(f"_tensors.so is not built, its checks run in Python:\n{why}", file=sys.stderr)
+    print(f"the native checks on tensors are not built and run in Python:\n{why}", file=sys.stderr)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
