@@ -111,9 +111,9 @@ PyObject *operands(PyObject *, PyObject *const *args, Py_ssize_t n)
             ok = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, d)) == t->size(d);
         if (PyErr_Occurred()) return nullptr;
         if (!ok) Py_RETURN_NONE;
-        found.push_back(t->const_data_ptr());
+        found.push_back(t->mutable_data_ptr());  // (written by some calls: a lazy clone gets its own storage first)
     }
-    found.push_back(ws->const_data_ptr());
+    found.push_back(ws->mutable_data_ptr());
     PyObject *out = PyList_New(n - 1);
     for (Py_ssize_t i = 0; out && i < n - 1; ++i) PyList_SET_ITEM(out, i, PyLong_FromVoidPtr(const_cast<void *>(found[i])));
     return out;
