@@ -377,8 +377,10 @@ dgq_status dgq_paged_decode_attn_bf16_window(const void *q_bf16, const void *k_n
  * of a run's first one hold its earlier tokens.  With them, s becomes the larger of the scale that is there
  * and that of the new values, and where it grows the codes in front are made anew from the values that
  * they stand for, once rounded.  A run that starts at place 0 starts the block anew, whatever was there.
- * Places behind the run are not written.  A slot that is named twice, or a block whose places come in
- * several runs of one call, ends up with one run's scale and codes of either.
+ * Places behind the run are not written.  A block belongs to one run of a call: a run whose block one of the 64
+ * tokens in front of it names too (a slot named twice; a token of a step dropped, slots 5, -1, 6; requests
+ * interleaved) is flagged in the workspace and left out.  Further apart it is not seen, and the block ends up
+ * with one run's scale and codes of either.
  *
  * format            DGQ_BLOCK8_INT8 or DGQ_BLOCK8_E4M3.
  * k_bf16, v_bf16    rows [num_tokens][Hkv][128] bf16, device, tokens k_token_stride / v_token_stride
@@ -715,7 +717,9 @@ dgq_status dgq_paged_decode_attn_format(int32_t format, const void *q_bf16, cons
 dgq_status dgq_workspace_init(void *workspace, size_t workspace_bytes, void *cuda_stream);
 
 /* Synchronise the stream and read the device-side error word of a workspace into
- * *device_error (0 = none; otherwise an internal code naming the wait that timed out).
+ * *device_error (0 = none; otherwise the first of: 1 to 3, a wait that timed out; 4, no block for a token;
+ * 5, a block id or slot outside the pool; 6, a length outside the call's sizes; 7, a block in several runs of a
+ * dgq_store_block8 call).
  * Returns DGQ_ERR_DEVICE when the word is non-zero.  The workspace must be re-initialised
  * after a device-side error. */
 dgq_status dgq_workspace_error(const void *workspace, void *cuda_stream, int32_t *device_error);

@@ -38,6 +38,7 @@ namespace dgq {
 
 constexpr int kB8Threads = 128, kB8Warps = kB8Threads / 32;
 constexpr int kB8Window = 128;         // slots that a block of threads looks at, at most
+constexpr int kB8Back = 64;            // slots in front of a run among which its block is looked for
 constexpr int kB8Rows = 16;            // rows of a warp
 constexpr int kB8Vecs = kB8Rows / 2;   // a lane's 16-byte vectors of one tensor: two rows per instruction
 constexpr float kB8Least = 0x1p-80f;   // a block below this is stored as zeros
@@ -181,6 +182,7 @@ __global__ void __launch_bounds__(kB8Threads, 7) store_block8_kernel(const Block
     for (int32_t base = y0; base < items; base += step, flip ^= 1) {  // (the same turns for all warps: barriers inside)
         const int32_t item = base + group;
         const bool live = item < items;
+        int32_t f0 = -1, f1 = -1;
         int32_t t0 = 0, h = 0, blk = 0, r0 = 0, n = 0;
         bool is_v = false;
         if (live) {
@@ -197,6 +199,10 @@ __global__ void __launch_bounds__(kB8Threads, 7) store_block8_kernel(const Block
             const bool a1 = lane + 32 < most && __ldg(a.slots + t0 + lane + 32) == slot + lane + 32;
             const uint32_t m0 = __ballot_sync(0xffffffffu, a0), m1 = __ballot_sync(0xffffffffu, a1);
             n = m0 == 0xffffffffu ? 32 + (m1 == 0xffffffffu ? 32 : __ffs(~m1) - 1) : __ffs(~m0) - 1;
+            // slots in front of it (looked at when the rows are on their way)
+            static_assert(kB8Back == 2 * 32, "two slots a lane");
+            if (lane < t0) f0 = __ldg(a.slots + t0 - 1 - lane);
+            if (lane + 32 < t0) f1 = __ldg(a.slots + t0 - 33 - lane);
         }
         // this lane: rows 2i + lane / 16 of the warp's 16, 16-byte vector lane % 16
         const int32_t row0 = part * kB8Rows + (lane >> 4), vec = lane & 15;
@@ -217,6 +223,11 @@ __global__ void __launch_bounds__(kB8Threads, 7) store_block8_kernel(const Block
             for (int w = group * per; w < (group + 1) * per; ++w) amax = fmaxf(amax, s_max[flip][w]);
         }
         if (!live) continue;
+        // a token in front that names the block, too: the block has another owner, the run is left out
+        if (__any_sync(0xffffffffu, f0 >> shift == blk || f1 >> shift == blk)) {
+            if (lane == 0) record_error(a.hdr, kErrSplitBlock);
+            continue;
+        }
         const float s = fmaxf(had, b8_scale<E4>(amax));
         const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
         uint2 *pool = reinterpret_cast<uint2 *>(is_v ? a.vpool : a.kpool) + (((int64_t)blk * a.Hkv + h) * bs + row0) * 16 + vec;

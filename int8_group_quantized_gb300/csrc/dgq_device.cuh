@@ -50,6 +50,7 @@ enum : uint32_t {
     kErrNoBlock = 4,        // append: a pair's next slot has no block-table column
     kErrBadBlock = 5,       // a block-table entry outside [0, num_blocks): its window/tile skipped
     kErrBadLength = 6,      // a request length outside what the call's sizes allow: clamped or skipped
+    kErrSplitBlock = 7,     // 8-bit store: a block's tokens in several runs of one call: the later ones left out
 };
 
 // WsHeader::path values
