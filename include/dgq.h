@@ -385,7 +385,9 @@ dgq_status dgq_paged_decode_attn_bf16_window(const void *q_bf16, const void *k_n
  * format            DGQ_BLOCK8_INT8 or DGQ_BLOCK8_E4M3.
  * k_bf16, v_bf16    rows [num_tokens][Hkv][128] bf16, device, tokens k_token_stride / v_token_stride
  *                   elements apart (a multiple of 8, at least Hkv * 128: slices of a fused projection);
- *                   finite, |x| < 2^100.
+ *                   finite, |x| < 2^100.  Any other value is flagged in the workspace, and one that is infinite
+ *                   or NaN makes the scale of its block and head NaN, and with it what is read from them, until
+ *                   a run starts the block anew.
  * slots_dev         [num_tokens] int32, device; -1: the token is left out.  Any other slot outside
  *                   [0, num_blocks * block_size) is flagged in the workspace and left out.
  * workspace         >= dgq_block8_workspace_size() bytes, zero-filled before first use.
@@ -418,7 +420,7 @@ dgq_status dgq_load_block8(int32_t format, const uint8_t *k_pool, const uint8_t 
                            int32_t batch, int32_t num_kv_heads, int32_t head_dim, void *k_bf16, void *v_bf16,
                            int32_t total_kv, void *workspace, size_t workspace_bytes, void *cuda_stream);
 
-/* dgq_paged_decode_attn over an 8-bit block cache (scales 0 or 2^-100 .. 2^100), of all cached tokens
+/* dgq_paged_decode_attn over an 8-bit block cache (scales 0 or 2^-100 .. 2^100, or NaN), of all cached tokens
  * (window == 0 and sinks == 0) or of a window and sinks as above.  Same kernel, work split, merge order,
  * limits and workspace (dgq_attn_workspace_size). */
 dgq_status dgq_paged_decode_attn_block8(int32_t format, const void *q_bf16, const void *k_new_bf16,
@@ -719,7 +721,7 @@ dgq_status dgq_workspace_init(void *workspace, size_t workspace_bytes, void *cud
 /* Synchronise the stream and read the device-side error word of a workspace into
  * *device_error (0 = none; otherwise the first of: 1 to 3, a wait that timed out; 4, no block for a token;
  * 5, a block id or slot outside the pool; 6, a length outside the call's sizes; 7, a block in several runs of a
- * dgq_store_block8 call).
+ * dgq_store_block8 call; 8, a value that dgq_store_block8 cannot hold).
  * Returns DGQ_ERR_DEVICE when the word is non-zero.  The workspace must be re-initialised
  * after a device-side error. */
 dgq_status dgq_workspace_error(const void *workspace, void *cuda_stream, int32_t *device_error);

@@ -274,6 +274,14 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 
+// The larger one, or NaN where one is.
+__device__ __forceinline__ float max_nan(float x, float y)
+{
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
+
 // 2^x on the MUFU unit (flush-to-zero); arguments here are <= 8 or -inf.
 __device__ __forceinline__ float ex2(float x)
 {
@@ -794,7 +802,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
                         mma16816(jj & 1 ? s1 : s0, codes2<Fmt, false>(wa, 0u, 0u), codes2<Fmt, false>(wb, 0u, 0u),
                                  codes2<Fmt, true>(wa, 0u, 0u), codes2<Fmt, true>(wb, 0u, 0u), qa0[jj], qa2[jj]);
                     }
-                    const float ve = lg2(fmaxf(__uint_as_float(sc.y), 0x1p-100f));  // (a block of zeros has scale 0)
+                    const float ve = lg2(max_nan(__uint_as_float(sc.y), 0x1p-100f));  // (a block of zeros has scale 0)
                     const float ks = __uint_as_float(sc.x) * kLog2eOverSqrtD;
                     float z[4];  // z + log2(scale of V) - m of (token, head): (0, 0) (0, 1) (1, 0) (1, 1)
 #pragma unroll
@@ -1106,7 +1114,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<Fmt>()) attn_kernel(
                     const float to = mb[g] + (lb[g] > 0.0f ? rintf(lg2(lb[g])) : 0.0f);
                     unit[g] = ex2(mb[g] - to);
                     if (r == 0 && g0 + g < G) {
-                        cw[(g0 + g) * kPartStride + 0] = fresh ? -INFINITY : to;
+                        cw[(g0 + g) * kPartStride + 0] = fresh ? -INFINITY : (isnan(lb[g]) ? 0.0f : to);  // (NaN is handed on)
                         cw[(g0 + g) * kPartStride + 1] = lb[g] * unit[g];
                     }
                 }

@@ -42,6 +42,7 @@ constexpr int kB8Back = 64;            // slots in front of a run among which it
 constexpr int kB8Rows = 16;            // rows of a warp
 constexpr int kB8Vecs = kB8Rows / 2;   // a lane's 16-byte vectors of one tensor: two rows per instruction
 constexpr float kB8Least = 0x1p-80f;   // a block below this is stored as zeros
+constexpr uint32_t kB8Most = 227u << 23;  // values of 2^100 and more (these bits of an fp32 number) are flagged
 
 struct Block8Args {
     const uint4 *k, *v;          // rows [T][Hkv][16 vectors], tokens k_stride / v_stride vectors apart
@@ -56,11 +57,12 @@ struct Block8Args {
 template <bool E4>
 __device__ __forceinline__ float b8_top() { return E4 ? 448.0f : 127.0f; }
 
-// The smallest bf16 number not below amax / top.
+// The smallest bf16 number not below amax / top; NaN of what is infinite or NaN.
 template <bool E4>
 __device__ __forceinline__ float b8_scale(float amax)
 {
     if (amax < kB8Least) return 0.0f;
+    if (!(amax < INFINITY)) return __uint_as_float(0x7FC00000u);
     return __uint_as_float((__float_as_uint(__fdiv_rn(amax, b8_top<E4>())) + 0xFFFFu) & 0xFFFF0000u);
 }
 
@@ -122,11 +124,12 @@ __device__ __forceinline__ float4 b8_decode4(uint32_t w)
 
 __device__ __forceinline__ __nv_bfloat162 b8_absmax(__nv_bfloat162 m, uint32_t w)
 {
-    return __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w)));
+    return __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w)));
 }
 
-// Largest |x| over the warp of a lane's vectors (rows that are not the run's hold zeros).
-__device__ __forceinline__ float b8_amax(const uint4 *x)
+// Largest |x| over the warp of a lane's vectors (rows that are not the run's hold zeros), as the bits of
+// an fp32 number.
+__device__ __forceinline__ uint32_t b8_amax(const uint4 *x)
 {
     __nv_bfloat162 m = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
@@ -136,10 +139,8 @@ __device__ __forceinline__ float b8_amax(const uint4 *x)
         m = b8_absmax(m, x[i].z);
         m = b8_absmax(m, x[i].w);
     }
-    float f = fmaxf(__low2float(m), __high2float(m));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, o));
-    return f;
+    // (as bits: in the order of the numbers they stand for, a NaN above all)
+    return __reduce_max_sync(0xffffffffu, max(__float_as_uint(__low2float(m)), __float_as_uint(__high2float(m))));
 }
 
 template <bool E4>
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kB8Threads, 7) store_block8_kernel(const Block
 {
     __shared__ int32_t s_start[kB8Window];            // tokens of the window that start a run
     __shared__ int32_t s_count[kB8Warps];
-    __shared__ float s_max[2][kB8Warps];
+    __shared__ uint32_t s_max[2][kB8Warps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t bs = a.bs, shift = __ffs(bs) - 1;
     const int32_t w0 = blockIdx.x * a.window;
@@ -216,11 +217,11 @@ __global__ void __launch_bounds__(kB8Threads, 7) store_block8_kernel(const Block
             x[i] = r >= 0 && r < n ? __ldcs(from + 2 * i * stride) : make_uint4(0u, 0u, 0u, 0u);
         }
         const float had = live && r0 > 0 ? __ldcg(scale) : 0.0f;  // tokens are there already
-        float amax = b8_amax(x);
+        uint32_t amax = b8_amax(x);
         if (per > 1) {  // the warps of the item
             if (lane == 0) s_max[flip][warp] = amax;
             __syncthreads();  // (also: every warp has read the scale)
-            for (int w = group * per; w < (group + 1) * per; ++w) amax = fmaxf(amax, s_max[flip][w]);
+            for (int w = group * per; w < (group + 1) * per; ++w) amax = max(amax, s_max[flip][w]);
         }
         if (!live) continue;
         // a token in front that names the block, too: the block has another owner, the run is left out
@@ -228,7 +229,9 @@ __global__ void __launch_bounds__(kB8Threads, 7) store_block8_kernel(const Block
             if (lane == 0) record_error(a.hdr, kErrSplitBlock);
             continue;
         }
-        const float s = fmaxf(had, b8_scale<E4>(amax));
+        if (amax >= kB8Most && lane == 0) record_error(a.hdr, kErrBadValue);
+        // (the larger one by their bits, as above: a NaN stays until the block is started anew)
+        const float s = __uint_as_float(max(__float_as_uint(had), __float_as_uint(b8_scale<E4>(__uint_as_float(amax)))));
         const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
         uint2 *pool = reinterpret_cast<uint2 *>(is_v ? a.vpool : a.kpool) + (((int64_t)blk * a.Hkv + h) * bs + row0) * 16 + vec;
         if (part == 0 && lane == 0 && (r0 == 0 || s != had)) *scale = s;

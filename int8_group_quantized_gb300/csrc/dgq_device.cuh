@@ -51,6 +51,7 @@ enum : uint32_t {
     kErrBadBlock = 5,       // a block-table entry outside [0, num_blocks): its window/tile skipped
     kErrBadLength = 6,      // a request length outside what the call's sizes allow: clamped or skipped
     kErrSplitBlock = 7,     // 8-bit store: a block's tokens in several runs of one call: the later ones left out
+    kErrBadValue = 8,       // 8-bit store: a value that is infinite, NaN, or 2^100 or more in size
 };
 
 // WsHeader::path values
