@@ -4,6 +4,7 @@ library is missing or older than its sources."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import os
 import shlex
 import shutil
@@ -79,8 +80,8 @@ def build_tensors(force: bool = False) -> None:
         newest = max(os.path.getmtime(f) for f in made_of)
         if not force and any(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (path, failed)):
             return
-        if os.path.exists(path):  # (of an earlier source)
-            os.remove(path)
+        with contextlib.suppress(FileNotFoundError):
+            os.remove(path)  # (of an earlier source)
         root = os.path.dirname(torch.__file__)
         inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
         tmp = path + f".{os.getpid()}.tmp"
