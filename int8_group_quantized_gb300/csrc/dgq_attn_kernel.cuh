@@ -55,7 +55,7 @@
 //    in fp32's range and no score within 2^-26 of the largest is lost, where w is flushed to 0 beside a
 //    scale 2^126 times as large.  At a piece's end O and the sum are brought to a reference of the scores alone,
 //    at which the sum is about 1, so that merges weigh by scores.  (Against w 2^-e, one exponential for four:
-//    131072 tokens E4M3 52.7 to 53.1 as called for 52.3 to 53.1, 32 of 2048 INT8 33.0 for 33.0.)
+//    131072 tokens 50.8 for 50.7 E4M3 and 50.7 for 50.5 INT8, 32 of 2048 30.4 for 30.2 and 30.3 for 30.2.)
 //    A block whose values are small has small weights, and one whose scores are small too; neither leaves
 //    the range of fp16 for the other's sake.  (fp16 may make a weight 0 that counts in the sum.)
 //    These instances have the 16 tokens as the rows of S = K Q^T (8 products a tile where S^T = Q K^T takes
@@ -63,7 +63,7 @@
 //    exceeds the reference by 8: a vote per tile in place of six shuffles.  The sum of the rounded weights, against
 //    which INT8's offset of 1152 is taken off, is one more product with ones.  Measured, us in a graph over
 //    inputs larger than L2: 131072 tokens (269 MB) 51.0 INT8, 51.3 E4M3; 32 of 2048 (135 MB) 31.6, 31.7;
-//    56.0, 62.8, 34.4 and 38.9 with S^T as the other formats (with today's start 50.6 and 30.3).  Of that the scales behind the ring in place of
+//    56.0, 62.8, 34.4 and 38.9 with S^T as the other formats (today 50.7, 50.8, 30.3, 30.4).  Of that the scales behind the ring in place of
 //    beside each stage (rows then keep to 128-byte lines of shared memory) made 4 us, E4M3 pairs converted
 //    without the header function's packing 5 (bit operations in place of half the conversions: 59.2).  Four
 //    blocks per SM at depth 2, and two at depth 5, were slower (51.7 to 60.9); refilling a stage before its

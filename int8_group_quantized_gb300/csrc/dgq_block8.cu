@@ -22,10 +22,12 @@
 // four blocks of 16 tokens, or share one of 64.  Runs are found on the fly: a block of threads looks at a
 // window of slots, from one token (decode steps: more blocks of threads than SMs) to 128.
 // Load: a warp for 16 tokens of one head of K or V, 2 KB of codes.
-// Measured, us in a graph: four chunks of 2048 tokens into blocks of 64, 8 heads (50 MB): E4M3 14.6, INT8
-// 13.8 (floor 7.4; blocks of 16: 12.6), 16.3 with K and V in one item at four blocks of threads per SM; it is two waves of
-// three dependent loads (slots, scale and rows, codes).  53000 tokens loaded (255 MB, two thirds of it
-// written): 44.9, 5.7 TB/s; 49.4 from a grid of eight blocks of threads per SM that walk the list.
+// Measured, us in a graph: four chunks of 2048 tokens into blocks of 64, 8 heads (50 MB): E4M3 15.0, INT8
+// 14.4 (floor 7.4; blocks of 16: 13.0), 16.3 with K and V in one item at four blocks of threads per SM; it is two waves of
+// three dependent loads (slots, scale and rows, codes).  Seven blocks of threads per SM spill 12 (INT8) and 20
+// bytes a thread, six spill none: 16.1 and 15.3.  The look at the 64 slots in front of a run is 0.3 to 0.5 of it.
+// 44240 tokens loaded (272 MB, two thirds of it written): 45.1, 6.0 TB/s; 49.4 from a grid of eight blocks of
+// threads per SM that walk the list.
 #include "dgq_device.cuh"
 #include "dgq.h"
 #include "dgq_launch.h"
