@@ -679,8 +679,10 @@ def _block8_id(fmt) -> int:
 
 def dgq_store_block8(fmt, k, v, slots, k_pool, v_pool, k_scales, v_scales, workspace, stream=None) -> None:
     """Rows of new tokens into an 8-bit cache with one scale per block and head.  fmt: "int8" or "e4m3";
-    k, v and slots as dgq_write_slots; pools uint8 [num_blocks, Hkv, bs, 128] and scales fp32 [num_blocks, Hkv],
-    updated in place; workspace uint8 (dgq_block8_workspace_size bytes).  All CUDA tensors."""
+    k, v and slots as dgq_write_slots, the tokens of a block one behind the other; pools uint8 [num_blocks, Hkv, bs, 128]
+    and scales fp32 [num_blocks, Hkv], updated in place; workspace uint8 (dgq_block8_workspace_size bytes), where
+    dgq_workspace_error then finds 7 for a block in several runs (the later ones left out) and 8 for values that are
+    infinite, NaN, or 2^100 and more in size.  All CUDA tensors."""
     torch = _torch()
     u8, f32 = torch.uint8, torch.float32
     T, Hkv, D = k.shape
